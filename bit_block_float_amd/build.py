@@ -12,7 +12,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libhif4.so")
-SOURCES = ["api.hip", "quant.hip", "gemm.hip", "pct.hip", "gptq.hip", "autoround.hip"]
+SOURCES = ["api.hip", "quant.hip", "gemm.hip", "pct.hip", "gptq.hip", "autoround.hip",
+           "api_fp8.hip", "fp8.hip", "gemm_fp8.hip", "api_norm.hip", "norm.hip"]
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 
 

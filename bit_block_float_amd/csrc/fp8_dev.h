@@ -1,0 +1,109 @@
+// fp8_dev.h -- device helpers of the E4M3 block format (the rule is stated in
+// hif4.h): the E8M0 scale of a block from its maximum, the encoding of 16
+// elements, and guarded 16-element loads.
+#pragma once
+
+#include "hif4_dev.h"
+
+namespace hif4 {
+
+constexpr int kFp8Block = 128;  // elements that share one scale along a row
+
+// Biased exponent (E8M0 byte) of the smallest power of two s >= 2^-127 with
+// amax <= 448 s; `bits` = |amax| as fp32 bits. 448 = 1.75 * 2^8, so the
+// exponent is that of amax minus 8, one more where the significand is above
+// 1.75. 255 (E8M0's NaN) if the block holds a NaN or an infinity.
+__device__ __forceinline__ uint32_t e8m0_of(uint32_t bits) {
+  const int e = (int)(bits >> 23) - 8 + (int)((bits & 0x7FFFFFu) > 0x600000u);
+  return bits >= 0x7F800000u ? 255u : (uint32_t)max(e, 0);
+}
+// 2^(127 - byte), the reciprocal of the scale (byte <= 247 here: normal).
+__device__ __forceinline__ float e8m0_inv(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+// The scale itself; byte 0 is 2^-127 (subnormal in fp32), 255 is NaN.
+__device__ __forceinline__ float e8m0_f32(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : byte == 0u ? 0x400000u : byte << 23);
+}
+
+// Four E4M3 codes RNE(v * inv). v * inv is exact (a power of two, and no
+// result leaves the normal fp32 range upwards), so the conversion's rounding
+// is the only one.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float inv) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
+}
+constexpr uint32_t kFp8NaN4 = 0x7F7F7F7Fu;  // four E4M3 NaNs
+
+// 8 consecutive elements of a row as fp32; elements at or past `valid` read as
+// zero. `vec`: the row is 16-byte aligned (a uniform flag), so a whole run is
+// one (bf16) or two (fp32) 16-byte loads.
+template <typename T>
+struct Run8;
+template <>
+struct Run8<uint16_t> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint16_t* p, int valid, bool vec) {
+    if (vec && valid >= 8) {
+      w = *reinterpret_cast<const uint4*>(p);
+    } else {
+      uint32_t h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = i < valid ? p[i] : 0u;
+      w = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
+                     h[6] | (h[7] << 16));
+    }
+  }
+  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t u = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+    return (i & 1) ? bf16hi_to_f32(u) : bf16lo_to_f32(u);
+  }
+};
+template <>
+struct Run8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, int valid, bool vec) {
+    if (vec && valid >= 8) {
+      a = reinterpret_cast<const float4*>(p)[0];
+      b = reinterpret_cast<const float4*>(p)[1];
+    } else {
+      float h[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = i < valid ? p[i] : 0.0f;
+      a = make_float4(h[0], h[1], h[2], h[3]);
+      b = make_float4(h[4], h[5], h[6], h[7]);
+    }
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ float get(int i) const {
+    switch (i) {
+      case 0: return a.x;
+      case 1: return a.y;
+      case 2: return a.z;
+      case 3: return a.w;
+      case 4: return b.x;
+      case 5: return b.y;
+      case 6: return b.z;
+      default: return b.w;
+    }
+  }
+};
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+}  // namespace hif4
+
+// Internal (hidden) host launchers; argument checks happen in api_fp8.hip.
+hipError_t hif4_launch_quantize_fp8(const void* x, bool bf16, int64_t rows, int64_t k, int64_t ld,
+                                    int block_rows, uint8_t* codes, uint8_t* scales, int64_t lds,
+                                    uint8_t* codes_t, uint8_t* scales_t, int64_t lds_t,
+                                    hipStream_t stream);
+hipError_t hif4_launch_dequantize_fp8(const uint8_t* codes, const void* scales, bool scales_f32,
+                                      int block_rows, int64_t lds, int64_t rows, int64_t k,
+                                      void* out, bool out_bf16, hipStream_t stream);
+size_t hif4_gemm_fp8_ws_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t hif4_launch_gemm_fp8(const uint8_t* x, const uint8_t* xs, int64_t ldxs, const uint8_t* w,
+                                const void* ws, int64_t ldws, bool ws_f32, int w_block, int64_t m,
+                                int64_t n, int64_t k, void* y, bool y_bf16, void* workspace,
+                                hipStream_t stream);

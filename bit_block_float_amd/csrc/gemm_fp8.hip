@@ -1,0 +1,462 @@
+// gemm_fp8.hip -- Y = X W^T on E4M3 codes with a scale per block of 128 along
+// K, on gfx950's scaled matrix cores.
+//
+// Y[i][j] = sum_b sx[i][b] sw[j][b] sum_{t in block b} cx[i][t] cw[j][t].
+// sx is a power of two (E8M0), and so is sw where the library quantized it.
+//
+// Which matrix instruction, by the type of Y:
+//  - bf16: v_mfma_scale_f32_32x32x64_f8f6f4 on the codes as they are, both E8M0
+//    bytes applied by the instruction. Measured on gfx950 (and the same for the
+//    unscaled fp8 forms): within each run of 8 consecutive K values a product
+//    is cut to a multiple of 2^-13 of the largest one's power of two before the
+//    8 are added; the runs and the accumulator add in full fp32. The loss is at
+//    most 7 * 2^-13 of each run's largest product, on random signs some 1e-5 of
+//    |Y|: far below the 2^-9 rounding of a bf16 result, and half the time.
+//  - fp32: the codes are widened to bf16 (v_cvt_scalef32_pk_bf16_fp8, exact,
+//    with the power-of-two scale applied; below 2^-126 bf16 is subnormal and
+//    may round) and multiplied by the bf16 forms, whose products and sums are
+//    full fp32: a float32 result is asked for where the last bits count.
+//  - up to 64 rows (bound by reading W) always the latter.
+// A weight whose scales are float32 (one per 128 x 128) keeps sx in the
+// operands and adds each block's partial sum times sw with one FMA per output.
+//
+// The MFMA's first operand is W, so a lane of the result holds one row of Y
+// (its column index) and runs of 4 consecutive columns.
+#include "fp8_dev.h"
+
+namespace hif4 {
+
+typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+typedef __attribute__((ext_vector_type(8))) __bf16 gbf16x8_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t bf16x8_words_t;
+typedef __attribute__((ext_vector_type(4))) uint32_t gu32x4_t;
+typedef __attribute__((ext_vector_type(16))) float gf32x16_t;
+typedef __attribute__((ext_vector_type(4))) float gf32x4_t;
+typedef __attribute__((address_space(3))) void glds_void_t;
+
+constexpr int kFmtE4M3 = 0;     // cbsz / blgp of the f8f6f4 forms
+constexpr int kUnitScale = 127; // E8M0 byte of 1.0
+constexpr int kRsrc3 = 0x00020000;
+
+__device__ __forceinline__ i32x8_t join(gu32x4_t a, gu32x4_t b) {
+  return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+__device__ __forceinline__ gf32x16_t mfma32(i32x8_t a, i32x8_t b, gf32x16_t c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, kFmtE4M3, kFmtE4M3, 0, sa, 0, sb);
+}
+
+// 8 codes (two words) as bf16 times the power of two `s`.
+__device__ __forceinline__ gbf16x8_t widen(uint32_t lo, uint32_t hi, float s) {
+  const bf16x8_words_t w = {
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false)),
+      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true))};
+  return __builtin_bit_cast(gbf16x8_t, w);
+}
+
+// Four consecutive columns of one row of Y.
+template <bool kBf16>
+__device__ __forceinline__ void store4(void* y, int64_t off, int col, int n, bool vec, float a,
+                                       float b, float c, float d) {
+  if constexpr (kBf16) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(y) + off;
+    if (vec && col + 4 <= n) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(f32_to_bf16(a) | (f32_to_bf16(b) << 16),
+                                                f32_to_bf16(c) | (f32_to_bf16(d) << 16));
+    } else {
+      if (col < n) p[0] = (uint16_t)f32_to_bf16(a);
+      if (col + 1 < n) p[1] = (uint16_t)f32_to_bf16(b);
+      if (col + 2 < n) p[2] = (uint16_t)f32_to_bf16(c);
+      if (col + 3 < n) p[3] = (uint16_t)f32_to_bf16(d);
+    }
+  } else {
+    float* p = reinterpret_cast<float*>(y) + off;
+    if (vec && col + 4 <= n) {
+      *reinterpret_cast<gf32x4_t*>(p) = gf32x4_t{a, b, c, d};
+    } else {
+      if (col < n) p[0] = a;
+      if (col + 1 < n) p[1] = b;
+      if (col + 2 < n) p[2] = c;
+      if (col + 3 < n) p[3] = d;
+    }
+  }
+}
+
+// Tile kernel. BM x BN of Y a workgroup, kWM x kWN waves. A stage is one block
+// of 128 along K: rows of 128 bytes = 8 chunks of 16, chunk c of row r in slot
+// c ^ ((r >> 1) & 7), so that the fragment reads of 16 consecutive rows land in
+// distinct bank groups. Stages reach LDS by direct-to-LDS buffer loads, 8 rows
+// an instruction, with the swizzle applied to the global address; rows past M
+// or N fail the buffer's range check and read as zero. The E8M0 bytes come four
+// blocks (a 32-bit word per row) at a time.
+template <int BM, int BN, int kWM, int kWN, bool kF32Scale, bool kBf16>
+__device__ __forceinline__ void gemm_fp8_tile(
+    const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
+    const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int64_t M,
+    int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n) {
+  constexpr int kWaves = kWM * kWN;
+  constexpr int kTM = BM / kWM / 32, kTN = BN / kWN / 32;  // 32 x 32 blocks of a wave
+  constexpr int kStage = (BM + BN) * 128;
+  constexpr int kScaleRing = (BM + BN) * 4;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage + 2 * kScaleRing];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / kWN, wn = wave % kWN;
+
+  // Tile order: consecutive workgroup ids go to different XCDs; each XCD gets a
+  // contiguous run of tiles, walked column by column in groups of 8 tile rows.
+  const uint32_t ntiles = tiles_m * tiles_n;
+  uint32_t t = blockIdx.x;
+  {
+    const uint32_t per_xcd = ntiles / 8;
+    if (t < per_xcd * 8) t = (t & 7) * per_xcd + (t >> 3);
+  }
+  const uint32_t group = 8, per_group = group * tiles_n;
+  const uint32_t gi = t / per_group, first = gi * group, in = t - gi * per_group;
+  const uint32_t gsize = min(tiles_m - first, group);
+  const int64_t m0 = (int64_t)(first + in % gsize) * BM, n0 = (int64_t)(in / gsize) * BN;
+
+  const int mrows = (int)min((int64_t)BM, M - m0), nrows = (int)min((int64_t)BN, N - n0);
+  const __amdgpu_buffer_rsrc_t rx =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(X + m0 * K), (short)0, mrows * K, kRsrc3);
+  const __amdgpu_buffer_rsrc_t rw =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(W + n0 * K), (short)0, nrows * K, kRsrc3);
+  const __amdgpu_buffer_rsrc_t rxs = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(XS + m0 * ldxs), (short)0, (int)(mrows * ldxs), kRsrc3);
+  const __amdgpu_buffer_rsrc_t rws = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((const uint8_t*)WS + (n0 >> w_shift) * ldws), (short)0,
+      (int)((((nrows - 1) >> w_shift) + 1) * ldws), kRsrc3);
+
+  // LDS: [stage][X rows, then W rows], then [ring slot][X words, then W words]
+  constexpr int kLoads = (BM + BN) / 8 / kWaves;   // per wave and stage
+  constexpr int kXLoads = BM / 8 / kWaves;
+  static_assert((BM + BN) % (8 * kWaves) == 0 && BM % (8 * kWaves) == 0, "whole loads a wave");
+  uint32_t voff[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int row = (i < kXLoads ? wave * kXLoads + i : wave * (kLoads - kXLoads) + i - kXLoads) * 8 +
+                    (lane >> 3);
+    voff[i] = (uint32_t)row * (uint32_t)K + (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+  }
+  auto load_stage = [&](int kb) {
+    char* base = lds + (kb & 1) * kStage;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (i < kXLoads)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rx, (glds_void_t*)(base + (wave * kXLoads + i) * 1024), 16, voff[i], kb * 128, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rw, (glds_void_t*)(base + BM * 128 + (wave * (kLoads - kXLoads) + i - kXLoads) * 1024),
+            16, voff[i], kb * 128, 0, 0);
+    }
+  };
+  // scale words of blocks 4g .. 4g + 3: 64 rows an instruction
+  auto load_scales = [&](int g) {
+    char* base = lds + 2 * kStage + (g & 1) * kScaleRing;
+    for (int r = wave; r < (kF32Scale ? BM : BM + BN) / 64; r += kWaves) {
+      if (r < BM / 64)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (glds_void_t*)(base + r * 256), 4,
+                                                 (uint32_t)(r * 64 + lane) * (uint32_t)ldxs, 4 * g,
+                                                 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rws, (glds_void_t*)(base + r * 256), 4,
+            (uint32_t)(((r - BM / 64) * 64 + lane) >> w_shift) * (uint32_t)ldws, 4 * g, 0, 0);
+    }
+  };
+
+  gf32x16_t acc[kTN][kTM];
+#pragma unroll
+  for (int i = 0; i < kTN; ++i)
+#pragma unroll
+    for (int j = 0; j < kTM; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  const int frow = lane & 31, fhalf = lane >> 5, fsw = (frow >> 1) & 7;
+  const int xrow = wm * (BM / kWM) + frow, wrow = wn * (BN / kWN) + frow;
+  uint32_t sxw[kTM], sww[kTN];
+  const float* wsf = reinterpret_cast<const float*>(WS) +
+                     (int64_t)((n0 + wn * (BN / kWN)) >> 7) * ldws;  // kF32Scale: one block row
+  const int KB = K / 128;
+  load_scales(0);
+  load_stage(0);
+  for (int kb = 0; kb < KB; ++kb) {
+    // stage kb has landed for this wave; after the barrier for all, and every
+    // wave has read the buffer that stage kb + 1 goes into
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (kb + 1 < KB) {
+      if (((kb + 1) & 3) == 0) load_scales((kb + 1) >> 2);
+      load_stage(kb + 1);
+    }
+    if ((kb & 3) == 0) {
+      const char* sb = lds + 2 * kStage + ((kb >> 2) & 1) * kScaleRing;
+#pragma unroll
+      for (int j = 0; j < kTM; ++j)
+        sxw[j] = *reinterpret_cast<const uint32_t*>(sb + (xrow + j * 32) * 4);
+      if constexpr (!kF32Scale) {
+#pragma unroll
+        for (int i = 0; i < kTN; ++i)
+          sww[i] = *reinterpret_cast<const uint32_t*>(sb + (BM + wrow + i * 32) * 4);
+      }
+    }
+    const int sh = 8 * (kb & 3);
+    const char* xs = lds + (kb & 1) * kStage + xrow * 128;
+    const char* ws = lds + (kb & 1) * kStage + (BM + wrow) * 128;
+    float wscale = 0.0f;
+    if constexpr (kF32Scale) wscale = wsf[kb];
+    auto chunk = [&](const char* row, int c) {
+      return *reinterpret_cast<const gu32x4_t*>(row + ((c ^ fsw) * 16));
+    };
+    if constexpr (kBf16) {
+      // half s of the block: lanes 0..31 chunks 4s, 4s + 1, lanes 32..63 the next two
+      auto frag = [&](const char* row, int s) {
+        return join(chunk(row, 4 * s + 2 * fhalf), chunk(row, 4 * s + 2 * fhalf + 1));
+      };
+      if constexpr (!kF32Scale) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          i32x8_t fx[kTM];
+#pragma unroll
+          for (int j = 0; j < kTM; ++j) fx[j] = frag(xs + j * 4096, s);
+#pragma unroll
+          for (int i = 0; i < kTN; ++i) {
+            const i32x8_t fw = frag(ws + i * 4096, s);
+#pragma unroll
+            for (int j = 0; j < kTM; ++j)
+              acc[i][j] = mfma32(fw, fx[j], acc[i][j], (int)(sww[i] >> sh), (int)(sxw[j] >> sh));
+          }
+        }
+      } else {
+        i32x8_t fx[2][kTM];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int j = 0; j < kTM; ++j) fx[s][j] = frag(xs + j * 4096, s);
+#pragma unroll
+        for (int i = 0; i < kTN; ++i) {
+          const i32x8_t w0 = frag(ws + i * 4096, 0), w1 = frag(ws + i * 4096, 1);
+#pragma unroll
+          for (int j = 0; j < kTM; ++j) {
+            gf32x16_t p = {0.0f};
+            p = mfma32(w0, fx[0][j], p, kUnitScale, (int)(sxw[j] >> sh));
+            p = mfma32(w1, fx[1][j], p, kUnitScale, (int)(sxw[j] >> sh));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(p[r], wscale, acc[i][j][r]);
+          }
+        }
+      }
+    } else {
+      // chunk pair q: lanes 0..31 chunk 2q, lanes 32..63 chunk 2q + 1, 16 codes
+      // each = the operands of two MFMAs
+      float sxf[kTM], swf[kTN];
+#pragma unroll
+      for (int j = 0; j < kTM; ++j) sxf[j] = e8m0_f32((sxw[j] >> sh) & 255u);
+#pragma unroll
+      for (int i = 0; i < kTN; ++i) swf[i] = kF32Scale ? 1.0f : e8m0_f32((sww[i] >> sh) & 255u);
+      if constexpr (!kF32Scale) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          gbf16x8_t fx[2][kTM];
+#pragma unroll
+          for (int j = 0; j < kTM; ++j) {
+            const gu32x4_t v = chunk(xs + j * 4096, 2 * q + fhalf);
+            fx[0][j] = widen(v.x, v.y, sxf[j]);
+            fx[1][j] = widen(v.z, v.w, sxf[j]);
+          }
+#pragma unroll
+          for (int i = 0; i < kTN; ++i) {
+            const gu32x4_t v = chunk(ws + i * 4096, 2 * q + fhalf);
+            const gbf16x8_t w0 = widen(v.x, v.y, swf[i]), w1 = widen(v.z, v.w, swf[i]);
+#pragma unroll
+            for (int j = 0; j < kTM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w0, fx[0][j], acc[i][j], 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < kTM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w1, fx[1][j], acc[i][j], 0, 0, 0);
+          }
+        }
+      } else {
+        // one row block at a time: the partial sums of all would not fit beside
+        // the accumulators
+#pragma unroll
+        for (int j = 0; j < kTM; ++j) {
+          gf32x16_t p[kTN];
+#pragma unroll
+          for (int i = 0; i < kTN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) p[i][r] = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const gu32x4_t v = chunk(xs + j * 4096, 2 * q + fhalf);
+            const gbf16x8_t x0 = widen(v.x, v.y, sxf[j]), x1 = widen(v.z, v.w, sxf[j]);
+#pragma unroll
+            for (int i = 0; i < kTN; ++i) {
+              const gu32x4_t u = chunk(ws + i * 4096, 2 * q + fhalf);
+              p[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(u.x, u.y, 1.0f), x0, p[i], 0, 0, 0);
+              p[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(u.z, u.w, 1.0f), x1, p[i], 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kTN; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(p[i][r], wscale, acc[i][j][r]);
+        }
+      }
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  const bool vec = (N & 3) == 0 && ((uintptr_t)Y & 15) == 0;
+#pragma unroll
+  for (int j = 0; j < kTM; ++j) {
+    const int64_t row = m0 + xrow + j * 32;
+    if (row >= M) continue;
+#pragma unroll
+    for (int i = 0; i < kTN; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int64_t col = n0 + wn * (BN / kWN) + i * 32 + 8 * g + 4 * fhalf;
+        if (col < N)
+          store4<kBf16>(Y, row * N + col, (int)col, (int)N, vec, acc[i][j][4 * g],
+                        acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+      }
+  }
+}
+
+// (The body is a device function: the host pass cannot instantiate it.)
+template <int BM, int BN, int kWM, int kWN, bool kF32Scale, bool kBf16>
+__global__ __launch_bounds__(kWM* kWN * 64) void gemm_fp8_tile_kernel(
+    const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
+    const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int64_t M,
+    int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n) {
+  gemm_fp8_tile<BM, BN, kWM, kWN, kF32Scale, kBf16>(X, XS, ldxs, W, WS, ldws, w_shift, M, N, K, Y,
+                                                    tiles_m, tiles_n);
+}
+
+// Few rows: bound by reading W once. A workgroup owns 16 columns of Y; its
+// waves take the K blocks in turn, W straight from memory into the MFMA's
+// operand registers, and their sums meet in LDS in a fixed order. Rows past M
+// or N repeat the last one and are not stored.
+constexpr int kSkinnyWaves = 8;
+template <int MB, bool kF32Scale, bool kBf16>
+__global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
+    const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
+    const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int M,
+    int64_t N, int K, void* __restrict__ Y) {
+  __shared__ gf32x4_t part[kSkinnyWaves][MB][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, kq = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int64_t wr = min(n0 + r16, N - 1);
+  const uint8_t* wp = W + wr * K + kq * 32;
+  const uint8_t* wsb = (const uint8_t*)WS + (wr >> w_shift) * ldws;
+  const float* wsf = (const float*)WS + (n0 >> 7) * ldws;
+  const uint8_t* xp[MB];
+  const uint8_t* xsb[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int xr = min(b * 16 + r16, M - 1);
+    xp[b] = X + (int64_t)xr * K + kq * 32;
+    xsb[b] = XS + (int64_t)xr * ldxs;
+  }
+  gf32x4_t acc[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) acc[b] = gf32x4_t{0, 0, 0, 0};
+  const int KB = K / 128;
+  for (int kb = wave; kb < KB; kb += kSkinnyWaves) {
+    const gu32x4_t* w = reinterpret_cast<const gu32x4_t*>(wp + (int64_t)kb * 128);
+    const gu32x4_t wa = w[0], wb = w[1];
+    const float sw = kF32Scale ? 1.0f : e8m0_f32(wsb[kb]);
+    const gbf16x8_t fw[4] = {widen(wa.x, wa.y, sw), widen(wa.z, wa.w, sw), widen(wb.x, wb.y, sw),
+                             widen(wb.z, wb.w, sw)};
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const gu32x4_t* x = reinterpret_cast<const gu32x4_t*>(xp[b] + (int64_t)kb * 128);
+      const gu32x4_t xa = x[0], xb = x[1];
+      const float sx = e8m0_f32(xsb[b][kb]);
+      gf32x4_t p = kF32Scale ? gf32x4_t{0, 0, 0, 0} : acc[b];
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[0], widen(xa.x, xa.y, sx), p, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[1], widen(xa.z, xa.w, sx), p, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[2], widen(xb.x, xb.y, sx), p, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[3], widen(xb.z, xb.w, sx), p, 0, 0, 0);
+      if constexpr (kF32Scale) {
+        const float swf = wsf[kb];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[b][r] = fmaf(p[r], swf, acc[b][r]);
+      } else {
+        acc[b] = p;
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < MB; ++b) part[wave][b][lane] = acc[b];
+  __syncthreads();
+  const bool vec = (N & 3) == 0 && ((uintptr_t)Y & 15) == 0;
+  for (int b = wave; b < MB; b += kSkinnyWaves) {
+    gf32x4_t s = part[0][b][lane];
+#pragma unroll
+    for (int w = 1; w < kSkinnyWaves; ++w) s += part[w][b][lane];
+    const int row = b * 16 + r16;
+    const int64_t col = n0 + kq * 4;
+    if (row < M && col < N)
+      store4<kBf16>(Y, (int64_t)row * N + col, (int)col, (int)N, vec, s[0], s[1], s[2], s[3]);
+  }
+}
+
+template <bool kF32Scale, bool kBf16>
+static hipError_t launch_gemm(const uint8_t* x, const uint8_t* xs, int64_t ldxs, const uint8_t* w,
+                              const void* ws, int64_t ldws, int w_shift, int64_t m, int64_t n,
+                              int64_t k, void* y, hipStream_t stream) {
+  if (m <= 64) {
+    const dim3 grid((unsigned)((n + 15) / 16)), block(kSkinnyWaves * 64);
+#define HIF4_SKINNY(mb)                                                                          \
+  hipLaunchKernelGGL((gemm_fp8_skinny_kernel<mb, kF32Scale, kBf16>), grid, block, 0, stream, x,  \
+                     xs, ldxs, w, ws, ldws, w_shift, (int)m, n, (int)k, y)
+    if (m <= 16) HIF4_SKINNY(1);
+    else if (m <= 32) HIF4_SKINNY(2);
+    else HIF4_SKINNY(4);
+#undef HIF4_SKINNY
+    return hipGetLastError();
+  }
+#define HIF4_TILED(bm, bn, wm, wn)                                                               \
+  do {                                                                                           \
+    const uint32_t tm = (uint32_t)((m + bm - 1) / bm), tn = (uint32_t)((n + bn - 1) / bn);       \
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<bm, bn, wm, wn, kF32Scale, kBf16>), dim3(tm * tn),  \
+                       dim3(wm * wn * 64), 0, stream, x, xs, ldxs, w, ws, ldws, w_shift, m, n,   \
+                       (int)k, y, tm, tn);                                                       \
+  } while (0)
+  if ((m + 255) / 256 * ((n + 255) / 256) >= 256) HIF4_TILED(256, 256, 2, 4);
+  else HIF4_TILED(128, 128, 2, 2);
+#undef HIF4_TILED
+  return hipGetLastError();
+}
+
+}  // namespace hif4
+
+using namespace hif4;
+
+hipError_t hif4_launch_gemm_fp8(const uint8_t* x, const uint8_t* xs, int64_t ldxs, const uint8_t* w,
+                                const void* ws, int64_t ldws, bool ws_f32, int w_block, int64_t m,
+                                int64_t n, int64_t k, void* y, bool y_bf16, void* workspace,
+                                hipStream_t stream) {
+  (void)workspace;
+  const int shift = w_block == 128 ? 7 : 0;
+  if (ws_f32) {
+    return y_bf16 ? launch_gemm<true, true>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, stream)
+                  : launch_gemm<true, false>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, stream);
+  }
+  return y_bf16 ? launch_gemm<false, true>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, stream)
+                : launch_gemm<false, false>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, stream);
+}
+
+// No launch needs scratch at present.
+size_t hif4_gemm_fp8_ws_bytes(int64_t m, int64_t n, int64_t k) {
+  (void)m, (void)n, (void)k;
+  return 0;
+}

@@ -70,6 +70,28 @@ def lib():
         L.hif4_higptq_block.argtypes = [p, i64, i64, i64, p, i64, i64, i64, ctypes.c_int, p, p, p,
                                         sz, p]
         L.hif4_higptq_block.restype = ctypes.c_int
+        i, d = ctypes.c_int, ctypes.c_double
+        L.hif4_quantize_fp8.argtypes = [p, i, i64, i64, i64, i64, i, p, p, i64, p]
+        L.hif4_quantize_fp8.restype = i
+        L.hif4_quantize_fp8_both.argtypes = [p, i, i64, i64, i64, i64, p, p, i64, p, p, i64, p]
+        L.hif4_quantize_fp8_both.restype = i
+        L.hif4_dequantize_fp8.argtypes = [p, p, i, i64, i64, i64, i64, p, i, p]
+        L.hif4_dequantize_fp8.restype = i
+        L.hif4_linear_fp8_workspace_bytes.argtypes = [i64, i64, i64]
+        L.hif4_linear_fp8_workspace_bytes.restype = sz
+        L.hif4_linear_fp8.argtypes = [p, p, i64, p, p, i64, i, i64, i64, i64, i64, p, i, p, sz, p]
+        L.hif4_linear_fp8.restype = i
+        L.hif4_layer_norm.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, i64, p, p, p]
+        L.hif4_layer_norm.restype = i
+        L.hif4_layer_norm_quantize.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, i64, p, p, p, p]
+        L.hif4_layer_norm_quantize.restype = i
+        L.hif4_layer_norm_quantize_fp8.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, p, i64, p]
+        L.hif4_layer_norm_quantize_fp8.restype = i
+        L.hif4_layer_norm_backward_workspace_bytes.argtypes = [i64, i64]
+        L.hif4_layer_norm_backward_workspace_bytes.restype = sz
+        L.hif4_layer_norm_backward.argtypes = [p, i64, p, i64, i, i64, i64, p, p, p, i, p, i64, p, p,
+                                               p, sz, p]
+        L.hif4_layer_norm_backward.restype = i
         _lib = L
     return _lib
 
@@ -374,3 +396,339 @@ def higptq(w, u, stream=None, scheme=1, block_units=8):
         higptq_block(w, u, unit0, min(block_units, units - unit0), codes, meta, workspace=ws,
                      stream=stream, scheme=scheme)
     return codes, meta
+
+
+# ---------------------------------------------------------------- 8-bit linear layers
+#
+# Codes are torch.float8_e4m3fn, power-of-two scales torch.float8_e8m0fnu (a
+# view of rows padded to whole 32-bit words: the stride is a multiple of 4).
+
+FP8_BLOCK = 128
+HIF4_SCALE_E8M0, HIF4_SCALE_F32 = 0, 1
+_DTYPE = {torch.float32: HIF4_F32, torch.bfloat16: HIF4_BF16}
+
+
+class _On:
+    """The device of a call's tensors and the stream its work goes to: checks
+    that every tensor given is on that device, makes it current, and allocates
+    outputs and workspaces on that stream (so their memory is not handed out
+    again while the stream still uses it)."""
+
+    def __init__(self, first, stream, **tensors):
+        if not first.is_cuda:
+            raise ValueError("tensors must be on the GPU")
+        for name, t in tensors.items():
+            if t is not None and t.device != first.device:
+                raise ValueError(f"{name} is on {t.device}, the call's other tensors on {first.device}")
+        if stream is not None and stream.device != first.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+        self.device = first.device
+        self.stream = stream if stream is not None else torch.cuda.current_stream(first.device)
+        self._ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self._ctx.__enter__()  # makes the stream's device current, too
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+def _check_rows(x, name):
+    if x.dtype not in _DTYPE or x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D fp32 or bf16 tensor with unit column stride")
+
+
+def _ld(t):
+    """Leading dimension of a 2-D tensor (a single row's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _up128(v):
+    return (v + 127) // 128 * 128
+
+
+def _empty_scales(rows, blocks, device):
+    full = torch.empty((rows, (blocks + 3) // 4 * 4), dtype=torch.float8_e8m0fnu, device=device)
+    return full[:, :blocks]
+
+
+def _check_out(t, name, shape, dtype):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape}")
+
+
+def _check_scales(t, name, rows, blocks):
+    """E8M0 scales [rows][blocks] whose rows are whole 32-bit words in memory."""
+    if t.dtype != torch.float8_e8m0fnu or tuple(t.shape) != (rows, blocks):
+        raise ValueError(f"{name} must be a float8_e8m0fnu tensor of shape {(rows, blocks)}")
+    if rows == 0 or blocks == 0:
+        return
+    ld = _ld(t)
+    held = t.untyped_storage().nbytes() - t.storage_offset()
+    if (blocks > 1 and t.stride(1) != 1) or ld % 4 or ld < blocks or held < (rows - 1) * ld + (blocks + 3) // 4 * 4:
+        raise ValueError(f"{name}: rows must be padded to a multiple of 4 bytes (stride {ld} for "
+                         f"{blocks} blocks)")
+
+
+def _scale_ld(t):
+    blocks = t.shape[1]
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), (blocks + 3) // 4 * 4)
+
+
+def _fp8_out(rows, length, block_rows, codes, scales, dev):
+    """Codes [rows][length up to 128s] and their scales, given or new."""
+    cols = _up128(length)
+    srows = (rows + block_rows - 1) // block_rows
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _check_out(codes, "codes", (rows, cols), torch.float8_e4m3fn)
+    if scales is None:
+        scales = _empty_scales(srows, cols // FP8_BLOCK, dev)
+    else:
+        _check_scales(scales, "scales", srows, cols // FP8_BLOCK)
+    return codes, scales
+
+
+def _check_block_rows(block_rows):
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+
+
+def quantize_fp8(x, block_rows=1, transposed=False, codes=None, scales=None, stream=None):
+    """E4M3-quantize x [rows][k] (bf16 or fp32) in blocks of 128 along k, or with
+    transposed=True x^T in blocks along the rows of x; block_rows=128: 128 x 128
+    tiles. Returns (codes [rows][k up to 128s], scales [rows / block_rows][blocks])."""
+    _check_rows(x, "x")
+    _check_block_rows(block_rows)
+    rows, k = x.shape
+    with _On(x, stream, codes=codes, scales=scales) as st:
+        out = (k, rows) if transposed else (rows, k)
+        codes, scales = _fp8_out(*out, block_rows, codes, scales, x.device)
+        _ok(lib().hif4_quantize_fp8(_ptr(x), _DTYPE[x.dtype], rows, k, _ld(x), block_rows,
+                                    int(bool(transposed)), _ptr(codes), _ptr(scales),
+                                    _scale_ld(scales), st), "hif4_quantize_fp8")
+    return codes, scales
+
+
+def quantize_fp8_both(x, block_rows=1, stream=None):
+    """quantize_fp8 of x and of x^T from one read: (codes, scales, codes_t, scales_t)."""
+    _check_rows(x, "x")
+    _check_block_rows(block_rows)
+    rows, k = x.shape
+    with _On(x, stream) as st:
+        codes, scales = _fp8_out(rows, k, block_rows, None, None, x.device)
+        codes_t, scales_t = _fp8_out(k, rows, block_rows, None, None, x.device)
+        _ok(lib().hif4_quantize_fp8_both(_ptr(x), _DTYPE[x.dtype], rows, k, _ld(x), block_rows,
+                                         _ptr(codes), _ptr(scales), _scale_ld(scales),
+                                         _ptr(codes_t), _ptr(scales_t), _scale_ld(scales_t), st),
+            "hif4_quantize_fp8_both")
+    return codes, scales, codes_t, scales_t
+
+
+def _check_codes(codes, name):
+    if (codes.dtype != torch.float8_e4m3fn or codes.dim() != 2 or not codes.is_contiguous()
+            or codes.shape[1] % FP8_BLOCK):
+        raise ValueError(f"{name} must be a contiguous 2-D float8_e4m3fn tensor, its rows a multiple "
+                         "of 128 long")
+
+
+def _weight_scales(scales, n, blocks, name):
+    """(scale type, block_rows, leading dimension) of a weight's scales."""
+    tiles = (n + FP8_BLOCK - 1) // FP8_BLOCK
+    if scales.dtype == torch.float32:
+        if tuple(scales.shape) != (tiles, blocks) or (blocks > 1 and scales.stride(1) != 1):
+            raise ValueError(f"{name}: float32 scales are one per 128 x 128 tile, {(tiles, blocks)}, "
+                             "with unit column stride")
+        return HIF4_SCALE_F32, FP8_BLOCK, _ld(scales)
+    rows = scales.shape[0] if scales.dim() == 2 and scales.shape[0] in (n, tiles) else n
+    _check_scales(scales, name, rows, blocks)
+    return HIF4_SCALE_E8M0, (1 if rows == n else FP8_BLOCK), _scale_ld(scales)
+
+
+def dequantize_fp8(codes, scales, k=None, out_dtype=torch.float32, out=None, stream=None):
+    """Values [rows][k] (fp32 or bf16) of codes and scales (E8M0 per 1 x 128 or
+    128 x 128, or float32 per 128 x 128); k: the columns before the padding."""
+    _check_codes(codes, "codes")
+    rows, kp = codes.shape
+    k = kp if k is None else int(k)
+    if _up128(k) != kp or k < 0:
+        raise ValueError(f"k = {k} does not fit codes of {kp} columns")
+    if out_dtype not in _DTYPE:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    with _On(codes, stream, scales=scales, out=out) as st:
+        kind, block_rows, ld = _weight_scales(scales, rows, kp // FP8_BLOCK, "scales")
+        if out is None:
+            out = torch.empty((rows, k), dtype=out_dtype, device=codes.device)
+        else:
+            _check_out(out, "out", (rows, k), out_dtype)
+        _ok(lib().hif4_dequantize_fp8(_ptr(codes), _ptr(scales), kind, block_rows, ld, rows, k,
+                                      _ptr(out), _DTYPE[out_dtype], st), "hif4_dequantize_fp8")
+    return out
+
+
+def linear_fp8_workspace_bytes(m, n, k):
+    return int(lib().hif4_linear_fp8_workspace_bytes(m, n, k))
+
+
+def linear_fp8(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=None, workspace=None,
+               stream=None):
+    """Y [m][n] = X W^T of E4M3 codes x_codes [m][k] (E8M0 scales per 1 x 128) and
+    w_codes [n][k] (E8M0 scales per 1 x 128 or 128 x 128, or float32 per 128 x 128)."""
+    _check_codes(x_codes, "x_codes")
+    _check_codes(w_codes, "w_codes")
+    (m, k), n = x_codes.shape, w_codes.shape[0]
+    if w_codes.shape[1] != k:
+        raise ValueError(f"x_codes has {k} columns, w_codes {w_codes.shape[1]}")
+    if y_dtype not in _DTYPE:
+        raise ValueError("y_dtype must be float32 or bfloat16")
+    with _On(x_codes, stream, x_scales=x_scales, w_codes=w_codes, w_scales=w_scales, y=y,
+             workspace=workspace) as st:
+        _check_scales(x_scales, "x_scales", m, k // FP8_BLOCK)
+        kind, block_rows, ldws = _weight_scales(w_scales, n, k // FP8_BLOCK, "w_scales")
+        if y is None:
+            y = torch.empty((m, n), dtype=y_dtype, device=x_codes.device)
+        else:
+            _check_out(y, "y", (m, n), y_dtype)
+        need = linear_fp8_workspace_bytes(m, n, k)
+        if workspace is None and need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=x_codes.device)
+        nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _ok(lib().hif4_linear_fp8(_ptr(x_codes), _ptr(x_scales), _scale_ld(x_scales), _ptr(w_codes),
+                                  _ptr(w_scales), ldws, kind, block_rows, m, n, k, _ptr(y),
+                                  _DTYPE[y_dtype], _ptr(workspace), nbytes, st), "hif4_linear_fp8")
+    return y
+
+
+def linear_fp8_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype=None,
+                        dw_dtype=torch.float32, stream=None):
+    """Gradients of Y = X W^T through the quantizers (taken as the identity):
+    dX [m][k] = Q(dY) W and dW [n][k] = Q(dY^T) X for dy [m][n] (bf16 or fp32),
+    with X^T and W^T quantized along m and n (quantize_fp8(..., transposed=True),
+    the weight with block_rows=128 or 1). dX is of dy's type unless dx_dtype says
+    otherwise."""
+    _check_rows(dy, "dy")
+    _check_codes(xt_codes, "xt_codes")
+    _check_codes(wt_codes, "wt_codes")
+    m, n = dy.shape
+    if xt_codes.shape[1] != _up128(m) or wt_codes.shape != (xt_codes.shape[0], _up128(n)):
+        raise ValueError(f"dy is {m} x {n}: xt_codes must be [k][{_up128(m)}], wt_codes [k][{_up128(n)}]")
+    if xt_scales.dtype == torch.float32:
+        raise ValueError("xt_scales must be float8_e8m0fnu, one per 1 x 128")
+    codes, scales, codes_t, scales_t = quantize_fp8_both(dy, stream=stream)
+    dx = linear_fp8(codes, scales, wt_codes, wt_scales, y_dtype=dx_dtype or dy.dtype, stream=stream)
+    dw = linear_fp8(codes_t, scales_t, xt_codes, xt_scales, y_dtype=dw_dtype, stream=stream)
+    return dx, dw
+
+
+# ---------------------------------------------------------------- layer norm
+
+
+def _check_affine(weight, bias, c):
+    """(weight, bias) dtype code; float32 when neither is given."""
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None and (t.dtype not in _DTYPE or tuple(t.shape) != (c,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 or bf16 tensor of shape {(c,)}")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError("weight and bias must have one dtype")
+    first = weight if weight is not None else bias
+    return HIF4_F32 if first is None else _DTYPE[first.dtype]
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-6, y=None, stream=None):
+    """Layer norm over the rows of x [rows][c] (bf16 or fp32): (y, mean, rstd), y
+    of x's dtype, mean and rstd float32 [rows] for the backward."""
+    _check_rows(x, "x")
+    rows, c = x.shape
+    wd = _check_affine(weight, bias, c)
+    with _On(x, stream, weight=weight, bias=bias, y=y) as st:
+        if y is None:
+            y = torch.empty((rows, c), dtype=x.dtype, device=x.device)
+        elif y.dtype != x.dtype or y.shape != x.shape or (c > 1 and y.stride(1) != 1):
+            raise ValueError("y must have x's dtype and shape and unit column stride")
+        mean = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        _ok(lib().hif4_layer_norm(_ptr(x), _DTYPE[x.dtype], rows, c, _ld(x), _ptr(weight),
+                                  _ptr(bias), wd, float(eps), _ptr(y), _ld(y), _ptr(mean),
+                                  _ptr(rstd), st), "hif4_layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_quantize(x, weight=None, bias=None, eps=1e-6, mask=None, codes=None, meta=None,
+                        stream=None):
+    """layer_norm (rounded to bf16) and quantize in one pass: (codes, meta, kept),
+    what linear_w4a4 takes as x_codes, x_meta and x_kept."""
+    _check_rows(x, "x")
+    rows, c = x.shape
+    wd = _check_affine(weight, bias, c)
+    if c % 64:
+        raise ValueError(f"HiF4 units are 64 wide: {c} columns")
+    with _On(x, stream, weight=weight, bias=bias, mask=mask, codes=codes, meta=meta) as st:
+        n_mask, kept = 0, None
+        if mask is not None:
+            if mask.dtype != torch.uint8 or tuple(mask.shape) != (c,) or not mask.is_contiguous():
+                raise ValueError(f"mask must be a contiguous uint8 tensor of shape {(c,)}")
+            n_mask = int(torch.count_nonzero(mask).item())
+            kept = torch.empty((rows, n_mask), dtype=torch.bfloat16, device=x.device)
+        if codes is None:
+            codes = torch.empty((rows, c // 2), dtype=torch.uint8, device=x.device)
+        else:
+            _check_out(codes, "codes", (rows, c // 2), torch.uint8)
+        if meta is None:
+            meta = torch.empty((rows, c // 64), dtype=torch.int32, device=x.device)
+        else:
+            _check_out(meta, "meta", (rows, c // 64), torch.int32)
+        _ok(lib().hif4_layer_norm_quantize(_ptr(x), _DTYPE[x.dtype], rows, c, _ld(x), _ptr(weight),
+                                           _ptr(bias), wd, float(eps), _ptr(mask), n_mask,
+                                           _ptr(kept) if n_mask else None, _ptr(codes), _ptr(meta),
+                                           st), "hif4_layer_norm_quantize")
+    return codes, meta, kept
+
+
+def layer_norm_quantize_fp8(x, weight=None, bias=None, eps=1e-6, codes=None, scales=None,
+                            stream=None):
+    """layer_norm and quantize_fp8 (blocks of 1 x 128) in one pass: (codes, scales),
+    what linear_fp8 takes as x_codes and x_scales."""
+    _check_rows(x, "x")
+    rows, c = x.shape
+    wd = _check_affine(weight, bias, c)
+    with _On(x, stream, weight=weight, bias=bias, codes=codes, scales=scales) as st:
+        codes, scales = _fp8_out(rows, c, 1, codes, scales, x.device)
+        _ok(lib().hif4_layer_norm_quantize_fp8(_ptr(x), _DTYPE[x.dtype], rows, c, _ld(x),
+                                               _ptr(weight), _ptr(bias), wd, float(eps),
+                                               _ptr(codes), _ptr(scales), _scale_ld(scales), st),
+            "hif4_layer_norm_quantize_fp8")
+    return codes, scales
+
+
+def layer_norm_backward_workspace_bytes(rows, c):
+    return int(lib().hif4_layer_norm_backward_workspace_bytes(rows, c))
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, workspace=None, stream=None):
+    """Gradients of layer_norm: (dx, dweight, dbias); dweight and dbias in the
+    weight's dtype (float32 without a weight)."""
+    _check_rows(x, "x")
+    _check_rows(dy, "dy")
+    rows, c = x.shape
+    if dy.dtype != x.dtype or dy.shape != x.shape:
+        raise ValueError("dy must have x's dtype and shape")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype != torch.float32 or tuple(t.shape) != (rows,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(rows,)}")
+    wd = _check_affine(weight, None, c)
+    with _On(x, stream, dy=dy, mean=mean, rstd=rstd, weight=weight, workspace=workspace) as st:
+        dx = torch.empty((rows, c), dtype=x.dtype, device=x.device)
+        wdt = weight.dtype if weight is not None else torch.float32
+        dweight = torch.empty((c,), dtype=wdt, device=x.device)
+        dbias = torch.empty((c,), dtype=wdt, device=x.device)
+        if workspace is None:
+            need = max(layer_norm_backward_workspace_bytes(rows, c), 1)
+            workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+        _ok(lib().hif4_layer_norm_backward(_ptr(dy), _ld(dy), _ptr(x), _ld(x), _DTYPE[x.dtype], rows,
+                                           c, _ptr(mean), _ptr(rstd), _ptr(weight), wd, _ptr(dx), c,
+                                           _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), st),
+            "hif4_layer_norm_backward")
+    return dx, dweight, dbias

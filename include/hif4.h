@@ -82,6 +82,9 @@ typedef enum hif4_status {
 
 typedef enum hif4_dtype { HIF4_F32 = 0, HIF4_BF16 = 1 } hif4_dtype;
 
+/* Scales of the 8-bit block format below. */
+typedef enum hif4_scale_type { HIF4_SCALE_E8M0 = 0, HIF4_SCALE_F32 = 1 } hif4_scale_type;
+
 /* Static, NUL-terminated description of a status code. Never NULL. */
 HIF4_EXPORT const char *hif4_status_string(int status);
 
@@ -402,6 +405,150 @@ HIF4_EXPORT size_t hif4_higptq_block_workspace_bytes(int64_t n, int64_t units);
 HIF4_EXPORT hif4_status hif4_higptq_block(float *w, int64_t n, int64_t k, int64_t ldw,
                               const float *u, int64_t ldu, int64_t unit0, int64_t units,
                               int scheme, uint8_t *codes, uint32_t *meta, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit linear layers: E4M3 codes with a scale per block of 128, for the
+ * layers a model keeps above 4 bits, and for their gradients.
+ *
+ * FORMAT
+ *  - codes u8: OCP E4M3 (sign, 4 exponent bits, 3 fraction bits; largest 448).
+ *  - A block is 128 consecutive elements of a row (block_rows = 1: activations
+ *    and gradients), or a 128 x 128 tile (block_rows = 128: weights, whose
+ *    transpose then has the transposed codes and scales). Its scale is the
+ *    smallest power of two s >= 2^-127 with max|x| <= 448 s, stored as the
+ *    E8M0 byte log2(s) + 127; codes are round-to-nearest-even(x / s). A block
+ *    that holds a NaN or an infinity gets scale byte 255 (E8M0's NaN) and
+ *    codes 0x7F: it decodes to NaN throughout.
+ *  - Rows of codes are contiguous, their length rounded up to a multiple of
+ *    128 with zero codes. Scales are [rows / block_rows, rounded up][lds],
+ *    lds >= the number of blocks in a row.
+ *  - Codes are 16-byte, E8M0 scales 4-byte aligned, and lds % 4 == 0 where a
+ *    product reads them (every entry point but the decoder asks for it): the
+ *    bytes of four blocks are one word. Bytes past the last block are read
+ *    and never used; each row holds lds of them, the last row too.
+ */
+
+/*
+ * hif4_quantize_fp8 -- quantize x [rows][k] in blocks along k, or (transposed)
+ * x^T, a [k][rows] matrix, in blocks along the rows of x.
+ *
+ *  x      [rows][ld] of x_dtype (HIF4_F32 or HIF4_BF16), ld >= k, aligned to
+ *         its element; any rows < 2^31, any k <= 2^22 (whole 16-byte runs are
+ *         read where base and ld allow it).
+ *  block_rows 1 or 128 (HIF4_ERR_ARG otherwise); transposed 0 or 1.
+ *  codes  [rows][k up to 128s], or transposed [k][rows up to 128s].
+ *  scales [rows][lds] / [ceil(rows/128)][lds], or transposed [k][lds] /
+ *         [ceil(k/128)][lds].
+ */
+HIF4_EXPORT hif4_status hif4_quantize_fp8(const void *x, int x_dtype, int64_t rows, int64_t k,
+                              int64_t ld, int64_t block_rows, int transposed, uint8_t *codes,
+                              uint8_t *scales, int64_t lds, hipStream_t stream);
+
+/*
+ * hif4_quantize_fp8_both -- both of the above from one read of x: what the two
+ * products of a linear layer's backward take (dY along n and along m), or a
+ * weight and its transpose (block_rows = 128).
+ */
+HIF4_EXPORT hif4_status hif4_quantize_fp8_both(const void *x, int x_dtype, int64_t rows, int64_t k,
+                              int64_t ld, int64_t block_rows, uint8_t *codes, uint8_t *scales,
+                              int64_t lds, uint8_t *codes_t, uint8_t *scales_t, int64_t lds_t,
+                              hipStream_t stream);
+
+/*
+ * hif4_dequantize_fp8 -- codes [rows][k up to 128s] and scales to values
+ * [rows][k] of out_dtype (element-aligned), code times scale rounded once.
+ *  scale_type HIF4_SCALE_E8M0 (u8) or HIF4_SCALE_F32 (float).
+ */
+HIF4_EXPORT hif4_status hif4_dequantize_fp8(const uint8_t *codes, const void *scales,
+                              int scale_type, int64_t block_rows, int64_t lds, int64_t rows,
+                              int64_t k, void *out, int out_dtype, hipStream_t stream);
+
+/* Workspace of hif4_linear_fp8; 0 for sizes it refuses, and where it needs
+ * none (then workspace may be NULL). */
+HIF4_EXPORT size_t hif4_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
+ * hif4_linear_fp8 -- Y = X W^T, Y[i][j] = sum over blocks b of
+ * sx[i][b] sw[j][b] sum over t in b of cx[i][t] cw[j][t], accumulated in fp32
+ * and rounded once to y_dtype.
+ *
+ *  x_codes [m][k], x_scales E8M0 [m][ldxs] (block_rows 1).
+ *  w_codes [n][k]; w_scales E8M0 [n][ldws] (w_block_rows 1) or
+ *          [ceil(n/128)][ldws] (128), or float [ceil(n/128)][ldws] with
+ *          HIF4_SCALE_F32 and w_block_rows 128 (a checkpoint's own scales;
+ *          HIF4_ERR_ARG with w_block_rows 1).
+ *  m, n    >= 0, below 2^31.  k >= 0, k % 128 == 0 (pad with zero codes), at
+ *          most 2^22; k = 0 gives Y = 0.
+ *  y       [m][n] contiguous of y_dtype, 16-byte aligned.
+ *  workspace >= hif4_linear_fp8_workspace_bytes(m, n, k), 256-byte aligned.
+ *  The two gradients of the layer are products of the same form:
+ *  dX = Q(dY) W: x = dY quantized along n, w = W transposed;
+ *  dW = Q(dY^T) X: x = dY transposed, w = X transposed (w_block_rows 1).
+ */
+HIF4_EXPORT hif4_status hif4_linear_fp8(const uint8_t *x_codes, const uint8_t *x_scales,
+                              int64_t ldxs, const uint8_t *w_codes, const void *w_scales,
+                              int64_t ldws, int w_scale_type, int64_t w_block_rows, int64_t m,
+                              int64_t n, int64_t k, void *y, int y_dtype, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm, the producer of a linear layer's input.
+ *
+ *  x      [rows][ld] of x_dtype (HIF4_F32 or HIF4_BF16), aligned to its
+ *         element (16-byte rows are read in whole runs); any rows < 2^31,
+ *         1 <= c <= 65536.
+ *  weight, bias  [c] of w_dtype, or NULL (1 and 0); element-aligned.
+ *  eps    finite and >= 0 (HIF4_ERR_ARG otherwise).
+ *  y = (x - mean) rstd weight + bias, rstd = (var + eps)^(-1/2), var the mean
+ *  of (x - mean)^2. Statistics in fp32; y rounded once.
+ */
+
+/* hif4_layer_norm -- y [rows][ldy] of x's type (may be x itself with the same
+ * leading dimension); mean and rstd float [rows], either may be NULL. */
+HIF4_EXPORT hif4_status hif4_layer_norm(const void *x, int x_dtype, int64_t rows, int64_t c,
+                              int64_t ld, const void *weight, const void *bias, int w_dtype,
+                              double eps, void *y, int64_t ldy, float *mean, float *rstd,
+                              hipStream_t stream);
+
+/*
+ * hif4_layer_norm_quantize -- the norm and hif4_quantize in one pass over x:
+ * codes, meta and kept are those of hif4_quantize on y rounded to bf16.
+ *  c % 64 == 0. mask, n_mask, kept, codes, meta as for hif4_quantize.
+ */
+HIF4_EXPORT hif4_status hif4_layer_norm_quantize(const void *x, int x_dtype, int64_t rows,
+                              int64_t c, int64_t ld, const void *weight, const void *bias,
+                              int w_dtype, double eps, const uint8_t *mask, int64_t n_mask,
+                              void *kept, uint8_t *codes, uint32_t *meta, hipStream_t stream);
+
+/* hif4_layer_norm_quantize_fp8 -- the norm and hif4_quantize_fp8 (block_rows 1)
+ * in one pass: codes [rows][c up to 128s] and scales [rows][lds] of y rounded
+ * to x's type. */
+HIF4_EXPORT hif4_status hif4_layer_norm_quantize_fp8(const void *x, int x_dtype, int64_t rows,
+                              int64_t c, int64_t ld, const void *weight, const void *bias,
+                              int w_dtype, double eps, uint8_t *codes, uint8_t *scales,
+                              int64_t lds, hipStream_t stream);
+
+/* Workspace of hif4_layer_norm_backward (0 for sizes it refuses). */
+HIF4_EXPORT size_t hif4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t c);
+
+/*
+ * hif4_layer_norm_backward -- with xhat = (x - mean) rstd and g = dy weight:
+ *  dx = rstd (g - mean(g) - xhat mean(g xhat)), the means over the row;
+ *  dweight = sum over rows of dy xhat, dbias = sum over rows of dy (fixed
+ *  order, no atomics).
+ *  dy [rows][lddy], x [rows][ldx], dx [rows][lddx] of x_dtype (dx may be dy
+ *  with the same leading dimension); mean, rstd float [rows] of the forward;
+ *  weight [c] of w_dtype or NULL (1). dweight, dbias [c] of w_dtype, written
+ *  (zeros for rows = 0), either may be NULL; with both NULL no workspace is
+ *  needed.
+ *  workspace >= hif4_layer_norm_backward_workspace_bytes(rows, c), 256-byte
+ *  aligned.
+ */
+HIF4_EXPORT hif4_status hif4_layer_norm_backward(const void *dy, int64_t lddy, const void *x,
+                              int64_t ldx, int x_dtype, int64_t rows, int64_t c, const float *mean,
+                              const float *rstd, const void *weight, int w_dtype, void *dx,
+                              int64_t lddx, void *dweight, void *dbias, void *workspace,
                               size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
