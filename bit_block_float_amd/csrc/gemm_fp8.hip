@@ -22,6 +22,8 @@
 //
 // The MFMA's first operand is W, so a lane of the result holds one row of Y
 // (its column index) and runs of 4 consecutive columns.
+#include <type_traits>
+
 #include "fp8_dev.h"
 
 namespace hif4 {
@@ -30,6 +32,7 @@ typedef __attribute__((ext_vector_type(8))) int i32x8_t;
 typedef __attribute__((ext_vector_type(8))) __bf16 gbf16x8_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t bf16x8_words_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t gu32x4_t;
+typedef __attribute__((ext_vector_type(2))) uint32_t gu32x2_t;
 typedef __attribute__((ext_vector_type(16))) float gf32x16_t;
 typedef __attribute__((ext_vector_type(4))) float gf32x4_t;
 typedef __attribute__((address_space(3))) void glds_void_t;
@@ -84,6 +87,85 @@ __device__ __forceinline__ void store4(void* y, int64_t off, int col, int n, boo
   }
 }
 
+// The wave's part of Y: kTN x kTM blocks of 32 x 32 (block (i, j): columns from
+// col0 + 32 i, rows from row0 + 32 j). In the MFMA's result lane l holds row
+// l & 31 and, in group g of 4 registers, columns 8 g + 4 (l >> 5) .. + 3: stored
+// from there, an instruction would touch 32 lines for 16 or 32 bytes each. The
+// rows go through LDS instead (`stage`: the wave's own kStageBytes; a wave's LDS
+// accesses complete in order) and leave as whole lines, past the caches' care
+// (Y is read by no one here). Measured on 57600 x 13824 x 5120 with bf16 Y: the
+// direct stores cost 0.69 of 3.85 ms.
+template <bool kBf16, int kTN>
+constexpr int kStageBytes = 32 * (kTN * 32 * (kBf16 ? 2 : 4) + 16);
+
+template <bool kBf16, int kTN, int kTM>
+__device__ __forceinline__ void store_tile(const gf32x16_t (&acc)[kTN][kTM], char* stage, void* Y,
+                                           int64_t row0, int64_t col0, int64_t M, int64_t N,
+                                           int lane) {
+  constexpr int kE = kBf16 ? 2 : 4, kPer = 16 / kE;          // elements a 16-byte piece
+  constexpr int kPitch = kTN * 32 * kE + 16;                 // rows start 4 banks apart
+  constexpr int kLanes = kTN * 32 * kE / 16;                 // pieces a row
+  constexpr int kRows = 64 / kLanes;                         // rows an instruction
+  const bool vec = (N & (kPer - 1)) == 0 && ((uintptr_t)Y & 15) == 0;
+  const bool whole = vec && row0 + 32 * kTM <= M && col0 + 32 * kTN <= N;  // uniform
+  char* const put = stage + (lane & 31) * kPitch + (lane >> 5) * 4 * kE;
+  const char* const get = stage + (lane / kLanes) * kPitch + (lane % kLanes) * 16;
+  const int64_t col = col0 + (lane % kLanes) * kPer;
+#pragma unroll
+  for (int j = 0; j < kTM; ++j) {
+#pragma unroll
+    for (int i = 0; i < kTN; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const gf32x16_t& a = acc[i][j];
+        char* dst = put + (i * 32 + 8 * g) * kE;
+        if constexpr (kBf16)
+          *reinterpret_cast<gu32x2_t*>(dst) =
+              gu32x2_t{f32_to_bf16(a[4 * g]) | (f32_to_bf16(a[4 * g + 1]) << 16),
+                       f32_to_bf16(a[4 * g + 2]) | (f32_to_bf16(a[4 * g + 3]) << 16)};
+        else
+          *reinterpret_cast<gf32x4_t*>(dst) =
+              gf32x4_t{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
+      }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < 32 / kRows; ++p) {
+      const gu32x4_t v = *reinterpret_cast<const gu32x4_t*>(get + p * kRows * kPitch);
+      const int64_t row = row0 + j * 32 + p * kRows + lane / kLanes;
+      char* dst = reinterpret_cast<char*>(Y) + (row * N + col) * kE;
+      if (whole || (vec && row < M && col + kPer <= N)) {
+        __builtin_nontemporal_store(v, reinterpret_cast<gu32x4_t*>(dst));
+      } else if (row < M) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          if (col + e >= N) break;
+          if constexpr (kBf16)
+            reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+          else
+            reinterpret_cast<uint32_t*>(dst)[e] = v[e];
+        }
+      }
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Tile (row, column) of workgroup t: consecutive workgroup ids go to different
+// XCDs; each XCD gets a contiguous run of tiles, walked column by column in
+// groups of 8 tile rows.
+__device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, int64_t& tm,
+                                        int64_t& tn) {
+  const uint32_t per_xcd = tiles_m * tiles_n / 8;
+  if (t < per_xcd * 8) t = (t & 7) * per_xcd + (t >> 3);
+  const uint32_t group = 8, per_group = group * tiles_n;
+  const uint32_t gi = t / per_group, first = gi * group, in = t - gi * per_group;
+  const uint32_t gsize = min(tiles_m - first, group);
+  tm = __builtin_amdgcn_readfirstlane(first + in % gsize);
+  tn = __builtin_amdgcn_readfirstlane(in / gsize);
+}
+
 // Tile kernel. BM x BN of Y a workgroup, kWM x kWN waves. A stage is one block
 // of 128 along K: rows of 128 bytes = 8 chunks of 16, chunk c of row r in slot
 // c ^ ((r >> 1) & 7), so that the fragment reads of 16 consecutive rows land in
@@ -106,18 +188,10 @@ __device__ __forceinline__ void gemm_fp8_tile(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / kWN, wn = wave % kWN;
 
-  // Tile order: consecutive workgroup ids go to different XCDs; each XCD gets a
-  // contiguous run of tiles, walked column by column in groups of 8 tile rows.
-  const uint32_t ntiles = tiles_m * tiles_n;
-  uint32_t t = blockIdx.x;
-  {
-    const uint32_t per_xcd = ntiles / 8;
-    if (t < per_xcd * 8) t = (t & 7) * per_xcd + (t >> 3);
-  }
-  const uint32_t group = 8, per_group = group * tiles_n;
-  const uint32_t gi = t / per_group, first = gi * group, in = t - gi * per_group;
-  const uint32_t gsize = min(tiles_m - first, group);
-  const int64_t m0 = (int64_t)(first + in % gsize) * BM, n0 = (int64_t)(in / gsize) * BN;
+  int64_t m0, n0;
+  tile_of(blockIdx.x, tiles_m, tiles_n, m0, n0);
+  m0 *= BM;
+  n0 *= BN;
 
   const int mrows = (int)min((int64_t)BM, M - m0), nrows = (int)min((int64_t)BN, N - n0);
   const __amdgpu_buffer_rsrc_t rx =
@@ -309,23 +383,12 @@ __device__ __forceinline__ void gemm_fp8_tile(
       }
     }
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-
-  const bool vec = (N & 3) == 0 && ((uintptr_t)Y & 15) == 0;
-#pragma unroll
-  for (int j = 0; j < kTM; ++j) {
-    const int64_t row = m0 + xrow + j * 32;
-    if (row >= M) continue;
-#pragma unroll
-    for (int i = 0; i < kTN; ++i)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t col = n0 + wn * (BN / kWN) + i * 32 + 8 * g + 4 * fhalf;
-        if (col < N)
-          store4<kBf16>(Y, row * N + col, (int)col, (int)N, vec, acc[i][j][4 * g],
-                        acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
-      }
-  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  static_assert(kWaves * kStageBytes<kBf16, kTN> <= (int)sizeof(lds), "epilogue stage");
+  store_tile<kBf16, kTN, kTM>(acc, lds + wave * kStageBytes<kBf16, kTN>, Y, m0 + wm * (BM / kWM),
+                              n0 + wn * (BN / kWN), M, N, lane);
 }
 
 // (The body is a device function: the host pass cannot instantiate it.)
@@ -336,6 +399,209 @@ __global__ __launch_bounds__(kWM* kWN * 64) void gemm_fp8_tile_kernel(
     int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n) {
   gemm_fp8_tile<BM, BN, kWM, kWN, kF32Scale, kBf16>(X, XS, ldxs, W, WS, ldws, w_shift, M, N, K, Y,
                                                     tiles_m, tiles_n);
+}
+
+// Large products with E8M0 scales on both sides. 256 x 256 of Y a workgroup, 4
+// waves of 128 x 128 (256 fp32 accumulators a lane), one workgroup a CU: against
+// 8 waves of 128 x 64 a third less is read from LDS per product, and LDS would
+// be busy as long as the matrix cores.
+//
+// A stage is one block (128 K values): rows of 128 bytes, whole cache lines,
+// chunk c of 16 bytes in slot c ^ ((row >> 1) & 7) (the reads of 16 consecutive
+// rows land in distinct bank groups). Two stages are in LDS, each multiplied in
+// two halves of 64 K values: while half 0 of block kb multiplies from registers,
+// half 1 is read into the other register set; then one barrier, after which no
+// wave needs the stage, and block kb + 2 goes out into it by direct-to-LDS loads
+// while half 1 multiplies and half 0 of block kb + 1 is read. Blocks past the end
+// load the last one again, into a stage that no one reads.
+constexpr int kBigSlot = 2 * 256 * 128;
+constexpr int kBigScaleRing = 2 * 256 * 4;
+constexpr int kBigLds = 2 * kBigSlot + 2 * kBigScaleRing + 1024;  // + a sink for idle scale loads
+
+template <bool kBf16>
+__device__ __forceinline__ void gemm_fp8_big(
+    const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
+    const uint8_t* __restrict__ W, const uint8_t* __restrict__ WS, int64_t ldws, int w_shift,
+    int64_t M, int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n) {
+  __shared__ __attribute__((aligned(1024))) char lds[kBigLds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  int64_t m0, n0;
+  tile_of(blockIdx.x, tiles_m, tiles_n, m0, n0);
+  m0 *= 256;
+  n0 *= 256;
+
+  const int mrows = (int)min((int64_t)256, M - m0), nrows = (int)min((int64_t)256, N - n0);
+  const __amdgpu_buffer_rsrc_t rx =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(X + m0 * K), (short)0, mrows * K, kRsrc3);
+  const __amdgpu_buffer_rsrc_t rw =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(W + n0 * K), (short)0, nrows * K, kRsrc3);
+  const int xs_bytes = (int)(mrows * ldxs), ws_bytes = (int)((((nrows - 1) >> w_shift) + 1) * ldws);
+
+  // loads: instruction i of a wave brings rows 64 wave + 8 (i & 7) .. + 7 of X (i < 8) or W
+  uint32_t voff[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int row = wave * 64 + i * 8 + (lane >> 3);
+    voff[i] = (uint32_t)row * (uint32_t)K + (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+  }
+  const int KB = K / 128;
+  auto load_part = [&](int kb, int i) {
+    char* dst = lds + (kb & 1) * kBigSlot + (i >> 3) * 32768 + wave * 8192 + (i & 7) * 1024;
+    const int off = min(kb, KB - 1) * 128;
+    if (i < 8)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (glds_void_t*)dst, 16, voff[i & 7], off, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (glds_void_t*)dst, 16, voff[i & 7], off, 0, 0);
+  };
+  // Scale words of blocks 4g .. 4g + 3: a wave brings 64 rows of X's in block 4g - 4
+  // and of W's in block 4g - 3. (One load a block, whose target is chosen without
+  // a branch: a branch in the loop would let the compiler move products across
+  // the step's barrier.)
+  const uint32_t xs_off = (uint32_t)(wave * 64 + lane) * (uint32_t)ldxs;
+  const uint32_t ws_off = (uint32_t)((wave * 64 + lane) >> w_shift) * (uint32_t)ldws;
+  const int last_group = (KB - 1) >> 2;
+  char* const scale_ring = lds + 2 * kBigSlot;
+  auto load_scale = [&](int kb) {
+    const int g = min((kb >> 2) + 1, last_group), part = kb & 3;
+    char* dst = part < 2 ? scale_ring + (((kb >> 2) + 1) & 1) * kBigScaleRing + part * 1024
+                         : scale_ring + 2 * kBigScaleRing;
+    const bool is_w = (part & 1) != 0;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(is_w ? WS + (n0 >> w_shift) * ldws : XS + m0 * ldxs), (short)0,
+        is_w ? ws_bytes : xs_bytes, kRsrc3);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (glds_void_t*)(dst + wave * 256), 4,
+                                             is_w ? ws_off : xs_off, 4 * g, 0, 0);
+  };
+
+  const int frow = lane & 31, fhalf = lane >> 5, fsw = (frow >> 1) & 7;
+  const char* const xbase = lds + (wm * 128 + frow) * 128;
+  const char* const wbase = lds + 32768 + (wn * 128 + frow) * 128;
+  // fragments of half a block: blocks of 32 rows 0..3 of X, 4..7 of W, two chunks each
+  struct Frags {
+    gu32x4_t v[8][2];
+  };
+  int slot[2][2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) slot[s][e] = ((4 * s + 2 * fhalf + e) ^ fsw) * 16;
+  auto read_part = [&](Frags& f, int kb, int s, int p) {  // p = 0..15
+    const char* base = ((p >> 1) < 4 ? xbase : wbase) + (kb & 1) * kBigSlot + ((p >> 1) & 3) * 4096;
+    f.v[p >> 1][p & 1] = *reinterpret_cast<const gu32x4_t*>(base + slot[s][p & 1]);
+  };
+  uint32_t sw[8];  // this block's scale bytes (low byte): X blocks, W blocks
+  uint32_t snext[8];
+  auto read_scale = [&](int kb, int b) {  // the word that holds block kb's byte
+    const char* base = scale_ring + ((kb >> 2) & 1) * kBigScaleRing + (b < 4 ? 0 : 1024);
+    snext[b] = *reinterpret_cast<const uint32_t*>(
+        base + ((b < 4 ? wm : wn) * 128 + (b & 3) * 32 + frow) * 4);
+  };
+
+  gf32x16_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  load_scale(-4);
+  load_scale(-3);
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) load_part(kb, i);
+  asm volatile("s_waitcnt vmcnt(16)" ::: "memory");  // scales and block 0
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  Frags f0, f1;
+#pragma unroll
+  for (int p = 0; p < 16; ++p) read_part(f0, 0, 0, p);
+#pragma unroll
+  for (int b = 0; b < 8; ++b) read_scale(0, b);
+
+  // one half (s of block kb): the products of `cur`, the other half's fragments
+  // into `nxt`, and in half 1 the loads of block kb + 2
+  auto half = [&](const Frags& cur, Frags& nxt, int kb, auto s, const uint32_t (&sc)[8]) {
+    constexpr int kS = decltype(s)::value;
+    auto reads = [&](int p) { read_part(nxt, kb + kS, 1 - kS, p); };
+    if constexpr (kBf16) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        // the reads first: the barrier waits for the last of them
+        if (c < 8) {
+          reads(2 * c);
+          reads(2 * c + 1);
+          if constexpr (kS == 1) {
+            load_part(kb + 2, 2 * c);
+            load_part(kb + 2, 2 * c + 1);
+          }
+        }
+        const int i = c >> 2, j = c & 3;
+        acc[i][j] = mfma32(join(cur.v[4 + i][0], cur.v[4 + i][1]), join(cur.v[j][0], cur.v[j][1]),
+                           acc[i][j], (int)sc[4 + i], (int)sc[j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+      float sf[8];
+#pragma unroll
+      for (int b = 0; b < 8; ++b) sf[b] = e8m0_f32(sc[b] & 255u);
+      gbf16x8_t d[2][8];  // widened operands of 16 K values a lane pair, two sets in turn
+#pragma unroll
+      for (int b = 0; b < 8; ++b) d[0][b] = widen(cur.v[b][0].x, cur.v[b][0].y, sf[b]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          if (c < 4) reads(4 * q + c);
+          if constexpr (kS == 1) {
+            if (c >= 4 && c < 12 && (c & 1) == 0) load_part(kb + 2, 4 * q + ((c - 4) >> 1));
+          }
+          if (q < 3 && (c & 1)) {
+            const gu32x4_t v = cur.v[c >> 1][(q + 1) >> 1];
+            d[(q + 1) & 1][c >> 1] = ((q + 1) & 1) ? widen(v.z, v.w, sf[c >> 1]) : widen(v.x, v.y, sf[c >> 1]);
+          }
+          const int i = c >> 2, j = c & 3;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d[q & 1][4 + i], d[q & 1][j],
+                                                              acc[i][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  };
+  using H0 = std::integral_constant<int, 0>;
+  using H1 = std::integral_constant<int, 1>;
+  for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+    for (int b = 0; b < 8; ++b) sw[b] = snext[b] >> (8 * (kb & 3));
+    half(f0, f1, kb, H0{}, sw);
+    // block kb is in registers everywhere, block kb + 1 has landed
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    load_scale(kb);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) read_scale(kb + 1, b);
+    half(f1, f0, kb, H1{}, sw);
+  }
+  // every load has landed and every wave has read what it will: the stages are free
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  static_assert(4 * kStageBytes<kBf16, 4> <= kBigLds, "epilogue stage");
+  store_tile<kBf16, 4, 4>(acc, lds + wave * kStageBytes<kBf16, 4>, Y, m0 + wm * 128, n0 + wn * 128,
+                          M, N, lane);
+}
+
+template <bool kBf16>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_fp8_big_kernel(const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
+                         const uint8_t* __restrict__ W, const uint8_t* __restrict__ WS, int64_t ldws,
+                         int w_shift, int64_t M, int64_t N, int K, void* __restrict__ Y,
+                         uint32_t tiles_m, uint32_t tiles_n) {
+  gemm_fp8_big<kBf16>(X, XS, ldxs, W, WS, ldws, w_shift, M, N, K, Y, tiles_m, tiles_n);
 }
 
 // Few rows: bound by reading W once. A workgroup owns 16 columns of Y; its
@@ -431,7 +697,15 @@ static hipError_t launch_gemm(const uint8_t* x, const uint8_t* xs, int64_t ldxs,
                        dim3(wm * wn * 64), 0, stream, x, xs, ldxs, w, ws, ldws, w_shift, m, n,   \
                        (int)k, y, tm, tn);                                                       \
   } while (0)
-  if ((m + 255) / 256 * ((n + 255) / 256) >= 256) HIF4_TILED(256, 256, 2, 4);
+  if ((m + 255) / 256 * ((n + 255) / 256) >= 256) {
+    if constexpr (kF32Scale) {
+      HIF4_TILED(256, 256, 2, 4);
+    } else {
+      const uint32_t tm = (uint32_t)((m + 255) / 256), tn = (uint32_t)((n + 255) / 256);
+      hipLaunchKernelGGL(gemm_fp8_big_kernel<kBf16>, dim3(tm * tn), dim3(256), 0, stream, x, xs,
+                         ldxs, w, (const uint8_t*)ws, ldws, w_shift, m, n, (int)k, y, tm, tn);
+    }
+  }
   else HIF4_TILED(128, 128, 2, 2);
 #undef HIF4_TILED
   return hipGetLastError();
