@@ -110,10 +110,15 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
   uint32_t u = __float_as_uint(f);
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
-// The same for any input: a NaN stays one (quiet, its sign kept).
+// The same for any input (a NaN stays one), by the conversion instruction
+// (v_cvt_pk_bf16_f32): one value, or two as the halves of a word.
 __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return (u & 0x7FFFFFFFu) > 0x7F800000u ? (u >> 16) | 0x40u : f32_to_bf16_rne(f);
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f);
+}
+__device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
+  typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+  const pair_t p = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, p);
 }
 
 }  // namespace hif4

@@ -61,16 +61,14 @@ __device__ __forceinline__ void load_w8(const void* w, bool w_bf16, bool vec, in
 }
 
 __device__ __forceinline__ void store_run8(uint16_t* p, int valid, bool vec, const float (&v)[8]) {
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = f32_to_bf16(v[i]);
   if (vec && valid >= 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16),
-                                              h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
+                   f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < valid) p[i] = (uint16_t)h[i];
+      if (i < valid) p[i] = (uint16_t)f32_to_bf16(v[i]);
   }
 }
 __device__ __forceinline__ void store_run8(float* p, int valid, bool vec, const float (&v)[8]) {
@@ -198,7 +196,7 @@ __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float lo = y[i >> 2][2 * (i & 3)], hi = y[i >> 2][2 * (i & 3) + 1];
-          wds[i] = f32_to_bf16(lo) | (f32_to_bf16(hi) << 16);
+          wds[i] = f32x2_to_bf16x2(lo, hi);
         }
         uint4 v0 = make_uint4(wds[0], wds[1], wds[2], wds[3]);
         uint4 v1 = make_uint4(wds[4], wds[5], wds[6], wds[7]);

@@ -412,26 +412,43 @@ class _On:
     """The device of a call's tensors and the stream its work goes to: checks
     that every tensor given is on that device, makes it current, and allocates
     outputs and workspaces on that stream (so their memory is not handed out
-    again while the stream still uses it)."""
+    again while the stream still uses it). Switches nothing where the current
+    device and stream are the call's."""
 
-    def __init__(self, first, stream, **tensors):
+    __slots__ = ("_ctx", "_raw")
+
+    def __init__(self, first, stream, *tensors):
         if not first.is_cuda:
             raise ValueError("tensors must be on the GPU")
-        for name, t in tensors.items():
-            if t is not None and t.device != first.device:
-                raise ValueError(f"{name} is on {t.device}, the call's other tensors on {first.device}")
-        if stream is not None and stream.device != first.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
-        self.device = first.device
-        self.stream = stream if stream is not None else torch.cuda.current_stream(first.device)
-        self._ctx = torch.cuda.stream(self.stream)
+        index = first.get_device()
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                raise ValueError(f"a tensor is on {t.device}, the call's first one on {first.device}")
+        self._ctx = None
+        if stream is not None:
+            if stream.device_index != index:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+            self._raw = stream.cuda_stream
+            self._ctx = torch.cuda.stream(stream)  # makes the stream's device current, too
+        else:
+            self._raw = torch._C._cuda_getCurrentRawStream(index)
+            if torch._C._cuda_getDevice() != index:
+                self._ctx = torch.cuda.device(index)
 
     def __enter__(self):
-        self._ctx.__enter__()  # makes the stream's device current, too
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self._raw
 
     def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+        return False
+
+
+def _at(t):
+    """Address of a tensor, or None."""
+    return t.data_ptr() if t is not None else None
 
 
 def _check_rows(x, name):
@@ -503,11 +520,11 @@ def quantize_fp8(x, block_rows=1, transposed=False, codes=None, scales=None, str
     _check_rows(x, "x")
     _check_block_rows(block_rows)
     rows, k = x.shape
-    with _On(x, stream, codes=codes, scales=scales) as st:
+    with _On(x, stream, codes, scales) as st:
         out = (k, rows) if transposed else (rows, k)
         codes, scales = _fp8_out(*out, block_rows, codes, scales, x.device)
-        _ok(lib().hif4_quantize_fp8(_ptr(x), _DTYPE[x.dtype], rows, k, _ld(x), block_rows,
-                                    int(bool(transposed)), _ptr(codes), _ptr(scales),
+        _ok(lib().hif4_quantize_fp8(_at(x), _DTYPE[x.dtype], rows, k, _ld(x), block_rows,
+                                    int(bool(transposed)), _at(codes), _at(scales),
                                     _scale_ld(scales), st), "hif4_quantize_fp8")
     return codes, scales
 
@@ -520,9 +537,9 @@ def quantize_fp8_both(x, block_rows=1, stream=None):
     with _On(x, stream) as st:
         codes, scales = _fp8_out(rows, k, block_rows, None, None, x.device)
         codes_t, scales_t = _fp8_out(k, rows, block_rows, None, None, x.device)
-        _ok(lib().hif4_quantize_fp8_both(_ptr(x), _DTYPE[x.dtype], rows, k, _ld(x), block_rows,
-                                         _ptr(codes), _ptr(scales), _scale_ld(scales),
-                                         _ptr(codes_t), _ptr(scales_t), _scale_ld(scales_t), st),
+        _ok(lib().hif4_quantize_fp8_both(_at(x), _DTYPE[x.dtype], rows, k, _ld(x), block_rows,
+                                         _at(codes), _at(scales), _scale_ld(scales),
+                                         _at(codes_t), _at(scales_t), _scale_ld(scales_t), st),
             "hif4_quantize_fp8_both")
     return codes, scales, codes_t, scales_t
 
@@ -557,14 +574,14 @@ def dequantize_fp8(codes, scales, k=None, out_dtype=torch.float32, out=None, str
         raise ValueError(f"k = {k} does not fit codes of {kp} columns")
     if out_dtype not in _DTYPE:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    with _On(codes, stream, scales=scales, out=out) as st:
+    with _On(codes, stream, scales, out) as st:
         kind, block_rows, ld = _weight_scales(scales, rows, kp // FP8_BLOCK, "scales")
         if out is None:
             out = torch.empty((rows, k), dtype=out_dtype, device=codes.device)
         else:
             _check_out(out, "out", (rows, k), out_dtype)
-        _ok(lib().hif4_dequantize_fp8(_ptr(codes), _ptr(scales), kind, block_rows, ld, rows, k,
-                                      _ptr(out), _DTYPE[out_dtype], st), "hif4_dequantize_fp8")
+        _ok(lib().hif4_dequantize_fp8(_at(codes), _at(scales), kind, block_rows, ld, rows, k,
+                                      _at(out), _DTYPE[out_dtype], st), "hif4_dequantize_fp8")
     return out
 
 
@@ -583,8 +600,7 @@ def linear_fp8(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=No
         raise ValueError(f"x_codes has {k} columns, w_codes {w_codes.shape[1]}")
     if y_dtype not in _DTYPE:
         raise ValueError("y_dtype must be float32 or bfloat16")
-    with _On(x_codes, stream, x_scales=x_scales, w_codes=w_codes, w_scales=w_scales, y=y,
-             workspace=workspace) as st:
+    with _On(x_codes, stream, x_scales, w_codes, w_scales, y, workspace) as st:
         _check_scales(x_scales, "x_scales", m, k // FP8_BLOCK)
         kind, block_rows, ldws = _weight_scales(w_scales, n, k // FP8_BLOCK, "w_scales")
         if y is None:
@@ -595,9 +611,9 @@ def linear_fp8(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=No
         if workspace is None and need:
             workspace = torch.empty((need,), dtype=torch.uint8, device=x_codes.device)
         nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _ok(lib().hif4_linear_fp8(_ptr(x_codes), _ptr(x_scales), _scale_ld(x_scales), _ptr(w_codes),
-                                  _ptr(w_scales), ldws, kind, block_rows, m, n, k, _ptr(y),
-                                  _DTYPE[y_dtype], _ptr(workspace), nbytes, st), "hif4_linear_fp8")
+        _ok(lib().hif4_linear_fp8(_at(x_codes), _at(x_scales), _scale_ld(x_scales), _at(w_codes),
+                                  _at(w_scales), ldws, kind, block_rows, m, n, k, _at(y),
+                                  _DTYPE[y_dtype], _at(workspace), nbytes, st), "hif4_linear_fp8")
     return y
 
 
@@ -642,16 +658,16 @@ def layer_norm(x, weight=None, bias=None, eps=1e-6, y=None, stream=None):
     _check_rows(x, "x")
     rows, c = x.shape
     wd = _check_affine(weight, bias, c)
-    with _On(x, stream, weight=weight, bias=bias, y=y) as st:
+    with _On(x, stream, weight, bias, y) as st:
         if y is None:
             y = torch.empty((rows, c), dtype=x.dtype, device=x.device)
         elif y.dtype != x.dtype or y.shape != x.shape or (c > 1 and y.stride(1) != 1):
             raise ValueError("y must have x's dtype and shape and unit column stride")
         mean = torch.empty((rows,), dtype=torch.float32, device=x.device)
         rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
-        _ok(lib().hif4_layer_norm(_ptr(x), _DTYPE[x.dtype], rows, c, _ld(x), _ptr(weight),
-                                  _ptr(bias), wd, float(eps), _ptr(y), _ld(y), _ptr(mean),
-                                  _ptr(rstd), st), "hif4_layer_norm")
+        _ok(lib().hif4_layer_norm(_at(x), _DTYPE[x.dtype], rows, c, _ld(x), _at(weight),
+                                  _at(bias), wd, float(eps), _at(y), _ld(y), _at(mean),
+                                  _at(rstd), st), "hif4_layer_norm")
     return y, mean, rstd
 
 
@@ -664,7 +680,7 @@ def layer_norm_quantize(x, weight=None, bias=None, eps=1e-6, mask=None, codes=No
     wd = _check_affine(weight, bias, c)
     if c % 64:
         raise ValueError(f"HiF4 units are 64 wide: {c} columns")
-    with _On(x, stream, weight=weight, bias=bias, mask=mask, codes=codes, meta=meta) as st:
+    with _On(x, stream, weight, bias, mask, codes, meta) as st:
         n_mask, kept = 0, None
         if mask is not None:
             if mask.dtype != torch.uint8 or tuple(mask.shape) != (c,) or not mask.is_contiguous():
@@ -679,9 +695,9 @@ def layer_norm_quantize(x, weight=None, bias=None, eps=1e-6, mask=None, codes=No
             meta = torch.empty((rows, c // 64), dtype=torch.int32, device=x.device)
         else:
             _check_out(meta, "meta", (rows, c // 64), torch.int32)
-        _ok(lib().hif4_layer_norm_quantize(_ptr(x), _DTYPE[x.dtype], rows, c, _ld(x), _ptr(weight),
-                                           _ptr(bias), wd, float(eps), _ptr(mask), n_mask,
-                                           _ptr(kept) if n_mask else None, _ptr(codes), _ptr(meta),
+        _ok(lib().hif4_layer_norm_quantize(_at(x), _DTYPE[x.dtype], rows, c, _ld(x), _at(weight),
+                                           _at(bias), wd, float(eps), _at(mask), n_mask,
+                                           _at(kept) if n_mask else None, _at(codes), _at(meta),
                                            st), "hif4_layer_norm_quantize")
     return codes, meta, kept
 
@@ -693,11 +709,11 @@ def layer_norm_quantize_fp8(x, weight=None, bias=None, eps=1e-6, codes=None, sca
     _check_rows(x, "x")
     rows, c = x.shape
     wd = _check_affine(weight, bias, c)
-    with _On(x, stream, weight=weight, bias=bias, codes=codes, scales=scales) as st:
+    with _On(x, stream, weight, bias, codes, scales) as st:
         codes, scales = _fp8_out(rows, c, 1, codes, scales, x.device)
-        _ok(lib().hif4_layer_norm_quantize_fp8(_ptr(x), _DTYPE[x.dtype], rows, c, _ld(x),
-                                               _ptr(weight), _ptr(bias), wd, float(eps),
-                                               _ptr(codes), _ptr(scales), _scale_ld(scales), st),
+        _ok(lib().hif4_layer_norm_quantize_fp8(_at(x), _DTYPE[x.dtype], rows, c, _ld(x),
+                                               _at(weight), _at(bias), wd, float(eps),
+                                               _at(codes), _at(scales), _scale_ld(scales), st),
             "hif4_layer_norm_quantize_fp8")
     return codes, scales
 
@@ -718,7 +734,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, workspace=None, stream=N
         if t.dtype != torch.float32 or tuple(t.shape) != (rows,) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(rows,)}")
     wd = _check_affine(weight, None, c)
-    with _On(x, stream, dy=dy, mean=mean, rstd=rstd, weight=weight, workspace=workspace) as st:
+    with _On(x, stream, dy, mean, rstd, weight, workspace) as st:
         dx = torch.empty((rows, c), dtype=x.dtype, device=x.device)
         wdt = weight.dtype if weight is not None else torch.float32
         dweight = torch.empty((c,), dtype=wdt, device=x.device)
@@ -726,9 +742,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, workspace=None, stream=N
         if workspace is None:
             need = max(layer_norm_backward_workspace_bytes(rows, c), 1)
             workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
-        _ok(lib().hif4_layer_norm_backward(_ptr(dy), _ld(dy), _ptr(x), _ld(x), _DTYPE[x.dtype], rows,
-                                           c, _ptr(mean), _ptr(rstd), _ptr(weight), wd, _ptr(dx), c,
-                                           _ptr(dweight), _ptr(dbias), _ptr(workspace),
+        _ok(lib().hif4_layer_norm_backward(_at(dy), _ld(dy), _at(x), _ld(x), _DTYPE[x.dtype], rows,
+                                           c, _at(mean), _at(rstd), _at(weight), wd, _at(dx), c,
+                                           _at(dweight), _at(dbias), _at(workspace),
                                            workspace.numel() * workspace.element_size(), st),
             "hif4_layer_norm_backward")
     return dx, dweight, dbias
