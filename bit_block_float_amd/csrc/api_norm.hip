@@ -40,11 +40,10 @@ hif4_status check_forward(const void* x, int x_dtype, int64_t rows, int64_t c, i
   a.rows = rows;
   a.ld = ld;
   a.c = (int)c;
-  a.vec = vec_rows(x, ld, x_dtype);
+  a.vec = c % 8 == 0 && vec_rows(x, ld, x_dtype) && aligned(weight, 16) && aligned(bias, 16);
   a.w = weight;
   a.b = bias;
   a.w_bf16 = w_dtype == HIF4_BF16;
-  a.w_vec = aligned(weight, 16) && aligned(bias, 16);
   a.eps = (float)eps;
   return HIF4_OK;
 }
@@ -65,7 +64,7 @@ hif4_status hif4_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t c,
   if (!aligned(y, elem(x_dtype)) || !aligned(mean, 4) || !aligned(rstd, 4)) return HIF4_ERR_ALIGN;
   a.y = y;
   a.ldy = ldy;
-  a.y_vec = vec_rows(y, ldy, x_dtype);
+  a.vec = a.vec && vec_rows(y, ldy, x_dtype);
   a.mean = mean;
   a.rstd = rstd;
   st = check_device();
@@ -148,11 +147,10 @@ hif4_status hif4_layer_norm_backward(const void* dy, int64_t lddy, const void* x
   a.ldx = ldx;
   a.lddx = lddx;
   a.c = (int)c;
-  a.vec = vec_rows(dy, lddy, x_dtype) && vec_rows(x, ldx, x_dtype);
-  a.dx_vec = vec_rows(dx, lddx, x_dtype);
+  a.vec = c % 8 == 0 && vec_rows(dy, lddy, x_dtype) && vec_rows(x, ldx, x_dtype) &&
+          vec_rows(dx, lddx, x_dtype) && aligned(weight, 16);
   a.w = weight;
   a.w_bf16 = w_dtype == HIF4_BF16;
-  a.w_vec = aligned(weight, 16);
   a.mean = mean;
   a.rstd = rstd;
   a.dx = dx;

@@ -24,20 +24,19 @@ __device__ __forceinline__ uint32_t max16_u32(uint32_t v) {  // over 16 aligned 
 // lanes a block; the block maximum is formed with DPP moves. One item a thread
 // and no loop, as in quantize_kernel: workgroups retire and are replaced on
 // whichever CUs run ahead.
-template <typename T>
+template <typename T, bool kVec>
 __global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(
     const T* __restrict__ x, int64_t ld, int k, uint32_t items_per_row, FastDiv item_div,
-    uint32_t total_items, bool vec, uint4* __restrict__ codes, uint8_t* __restrict__ scales,
+    uint32_t total_items, uint4* __restrict__ codes, uint8_t* __restrict__ scales,
     int64_t lds) {
   const uint32_t it = blockIdx.x * 256u + threadIdx.x;
   if (it >= total_items) return;  // whole blocks: items_per_row is a multiple of 8
   const uint32_t row = fdiv(it, item_div);
   const uint32_t j = it - row * items_per_row;
-  const T* src = x + (int64_t)row * ld + (int64_t)j * 16;
-  const int valid = k - (int)j * 16;
+  const T* src = x + (int64_t)row * ld;
   Run8<T> r0, r1;
-  r0.load(src, valid, vec);
-  r1.load(src + 8, valid - 8, vec);
+  r0.template load<kVec>(src, (int)j * 16, k);
+  r1.template load<kVec>(src, (int)j * 16 + 8, k);
   uint32_t am = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) am = max(am, max(abs_bits(r0.get(i)), abs_bits(r1.get(i))));
@@ -59,9 +58,9 @@ __global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(
 // which go through LDS to leave as whole 128-byte lines.
 //  kTile: one scale for the tile; else one per row (kRows) or column (kCols).
 //  kRows: codes [rows][ceil(k/128)*128]; kCols: codes_t [k][ceil(rows/128)*128].
-template <typename T, bool kTile, bool kRows, bool kCols>
+template <typename T, bool kTile, bool kRows, bool kCols, bool kVec>
 __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
-    const T* __restrict__ x, int64_t ld, int64_t rows, int k, bool vec, uint32_t tiles_k,
+    const T* __restrict__ x, int64_t ld, int64_t rows, int k, uint32_t tiles_k,
     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t lds,
     uint8_t* __restrict__ codes_t, uint8_t* __restrict__ scales_t, int64_t lds_t) {
   constexpr int kPitch = 128 + 16;  // 16-byte reads stay aligned, columns spread over banks
@@ -75,10 +74,10 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
   const int col0 = tk * 128 + cg * 8;
   Run8<T> v[8];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    if (row0 + r < rows) v[r].load(x + (row0 + r) * ld + col0, k - col0, vec);
-    else v[r].zero();
-  }
+  for (int r = 0; r < 8; ++r)
+    v[r].template load<kVec>(x + min(row0 + r, rows - 1) * ld, col0, k);
+#pragma unroll
+  for (int r = 0; r < 8; ++r) v[r].keep_if(row0 + r < rows);
   uint32_t e_tile = 0;
   uint32_t e_col[8];
   if constexpr (kTile) {
@@ -209,12 +208,11 @@ __global__ __launch_bounds__(256) void dequantize_fp8_kernel(
   }
 }
 
-template <typename T>
+template <typename T, bool kVec>
 static hipError_t launch_quantize(const T* x, int64_t rows, int64_t k, int64_t ld, int block_rows,
                                   uint8_t* codes, uint8_t* scales, int64_t lds, uint8_t* codes_t,
                                   uint8_t* scales_t, int64_t lds_t, hipStream_t stream) {
   const int64_t tiles_k = (k + 127) / 128, kp = tiles_k * 128;
-  const bool vec = ((uintptr_t)x & 15) == 0 && ld % (16 / (int64_t)sizeof(T)) == 0;
   if (block_rows == 1 && !codes_t) {
     const uint32_t ipr = (uint32_t)(kp / 16);
     const FastDiv fd = make_fastdiv(ipr);
@@ -222,8 +220,8 @@ static hipError_t launch_quantize(const T* x, int64_t rows, int64_t k, int64_t l
     for (int64_t r0 = 0; r0 < rows; r0 += max_rows) {
       const int64_t nr = rows - r0 < max_rows ? rows - r0 : max_rows;
       const uint32_t total = (uint32_t)(nr * ipr);
-      hipLaunchKernelGGL(quantize_fp8_rows_kernel<T>, dim3((total + 255) / 256), dim3(256), 0,
-                         stream, x + r0 * ld, ld, (int)k, ipr, fd, total, vec,
+      hipLaunchKernelGGL((quantize_fp8_rows_kernel<T, kVec>), dim3((total + 255) / 256), dim3(256),
+                         0, stream, x + r0 * ld, ld, (int)k, ipr, fd, total,
                          reinterpret_cast<uint4*>(codes + r0 * kp), scales + r0 * lds, lds);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
@@ -234,8 +232,8 @@ static hipError_t launch_quantize(const T* x, int64_t rows, int64_t k, int64_t l
   const dim3 grid((unsigned)tiles), block(256);
   const uint32_t tk = (uint32_t)tiles_k;
 #define HIF4_TILE(tile, r, c)                                                                     \
-  hipLaunchKernelGGL((quantize_fp8_tile_kernel<T, tile, r, c>), grid, block, 0, stream, x, ld,    \
-                     rows, (int)k, vec, tk, codes, scales, lds, codes_t, scales_t, lds_t)
+  hipLaunchKernelGGL((quantize_fp8_tile_kernel<T, tile, r, c, kVec>), grid, block, 0, stream, x,  \
+                     ld, rows, (int)k, tk, codes, scales, lds, codes_t, scales_t, lds_t)
   if (block_rows == 1) {
     if (codes) HIF4_TILE(false, true, true);
     else HIF4_TILE(false, false, true);
@@ -257,11 +255,13 @@ hipError_t hif4_launch_quantize_fp8(const void* x, bool bf16, int64_t rows, int6
                                     int block_rows, uint8_t* codes, uint8_t* scales, int64_t lds,
                                     uint8_t* codes_t, uint8_t* scales_t, int64_t lds_t,
                                     hipStream_t stream) {
-  if (bf16)
-    return launch_quantize((const uint16_t*)x, rows, k, ld, block_rows, codes, scales, lds, codes_t,
-                           scales_t, lds_t, stream);
-  return launch_quantize((const float*)x, rows, k, ld, block_rows, codes, scales, lds, codes_t,
-                         scales_t, lds_t, stream);
+  const bool vec = ((uintptr_t)x & 15) == 0 && ld % (bf16 ? 8 : 4) == 0 && k % 8 == 0;
+#define HIF4_QUANTIZE(T, v)                                                                     \
+  launch_quantize<T, v>((const T*)x, rows, k, ld, block_rows, codes, scales, lds, codes_t,       \
+                        scales_t, lds_t, stream)
+  if (bf16) return vec ? HIF4_QUANTIZE(uint16_t, true) : HIF4_QUANTIZE(uint16_t, false);
+  return vec ? HIF4_QUANTIZE(float, true) : HIF4_QUANTIZE(float, false);
+#undef HIF4_QUANTIZE
 }
 
 hipError_t hif4_launch_dequantize_fp8(const uint8_t* codes, const void* scales, bool scales_f32,

@@ -35,26 +35,41 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
 }
 constexpr uint32_t kFp8NaN4 = 0x7F7F7F7Fu;  // four E4M3 NaNs
 
-// 8 consecutive elements of a row as fp32; elements at or past `valid` read as
-// zero. `vec`: the row is 16-byte aligned (a uniform flag), so a whole run is
-// one (bf16) or two (fp32) 16-byte loads.
+// 8 consecutive elements of a row of c >= 1, from column col; elements at or past
+// c are zero. The loads are unconditional, from clamped addresses (a load behind
+// a branch is waited for at the branch's end, one after the other). kVec: rows
+// are 16-byte aligned and c % 8 == 0, so a run is whole or empty: one (bf16) or
+// two (fp32) 16-byte loads. Otherwise element by element.
 template <typename T>
 struct Run8;
 template <>
 struct Run8<uint16_t> {
   uint4 w;
-  __device__ __forceinline__ void load(const uint16_t* p, int valid, bool vec) {
-    if (vec && valid >= 8) {
-      w = *reinterpret_cast<const uint4*>(p);
+  template <bool kVec>
+  __device__ __forceinline__ void load(const uint16_t* row, int col, int c) {
+    if constexpr (kVec) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + (col < c ? col : 0));
+      const uint32_t m = col < c ? 0xFFFFFFFFu : 0u;
+      w = make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
     } else {
       uint32_t h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = i < valid ? p[i] : 0u;
+      for (int i = 0; i < 8; ++i) h[i] = row[min(col + i, c - 1)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = col + i < c ? h[i] : 0u;
       w = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
                      h[6] | (h[7] << 16));
     }
   }
-  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void keep_if(bool ok) {
+    const uint32_t m = ok ? 0xFFFFFFFFu : 0u;
+    w = make_uint4(w.x & m, w.y & m, w.z & m, w.w & m);
+  }
+  // keeps the run as the words it was loaded as: the compiler cannot carry fp32
+  // copies of the elements (twice the registers) past this point
+  __device__ __forceinline__ void opaque() {
+    asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+  }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t u = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
     return (i & 1) ? bf16hi_to_f32(u) : bf16lo_to_f32(u);
@@ -62,32 +77,28 @@ struct Run8<uint16_t> {
 };
 template <>
 struct Run8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p, int valid, bool vec) {
-    if (vec && valid >= 8) {
-      a = reinterpret_cast<const float4*>(p)[0];
-      b = reinterpret_cast<const float4*>(p)[1];
+  float v[8];
+  template <bool kVec>
+  __device__ __forceinline__ void load(const float* row, int col, int c) {
+    if constexpr (kVec) {
+      const float4* p = reinterpret_cast<const float4*>(row + (col < c ? col : 0));
+      const float4 a = p[0], b = p[1];
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      keep_if(col < c);
     } else {
-      float h[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = i < valid ? p[i] : 0.0f;
-      a = make_float4(h[0], h[1], h[2], h[3]);
-      b = make_float4(h[4], h[5], h[6], h[7]);
+      for (int i = 0; i < 8; ++i) v[i] = row[min(col + i, c - 1)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = col + i < c ? v[i] : 0.0f;
     }
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
-  __device__ __forceinline__ float get(int i) const {
-    switch (i) {
-      case 0: return a.x;
-      case 1: return a.y;
-      case 2: return a.z;
-      case 3: return a.w;
-      case 4: return b.x;
-      case 5: return b.y;
-      case 6: return b.z;
-      default: return b.w;
-    }
+  __device__ __forceinline__ void keep_if(bool ok) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = ok ? v[i] : 0.0f;
   }
+  __device__ __forceinline__ void opaque() {}
+  __device__ __forceinline__ float get(int i) const { return v[i]; }
 };
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }

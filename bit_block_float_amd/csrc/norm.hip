@@ -10,6 +10,7 @@
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy.
 // Statistics, sums and gradients are fp32; results are rounded once.
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8_dev.h"
 #include "norm_dev.h"
@@ -17,13 +18,28 @@
 
 namespace hif4 {
 
+#ifndef NORM_WG
+#define NORM_WG 64
+#endif
 enum NormOut { kOutY = 0, kOutHif4 = 1, kOutFp8 = 2 };
 
-// Sum over the lanes of a wave, the same bits in every lane (butterfly order).
+// Sum over the lanes of a wave, the same bits in every lane: DPP moves inside
+// each row of 16 lanes, then the rows by permlane swaps (which leave the two
+// rows, or halves, of a pair in two registers): no LDS permutes.
+__device__ __forceinline__ float row16_sum(float v) {
+  auto f = [](uint32_t u) { return __uint_as_float(u); };
+  v += f(dpp<kDppQuadXor1>(__float_as_uint(v)));
+  v += f(dpp<kDppQuadXor2>(__float_as_uint(v)));
+  v += f(dpp<kDppHalfMirror>(__float_as_uint(v)));
+  return v + f(dpp<0x140>(__float_as_uint(v)));  // row_mirror
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  return v;
+  auto f = [](uint32_t u) { return __uint_as_float(u); };
+  v = row16_sum(v);
+  auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = f(p[0]) + f(p[1]);
+  p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(p[0]) + f(p[1]);
 }
 
 // Sum over the P threads that share a row (P = 64: one wave; else the whole
@@ -42,26 +58,29 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
 }
 
 // 8 weights or biases from column `col` (fp32 or bf16), 1 / 0 without one.
-__device__ __forceinline__ void load_w8(const void* w, bool w_bf16, bool vec, int col, int c,
-                                        float fallback, float (&v)[8]) {
+template <bool kVec>
+__device__ __forceinline__ void load_w8(const void* w, bool w_bf16, int col, int c, float fallback,
+                                        float (&v)[8]) {
   if (w == nullptr) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fallback;
   } else if (w_bf16) {
     Run8<uint16_t> r;
-    r.load(reinterpret_cast<const uint16_t*>(w) + col, c - col, vec);
+    r.load<kVec>(reinterpret_cast<const uint16_t*>(w), col, c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = r.get(i);
   } else {
     Run8<float> r;
-    r.load(reinterpret_cast<const float*>(w) + col, c - col, vec);
+    r.load<kVec>(reinterpret_cast<const float*>(w), col, c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = r.get(i);
   }
 }
 
-__device__ __forceinline__ void store_run8(uint16_t* p, int valid, bool vec, const float (&v)[8]) {
-  if (vec && valid >= 8) {
+template <bool kVec>
+__device__ __forceinline__ void store_run8(uint16_t* p, int valid, const float (&v)[8]) {
+  if constexpr (kVec) {
+    if (valid <= 0) return;
     *reinterpret_cast<uint4*>(p) =
         make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
                    f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
@@ -71,8 +90,10 @@ __device__ __forceinline__ void store_run8(uint16_t* p, int valid, bool vec, con
       if (i < valid) p[i] = (uint16_t)f32_to_bf16(v[i]);
   }
 }
-__device__ __forceinline__ void store_run8(float* p, int valid, bool vec, const float (&v)[8]) {
-  if (vec && valid >= 8) {
+template <bool kVec>
+__device__ __forceinline__ void store_run8(float* p, int valid, const float (&v)[8]) {
+  if constexpr (kVec) {
+    if (valid <= 0) return;
     reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
   } else {
@@ -82,12 +103,65 @@ __device__ __forceinline__ void store_run8(float* p, int valid, bool vec, const 
   }
 }
 
+// Item j (16 columns) of a row of results: as they are, to HiF4, or to E4M3.
+template <typename T, int kOut, bool kVec>
+__device__ __forceinline__ void store_item(const NormArgs& a, float (&y)[2][8], int64_t row, int j,
+                                           int c, uint32_t info) {
+  const int col = j * 16;
+  if constexpr (kOut == kOutY) {
+    T* dst = reinterpret_cast<T*>(a.y) + row * a.ldy + col;
+    store_run8<kVec>(dst, c - col, y[0]);
+    store_run8<kVec>(dst + 8, c - col - 8, y[1]);
+  } else if constexpr (kOut == kOutHif4) {
+    uint32_t wds[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float lo = y[i >> 2][2 * (i & 3)], hi = y[i >> 2][2 * (i & 3) + 1];
+      wds[i] = f32x2_to_bf16x2(lo, hi);
+    }
+    uint4 v0 = make_uint4(wds[0], wds[1], wds[2], wds[3]);
+    uint4 v1 = make_uint4(wds[4], wds[5], wds[6], wds[7]);
+    if (a.mask) {
+      keep_item_values(v0, v1, info, row, a.kept, a.n_mask);
+      uint32_t z[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t lo = (info >> (16 + 2 * i)) & 1u, hi = (info >> (17 + 2 * i)) & 1u;
+        z[i] = ~((lo * 0x0000FFFFu) | (hi * 0xFFFF0000u));
+      }
+      v0 = make_uint4(v0.x & z[0], v0.y & z[1], v0.z & z[2], v0.w & z[3]);
+      v1 = make_uint4(v1.x & z[4], v1.y & z[5], v1.z & z[6], v1.w & z[7]);
+    }
+    quantize_item(v0, v1, (uint32_t)j, (uint32_t)j,
+                  reinterpret_cast<uint32_t*>(a.codes + row * (c / 2)), a.meta + row * (c / 64));
+  } else {
+    uint32_t am = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (sizeof(T) == 2) y[h][i] = bf16lo_to_f32(f32_to_bf16(y[h][i]));
+        if (col + 8 * h + i >= c) y[h][i] = 0.0f;  // the padding of the last block
+        am = max(am, abs_bits(y[h][i]));
+      }
+    const uint32_t e = e8m0_of(max8_u32(am));
+    const float inv = e8m0_inv(min(e, 254u));
+    uint4 w = make_uint4(encode4(y[0][0], y[0][1], y[0][2], y[0][3], inv),
+                         encode4(y[0][4], y[0][5], y[0][6], y[0][7], inv),
+                         encode4(y[1][0], y[1][1], y[1][2], y[1][3], inv),
+                         encode4(y[1][4], y[1][5], y[1][6], y[1][7], inv));
+    if (e == 255u) w = make_uint4(kFp8NaN4, kFp8NaN4, kFp8NaN4, kFp8NaN4);
+    *reinterpret_cast<uint4*>(a.codes + row * a.kp + col) = w;
+    if ((j & 7) == 0) a.scales[row * a.lds + (j >> 3)] = (uint8_t)e;
+  }
+}
+
 // Forward. P threads share a row; a lane owns items (16 consecutive elements)
 // t, t + P, ..., the quantizers' own mapping, so 4 aligned lanes hold a HiF4
 // unit and 8 an E4M3 block when the row leaves through one of them. The value
 // quantized is the one kOutY would store (rounded to bf16 for HiF4, to x's type
 // for E4M3), so the codes are those of the two calls in turn.
-template <typename T, int P, int kItems, int kOut>
+template <typename T, int P, int kItems, int kOut, bool kVec>
 __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a) {
   constexpr int kRowsPerBlock = P > 64 ? 1 : 4;
   __shared__ float slots[2][P / 64];
@@ -145,8 +219,8 @@ __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a
 #pragma unroll
     for (int n = 0; n < kItems; ++n) {
       const int col = (n * P + t) * 16;
-      r0[n].load(src + col, c - col, a.vec);
-      r1[n].load(src + col + 8, c - col - 8, a.vec);
+      r0[n].template load<kVec>(src, col, c);
+      r1[n].template load<kVec>(src, col + 8, c);
     }
     float s = 0.0f;
 #pragma unroll
@@ -181,58 +255,136 @@ __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float w[8], b[8];
-        load_w8(a.w, a.w_bf16, a.w_vec, col + 8 * h, c, 1.0f, w);
-        load_w8(a.b, a.w_bf16, a.w_vec, col + 8 * h, c, 0.0f, b);
+        load_w8<kVec>(a.w, a.w_bf16, col + 8 * h, c, 1.0f, w);
+        load_w8<kVec>(a.b, a.w_bf16, col + 8 * h, c, 0.0f, b);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           y[h][i] = fmaf(((h ? r1[n] : r0[n]).get(i) - mean) * rstd, w[i], b[i]);
       }
-      if constexpr (kOut == kOutY) {
-        T* dst = reinterpret_cast<T*>(a.y) + row * a.ldy + col;
-        store_run8(dst, c - col, a.y_vec, y[0]);
-        store_run8(dst + 8, c - col - 8, a.y_vec, y[1]);
-      } else if constexpr (kOut == kOutHif4) {
-        uint32_t wds[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float lo = y[i >> 2][2 * (i & 3)], hi = y[i >> 2][2 * (i & 3) + 1];
-          wds[i] = f32x2_to_bf16x2(lo, hi);
-        }
-        uint4 v0 = make_uint4(wds[0], wds[1], wds[2], wds[3]);
-        uint4 v1 = make_uint4(wds[4], wds[5], wds[6], wds[7]);
-        if (a.mask) {
-          keep_item_values(v0, v1, info[n], row, a.kept, a.n_mask);
-          uint32_t z[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t lo = (info[n] >> (16 + 2 * i)) & 1u, hi = (info[n] >> (17 + 2 * i)) & 1u;
-            z[i] = ~((lo * 0x0000FFFFu) | (hi * 0xFFFF0000u));
-          }
-          v0 = make_uint4(v0.x & z[0], v0.y & z[1], v0.z & z[2], v0.w & z[3]);
-          v1 = make_uint4(v1.x & z[4], v1.y & z[5], v1.z & z[6], v1.w & z[7]);
-        }
-        quantize_item(v0, v1, (uint32_t)j, (uint32_t)j,
-                      reinterpret_cast<uint32_t*>(a.codes + row * (c / 2)), a.meta + row * (c / 64));
-      } else {
-        uint32_t am = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (sizeof(T) == 2) y[h][i] = bf16lo_to_f32(f32_to_bf16(y[h][i]));
-            if (col + 8 * h + i >= c) y[h][i] = 0.0f;  // the padding of the last block
-            am = max(am, abs_bits(y[h][i]));
-          }
-        const uint32_t e = e8m0_of(max8_u32(am));
-        const float inv = e8m0_inv(min(e, 254u));
-        uint4 w = make_uint4(encode4(y[0][0], y[0][1], y[0][2], y[0][3], inv),
-                             encode4(y[0][4], y[0][5], y[0][6], y[0][7], inv),
-                             encode4(y[1][0], y[1][1], y[1][2], y[1][3], inv),
-                             encode4(y[1][4], y[1][5], y[1][6], y[1][7], inv));
-        if (e == 255u) w = make_uint4(kFp8NaN4, kFp8NaN4, kFp8NaN4, kFp8NaN4);
-        *reinterpret_cast<uint4*>(a.codes + row * a.kp + col) = w;
-        if ((j & 7) == 0) a.scales[row * a.lds + (j >> 3)] = (uint8_t)e;
+      store_item<T, kOut, kVec>(a, y, row, j, c, info[n]);
+    }
+  }
+}
+
+// Forward of rows of up to 16384 columns. The block's T = blockDim.x threads (64
+// times the waves that a row's items of 16 columns fill) own one item each, of R
+// rows at a time: weight and bias stay in registers for all rows, where the
+// kernel above reads them again for each (57600 x 5120: they are twice x's own
+// bytes), and two barriers serve R rows. Everything else is as above.
+template <typename T, int R, int kOut, bool kMulti, bool kVec>
+__global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
+  __shared__ float slots[2][R][16];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int waves = kMulti ? (int)(blockDim.x >> 6) : 1;
+  const int c = a.c, col = t * 16;
+  const int items = kOut == kOutFp8 ? a.kp / 16 : (c + 15) / 16;
+  const bool live = t < items;
+
+  uint32_t info = 0;
+  if constexpr (kOut == kOutHif4) {
+    if (a.mask) {
+      __shared__ uint32_t part[16];
+      uint32_t m16 = 0;
+      if (live) {
+        const uint4 mk = *reinterpret_cast<const uint4*>(a.mask + col);
+        m16 = nonzero_bytes(mk.x) | (nonzero_bytes(mk.y) << 4) | (nonzero_bytes(mk.z) << 8) |
+              (nonzero_bytes(mk.w) << 12);
       }
+      const uint32_t cnt = __popc(m16);
+      uint32_t incl = cnt;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = (uint32_t)__shfl_up((int)incl, d, 64);
+        if (lane >= d) incl += o;
+      }
+      uint32_t base = incl - cnt;
+      if constexpr (kMulti) {
+        if (lane == 63) part[wave] = incl;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) base += part[w];
+      }
+      info = (m16 << 16) | (base & 0xFFFFu);
+    }
+  }
+
+  float w[2][8], b[2][8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    load_w8<kVec>(a.w, a.w_bf16, col + 8 * h, c, 1.0f, w[h]);
+    load_w8<kVec>(a.b, a.w_bf16, col + 8 * h, c, 0.0f, b[h]);
+  }
+
+  // sums over the row's threads, R at once; `slot` turns between the two
+  auto row_sums = [&](float (&v)[R], int slot) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = wave_sum(v[r]);
+    if constexpr (kMulti) {
+      if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) slots[slot][r][wave] = v[r];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        v[r] = row16_sum((lane & 15) < waves ? slots[slot][r][lane & 15] : 0.0f);
+    }
+  };
+
+  const float fc = (float)c, inv_c = 1.0f / (float)c;
+  for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < a.rows; row0 += (int64_t)gridDim.x * R) {
+    Run8<T> x0[R], x1[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      // rows past the end read the last one again and are not stored
+      const int64_t row = min(row0 + r, a.rows - 1);
+      const T* src = reinterpret_cast<const T*>(a.x) + row * a.ld;
+      x0[r].template load<kVec>(src, col, c);
+      x1[r].template load<kVec>(src, col + 8, c);
+    }
+    float mean[R], rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mean[r] += x0[r].get(i) + x1[r].get(i);
+    }
+    row_sums(mean, 0);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] /= fc;
+      x0[r].opaque();
+      x1[r].opaque();
+      float q = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d0 = col + i < c ? x0[r].get(i) - mean[r] : 0.0f;
+        const float d1 = col + 8 + i < c ? x1[r].get(i) - mean[r] : 0.0f;
+        q = fmaf(d0, d0, q);
+        q = fmaf(d1, d1, q);
+      }
+      rstd[r] = q;
+    }
+    row_sums(rstd, 1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) rstd[r] = 1.0f / sqrtf(rstd[r] * inv_c + a.eps);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = row0 + r;
+      if (row >= a.rows) break;  // uniform
+      if (kOut == kOutY && t == 0) {
+        if (a.mean) a.mean[row] = mean[r];
+        if (a.rstd) a.rstd[row] = rstd[r];
+      }
+      if (!live) continue;  // whole quads / octets of lanes: items is a multiple of 4 / 8
+      x0[r].opaque();
+      x1[r].opaque();
+      float y[2][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[0][i] = fmaf((x0[r].get(i) - mean[r]) * rstd[r], w[0][i], b[0][i]);
+        y[1][i] = fmaf((x1[r].get(i) - mean[r]) * rstd[r], w[1][i], b[1][i]);
+      }
+      store_item<T, kOut, kVec>(a, y, row, t, c, info);
     }
   }
 }
@@ -241,7 +393,7 @@ __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a
 // the same kRuns runs of 8 columns in every row and keeps their weight and its
 // part of dw and db in registers. The parts of all workgroups go to `parts`
 // ([gridDim.x][2][c]) and are added in a fixed order by the kernel below.
-template <typename T, int kRuns, bool kSums>
+template <typename T, int kRuns, bool kSums, bool kVec>
 __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs a) {
   __shared__ float sums[2][2][16];
   const int t = threadIdx.x, nt = blockDim.x, c = a.c;
@@ -250,7 +402,7 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
   float w[kRuns][8], dw[kRuns][8], db[kRuns][8];
 #pragma unroll
   for (int n = 0; n < kRuns; ++n) {
-    load_w8(a.w, a.w_bf16, a.w_vec, (n * nt + t) * 8, c, 1.0f, w[n]);
+    load_w8<kVec>(a.w, a.w_bf16, (n * nt + t) * 8, c, 1.0f, w[n]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[n][i] = db[n][i] = 0.0f;
   }
@@ -262,8 +414,8 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
 #pragma unroll
     for (int n = 0; n < kRuns; ++n) {
       const int col = (n * nt + t) * 8;
-      xr[n].load(xs + col, c - col, a.vec);
-      dr[n].load(ds + col, c - col, a.vec);
+      xr[n].template load<kVec>(xs, col, c);
+      dr[n].template load<kVec>(ds, col, c);
     }
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s1 = 0.0f, s2 = 0.0f;
@@ -288,13 +440,8 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
       sums[flip][1][t >> 6] = s2;
     }
     __syncthreads();
-    s1 = s2 = 0.0f;
-    for (int i = 0; i < waves; ++i) {
-      s1 += sums[flip][0][i];
-      s2 += sums[flip][1][i];
-    }
-    s1 *= inv_c;
-    s2 *= inv_c;
+    s1 = row16_sum((t & 15) < waves ? sums[flip][0][t & 15] : 0.0f) * inv_c;
+    s2 = row16_sum((t & 15) < waves ? sums[flip][1][t & 15] : 0.0f) * inv_c;
     T* o = reinterpret_cast<T*>(a.dx) + row * a.lddx;
 #pragma unroll
     for (int n = 0; n < kRuns; ++n) {
@@ -305,7 +452,7 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
         const float xhat = (xr[n].get(i) - mean) * rstd;
         v[i] = (dr[n].get(i) * w[n][i] - s1 - xhat * s2) * rstd;
       }
-      store_run8(o + col, c - col, a.dx_vec, v);
+      store_run8<kVec>(o + col, c - col, v);
     }
   }
   if constexpr (kSums) {
@@ -349,26 +496,36 @@ __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(const float* __r
   }
 }
 
-template <typename T, int kOut>
+template <typename T, int kOut, bool kVec>
 static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
-  const int cols = kOut == kOutFp8 ? a.kp : (a.c + 15) / 16 * 16;
-  const unsigned wave_grid = (unsigned)std::min<int64_t>((a.rows + 3) / 4, 256 * 32);
-  const unsigned row_grid = (unsigned)std::min<int64_t>(a.rows, 256 * 32);
-#define HIF4_NORM(P, items)                                                               \
-  hipLaunchKernelGGL((layer_norm_kernel<T, P, items, kOut>), dim3(P > 64 ? row_grid : wave_grid), \
-                     dim3(P > 64 ? P : 256), 0, stream, a)
-  const bool wide = sizeof(T) == 4;
-  if (cols <= 64 * 16) HIF4_NORM(64, 1);
-  else if (cols <= 64 * 16 * 2) HIF4_NORM(64, 2);
-  else if (!wide && cols <= 64 * 16 * 5) HIF4_NORM(64, 5);
-  else if (cols <= 256 * 16 * 2) HIF4_NORM(256, 2);
-  else if (cols <= 256 * 16 * 4) HIF4_NORM(256, 4);
-  else HIF4_NORM(1024, 4);
+  const int items = kOut == kOutFp8 ? a.kp / 16 : (a.c + 15) / 16;
+  if (items > 1024) {
+    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 256 * 32);
+    hipLaunchKernelGGL((layer_norm_kernel<T, 1024, 4, kOut, kVec>), dim3(grid), dim3(1024), 0, stream, a);
+    return hipGetLastError();
+  }
+  const int waves = (items + 63) / 64;
+  // rows at once (fp32 rows fill twice the registers, element loads twice again)
+  constexpr int kMany = !kVec ? 1 : sizeof(T) == 2 ? 4 : 2;
+  const bool many = a.rows >= 256 * 8 * 4;
+  const int r = many ? kMany : 1;
+  const unsigned grid =
+      (unsigned)std::min<int64_t>((a.rows + r - 1) / r, (int64_t)256 * NORM_WG / waves);
+#define HIF4_NORM(rr, multi)                                                              \
+  hipLaunchKernelGGL((layer_norm_rows_kernel<T, rr, kOut, multi, kVec>), dim3(grid), dim3(64 * waves), 0, \
+                     stream, a)
+  if (many) {
+    if (waves > 1) HIF4_NORM(kMany, true);
+    else HIF4_NORM(kMany, false);
+  } else {
+    if (waves > 1) HIF4_NORM(1, true);
+    else HIF4_NORM(1, false);
+  }
 #undef HIF4_NORM
   return hipGetLastError();
 }
 
-template <typename T>
+template <typename T, bool kVec>
 static hipError_t launch_norm_backward(const NormBackArgs& a, int grid, hipStream_t stream) {
   const int runs = (a.c + 7) / 8;
   const int per = (runs + 1023) / 1024 <= 1 ? (runs > 512 ? 2 : 1) : (runs + 1023) / 1024;
@@ -377,10 +534,10 @@ static hipError_t launch_norm_backward(const NormBackArgs& a, int grid, hipStrea
 #define HIF4_BACK(k)                                                                               \
   do {                                                                                             \
     if (a.parts)                                                                                   \
-      hipLaunchKernelGGL((layer_norm_backward_kernel<T, k, true>), dim3(grid), dim3(threads), 0,   \
+      hipLaunchKernelGGL((layer_norm_backward_kernel<T, k, true, kVec>), dim3(grid), dim3(threads), 0,   \
                          stream, a);                                                               \
     else                                                                                           \
-      hipLaunchKernelGGL((layer_norm_backward_kernel<T, k, false>), dim3(grid), dim3(threads), 0,  \
+      hipLaunchKernelGGL((layer_norm_backward_kernel<T, k, false, kVec>), dim3(grid), dim3(threads), 0,  \
                          stream, a);                                                               \
   } while (0)
   switch (kr) {
@@ -398,15 +555,18 @@ static hipError_t launch_norm_backward(const NormBackArgs& a, int grid, hipStrea
 using namespace hif4;
 
 hipError_t hif4_launch_layer_norm(const NormArgs& a, bool x_bf16, int out, hipStream_t stream) {
+  const auto go = [&](auto type, auto kind) {
+    using T = decltype(type);
+    constexpr int kOut = decltype(kind)::value;
+    return a.vec ? launch_norm<T, kOut, true>(a, stream) : launch_norm<T, kOut, false>(a, stream);
+  };
+  const auto by_type = [&](auto kind) {
+    return x_bf16 ? go(uint16_t{}, kind) : go(float{}, kind);
+  };
   switch (out) {
-    case kOutY:
-      return x_bf16 ? launch_norm<uint16_t, kOutY>(a, stream) : launch_norm<float, kOutY>(a, stream);
-    case kOutHif4:
-      return x_bf16 ? launch_norm<uint16_t, kOutHif4>(a, stream)
-                    : launch_norm<float, kOutHif4>(a, stream);
-    default:
-      return x_bf16 ? launch_norm<uint16_t, kOutFp8>(a, stream)
-                    : launch_norm<float, kOutFp8>(a, stream);
+    case kOutY: return by_type(std::integral_constant<int, kOutY>{});
+    case kOutHif4: return by_type(std::integral_constant<int, kOutHif4>{});
+    default: return by_type(std::integral_constant<int, kOutFp8>{});
   }
 }
 
@@ -418,8 +578,13 @@ int hif4_layer_norm_backward_parts(int64_t rows) {
 hipError_t hif4_launch_layer_norm_backward(const NormBackArgs& a, bool x_bf16, void* dw, void* db,
                                            hipStream_t stream) {
   const int grid = hif4_layer_norm_backward_parts(a.rows);
-  hipError_t e = x_bf16 ? launch_norm_backward<uint16_t>(a, grid, stream)
-                        : launch_norm_backward<float>(a, grid, stream);
+  hipError_t e;
+  if (a.vec)
+    e = x_bf16 ? launch_norm_backward<uint16_t, true>(a, grid, stream)
+               : launch_norm_backward<float, true>(a, grid, stream);
+  else
+    e = x_bf16 ? launch_norm_backward<uint16_t, false>(a, grid, stream)
+               : launch_norm_backward<float, false>(a, grid, stream);
   if (e != hipSuccess || !a.parts) return e;
   hipLaunchKernelGGL(layer_norm_parts_kernel, dim3((unsigned)((2 * (int64_t)a.c + 63) / 64)),
                      dim3(1024), 0, stream, a.parts, grid, a.c, dw, db, a.w_bf16);

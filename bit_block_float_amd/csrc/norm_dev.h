@@ -11,13 +11,12 @@ struct NormArgs {
   const void* x;
   int64_t rows, ld;
   int c;
-  bool vec;  // every row of x is 16-byte aligned
+  bool vec;  // c % 8 == 0, and every row of x, y, weight and bias is 16-byte aligned
   const void *w, *b;
-  bool w_bf16, w_vec;
+  bool w_bf16;
   float eps;
   void* y;  // plain output, of x's type
   int64_t ldy;
-  bool y_vec;
   float *mean, *rstd;  // either may be NULL
   uint8_t* codes;      // HiF4 [rows][c/2] or E4M3 [rows][kp]
   uint32_t* meta;      // HiF4
@@ -33,9 +32,9 @@ struct NormBackArgs {
   const void *dy, *x;
   int64_t rows, lddy, ldx, lddx;
   int c;
-  bool vec, dx_vec;
+  bool vec;  // as above, for x, dy, dx and weight
   const void* w;
-  bool w_bf16, w_vec;
+  bool w_bf16;
   const float *mean, *rstd;
   void* dx;
   float* parts;  // NULL: no weight or bias gradient
