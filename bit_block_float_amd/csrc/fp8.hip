@@ -37,17 +37,9 @@ __global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(
   Run8<T> r0, r1;
   r0.template load<kVec>(src, (int)j * 16, k);
   r1.template load<kVec>(src, (int)j * 16 + 8, k);
-  uint32_t am = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) am = max(am, max(abs_bits(r0.get(i)), abs_bits(r1.get(i))));
-  const uint32_t e = e8m0_of(max8_u32(am));
-  const float inv = e8m0_inv(min(e, 254u));
-  uint4 w;
-  w.x = encode4(r0.get(0), r0.get(1), r0.get(2), r0.get(3), inv);
-  w.y = encode4(r0.get(4), r0.get(5), r0.get(6), r0.get(7), inv);
-  w.z = encode4(r1.get(0), r1.get(1), r1.get(2), r1.get(3), inv);
-  w.w = encode4(r1.get(4), r1.get(5), r1.get(6), r1.get(7), inv);
-  if (e == 255u) w = make_uint4(kFp8NaN4, kFp8NaN4, kFp8NaN4, kFp8NaN4);
+  const uint32_t e = e8m0_of(max8_u32(max(r0.abs_max(), r1.abs_max())));
+  const uint2 c0 = r0.encode(e), c1 = r1.encode(e);
+  const uint4 w = make_uint4(c0.x, c0.y, c1.x, c1.y);
   codes[it] = w;
   if ((j & 7u) == 0u) scales[(int64_t)row * lds + (j >> 3)] = (uint8_t)e;
 }
@@ -83,9 +75,7 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
   if constexpr (kTile) {
     uint32_t am = 0;
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) am = max(am, abs_bits(v[r].get(i)));
+    for (int r = 0; r < 8; ++r) am = max(am, v[r].abs_max());
     am = max16_u32(am);
     am = max(am, (uint32_t)__shfl_xor((int)am, 16, 64));
     am = max(am, (uint32_t)__shfl_xor((int)am, 32, 64));
@@ -93,11 +83,11 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
     __syncthreads();
     e_tile = e8m0_of(max(max(part[0][0], part[1][0]), max(part[2][0], part[3][0])));
   } else if constexpr (kCols) {
+    uint32_t cm[8];
+    column_max(v, cm);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t am = 0;
-#pragma unroll
-      for (int r = 0; r < 8; ++r) am = max(am, abs_bits(v[r].get(i)));
+      uint32_t am = cm[i];
       am = max(am, (uint32_t)__shfl_xor((int)am, 16, 64));
       am = max(am, (uint32_t)__shfl_xor((int)am, 32, 64));
       if (lane < 16) part[wave][cg * 8 + i] = am;
@@ -114,16 +104,8 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       uint32_t e = e_tile;
-      if constexpr (!kTile) {
-        uint32_t am = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) am = max(am, abs_bits(v[r].get(i)));
-        e = e8m0_of(max16_u32(am));
-      }
-      const float inv = e8m0_inv(min(e, 254u));
-      uint2 w = make_uint2(encode4(v[r].get(0), v[r].get(1), v[r].get(2), v[r].get(3), inv),
-                           encode4(v[r].get(4), v[r].get(5), v[r].get(6), v[r].get(7), inv));
-      if (e == 255u) w = make_uint2(kFp8NaN4, kFp8NaN4);
+      if constexpr (!kTile) e = e8m0_of(max16_u32(v[r].abs_max()));
+      const uint2 w = v[r].encode(e);
       if (row0 + r < rows) {
         *reinterpret_cast<uint2*>(codes + (row0 + r) * kp + col0) = w;
         if (!kTile && cg == 0) scales[(row0 + r) * lds + tk] = (uint8_t)e;
@@ -135,10 +117,7 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t e = kTile ? e_tile : e_col[i];
-      const float inv = e8m0_inv(min(e, 254u));
-      uint2 w = make_uint2(encode4(v[0].get(i), v[1].get(i), v[2].get(i), v[3].get(i), inv),
-                           encode4(v[4].get(i), v[5].get(i), v[6].get(i), v[7].get(i), inv));
-      if (e == 255u) w = make_uint2(kFp8NaN4, kFp8NaN4);
+      const uint2 w = encode_column(v, i, e);
       *reinterpret_cast<uint2*>(tile + (cg * 8 + i) * kPitch + rg * 8) = w;
       if (!kTile && rg == 0 && col0 + i < k)
         scales_t[(int64_t)(col0 + i) * lds_t + tr] = (uint8_t)e;

@@ -35,6 +35,25 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
 }
 constexpr uint32_t kFp8NaN4 = 0x7F7F7F7Fu;  // four E4M3 NaNs
 
+// Four codes of two words of bf16 pairs: RNE(x / scale) by the scaled conversion
+// (checked on every bf16 value against the rule over E8M0's range).
+__device__ __forceinline__ uint32_t encode4_bf16(uint32_t lo, uint32_t hi, float scale) {
+  typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+  typedef short half2_t __attribute__((ext_vector_type(2)));
+  half2_t r = {0, 0};
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(pair_t, lo), scale, false);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(pair_t, hi), scale, true);
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// Per-half maximum of two words of u16 pairs; with the sign bits cleared, bf16
+// magnitudes order as integers (NaNs above infinity).
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+  typedef unsigned short u16_pair_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16_pair_t, a),
+                                                                __builtin_bit_cast(u16_pair_t, b)));
+}
+
 // 8 consecutive elements of a row of c >= 1, from column col; elements at or past
 // c are zero. The loads are unconditional, from clamped addresses (a load behind
 // a branch is waited for at the branch's end, one after the other). kVec: rows
@@ -70,6 +89,18 @@ struct Run8<uint16_t> {
   __device__ __forceinline__ void opaque() {
     asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
   }
+  // the largest magnitude, as fp32 bits
+  __device__ __forceinline__ uint32_t abs_max() const {
+    const uint32_t m = pair_max(pair_max(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                pair_max(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+  // the 8 codes under the scale byte e (all NaN for 255)
+  __device__ __forceinline__ uint2 encode(uint32_t e) const {
+    const float s = e8m0_f32(e);
+    const uint2 r = make_uint2(encode4_bf16(w.x, w.y, s), encode4_bf16(w.z, w.w, s));
+    return e == 255u ? make_uint2(kFp8NaN4, kFp8NaN4) : r;
+  }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t u = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
     return (i & 1) ? bf16hi_to_f32(u) : bf16lo_to_f32(u);
@@ -98,8 +129,62 @@ struct Run8<float> {
     for (int i = 0; i < 8; ++i) v[i] = ok ? v[i] : 0.0f;
   }
   __device__ __forceinline__ void opaque() {}
+  __device__ __forceinline__ uint32_t abs_max() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
+  }
+  __device__ __forceinline__ uint2 encode(uint32_t e) const {
+    const float inv = e8m0_inv(min(e, 254u));
+    const uint2 r = make_uint2(encode4(v[0], v[1], v[2], v[3], inv),
+                               encode4(v[4], v[5], v[6], v[7], inv));
+    return e == 255u ? make_uint2(kFp8NaN4, kFp8NaN4) : r;
+  }
   __device__ __forceinline__ float get(int i) const { return v[i]; }
 };
+
+// Columns of 8 runs (8 rows x 8 columns): the largest magnitude of each column as
+// fp32 bits, and the 8 codes of column i.
+__device__ __forceinline__ void column_max(const Run8<uint16_t> (&v)[8], uint32_t (&m)[8]) {
+  uint32_t p[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    p[0] = pair_max(p[0], v[r].w.x & 0x7FFF7FFFu);
+    p[1] = pair_max(p[1], v[r].w.y & 0x7FFF7FFFu);
+    p[2] = pair_max(p[2], v[r].w.z & 0x7FFF7FFFu);
+    p[3] = pair_max(p[3], v[r].w.w & 0x7FFF7FFFu);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = (i & 1) ? p[i >> 1] & 0xFFFF0000u : p[i >> 1] << 16;
+}
+__device__ __forceinline__ void column_max(const Run8<float> (&v)[8], uint32_t (&m)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m[i] = 0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) m[i] = max(m[i], __float_as_uint(v[r].v[i]) & 0x7FFFFFFFu);
+  }
+}
+__device__ __forceinline__ uint2 encode_column(const Run8<uint16_t> (&v)[8], int i, uint32_t e) {
+  const float s = e8m0_f32(e);
+  uint32_t p[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {  // rows 2q, 2q + 1 of the column as one word
+    const uint4 &a = v[2 * q].w, &b = v[2 * q + 1].w;
+    const uint32_t x = i < 2 ? a.x : i < 4 ? a.y : i < 6 ? a.z : a.w;
+    const uint32_t y = i < 2 ? b.x : i < 4 ? b.y : i < 6 ? b.z : b.w;
+    p[q] = __builtin_amdgcn_perm(y, x, (i & 1) ? 0x07060302u : 0x05040100u);
+  }
+  const uint2 r = make_uint2(encode4_bf16(p[0], p[1], s), encode4_bf16(p[2], p[3], s));
+  return e == 255u ? make_uint2(kFp8NaN4, kFp8NaN4) : r;
+}
+__device__ __forceinline__ uint2 encode_column(const Run8<float> (&v)[8], int i, uint32_t e) {
+  const float inv = e8m0_inv(min(e, 254u));
+  const uint2 r = make_uint2(encode4(v[0].v[i], v[1].v[i], v[2].v[i], v[3].v[i], inv),
+                             encode4(v[4].v[i], v[5].v[i], v[6].v[i], v[7].v[i], inv));
+  return e == 255u ? make_uint2(kFp8NaN4, kFp8NaN4) : r;
+}
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 

@@ -18,6 +18,9 @@
 
 namespace hif4 {
 
+#ifndef NQR
+#define NQR 2
+#endif
 #ifndef NORM_WG
 #define NORM_WG 64
 #endif
@@ -77,13 +80,19 @@ __device__ __forceinline__ void load_w8(const void* w, bool w_bf16, int col, int
   }
 }
 
+// 8 values rounded to bf16.
+__device__ __forceinline__ Run8<uint16_t> pack8(const float (&v)[8]) {
+  Run8<uint16_t> r;
+  r.w = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
+                   f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+  return r;
+}
+
 template <bool kVec>
 __device__ __forceinline__ void store_run8(uint16_t* p, int valid, const float (&v)[8]) {
   if constexpr (kVec) {
     if (valid <= 0) return;
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
-                   f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+    *reinterpret_cast<uint4*>(p) = pack8(v).w;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -113,14 +122,7 @@ __device__ __forceinline__ void store_item(const NormArgs& a, float (&y)[2][8], 
     store_run8<kVec>(dst, c - col, y[0]);
     store_run8<kVec>(dst + 8, c - col - 8, y[1]);
   } else if constexpr (kOut == kOutHif4) {
-    uint32_t wds[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float lo = y[i >> 2][2 * (i & 3)], hi = y[i >> 2][2 * (i & 3) + 1];
-      wds[i] = f32x2_to_bf16x2(lo, hi);
-    }
-    uint4 v0 = make_uint4(wds[0], wds[1], wds[2], wds[3]);
-    uint4 v1 = make_uint4(wds[4], wds[5], wds[6], wds[7]);
+    uint4 v0 = pack8(y[0]).w, v1 = pack8(y[1]).w;
     if (a.mask) {
       keep_item_values(v0, v1, info, row, a.kept, a.n_mask);
       uint32_t z[8];
@@ -135,23 +137,24 @@ __device__ __forceinline__ void store_item(const NormArgs& a, float (&y)[2][8], 
     quantize_item(v0, v1, (uint32_t)j, (uint32_t)j,
                   reinterpret_cast<uint32_t*>(a.codes + row * (c / 2)), a.meta + row * (c / 64));
   } else {
-    uint32_t am = 0;
+    Run8<T> r[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (!kVec) {  // the padding of the last block (whole runs: below)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (sizeof(T) == 2) y[h][i] = bf16lo_to_f32(f32_to_bf16(y[h][i]));
-        if (col + 8 * h + i >= c) y[h][i] = 0.0f;  // the padding of the last block
-        am = max(am, abs_bits(y[h][i]));
+        for (int i = 0; i < 8; ++i) y[h][i] = col + 8 * h + i < c ? y[h][i] : 0.0f;
       }
-    const uint32_t e = e8m0_of(max8_u32(am));
-    const float inv = e8m0_inv(min(e, 254u));
-    uint4 w = make_uint4(encode4(y[0][0], y[0][1], y[0][2], y[0][3], inv),
-                         encode4(y[0][4], y[0][5], y[0][6], y[0][7], inv),
-                         encode4(y[1][0], y[1][1], y[1][2], y[1][3], inv),
-                         encode4(y[1][4], y[1][5], y[1][6], y[1][7], inv));
-    if (e == 255u) w = make_uint4(kFp8NaN4, kFp8NaN4, kFp8NaN4, kFp8NaN4);
-    *reinterpret_cast<uint4*>(a.codes + row * a.kp + col) = w;
+      if constexpr (sizeof(T) == 2) {
+        r[h] = pack8(y[h]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[h].v[i] = y[h][i];
+      }
+      if constexpr (kVec) r[h].keep_if(col + 8 * h < c);
+    }
+    const uint32_t e = e8m0_of(max8_u32(max(r[0].abs_max(), r[1].abs_max())));
+    const uint2 c0 = r[0].encode(e), c1 = r[1].encode(e);
+    *reinterpret_cast<uint4*>(a.codes + row * a.kp + col) = make_uint4(c0.x, c0.y, c1.x, c1.y);
     if ((j & 7) == 0) a.scales[row * a.lds + (j >> 3)] = (uint8_t)e;
   }
 }
@@ -354,15 +357,16 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
       mean[r] /= fc;
       x0[r].opaque();
       x1[r].opaque();
-      float q = 0.0f;
+      float q0 = 0.0f, q1 = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d0 = col + i < c ? x0[r].get(i) - mean[r] : 0.0f;
-        const float d1 = col + 8 + i < c ? x1[r].get(i) - mean[r] : 0.0f;
-        q = fmaf(d0, d0, q);
-        q = fmaf(d1, d1, q);
+        const float d0 = kVec || col + i < c ? x0[r].get(i) - mean[r] : 0.0f;
+        const float d1 = kVec || col + 8 + i < c ? x1[r].get(i) - mean[r] : 0.0f;
+        q0 = fmaf(d0, d0, q0);
+        q1 = fmaf(d1, d1, q1);
       }
-      rstd[r] = q;
+      // kVec: a run is whole or empty
+      rstd[r] = (!kVec || col < c ? q0 : 0.0f) + (!kVec || col + 8 < c ? q1 : 0.0f);
     }
     row_sums(rstd, 1);
 #pragma unroll
@@ -506,7 +510,7 @@ static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   }
   const int waves = (items + 63) / 64;
   // rows at once (fp32 rows fill twice the registers, element loads twice again)
-  constexpr int kMany = !kVec ? 1 : sizeof(T) == 2 ? 4 : 2;
+  constexpr int kMany = !kVec ? 1 : sizeof(T) == 2 ? (kOut == kOutY ? 4 : NQR) : 2;
   const bool many = a.rows >= 256 * 8 * 4;
   const int r = many ? kMany : 1;
   const unsigned grid =
