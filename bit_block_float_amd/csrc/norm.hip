@@ -18,11 +18,8 @@
 
 namespace hif4 {
 
-#ifndef NQR
-#define NQR 2
-#endif
-#ifndef NORM_WG
-#define NORM_WG 64
+#ifndef WWG
+#define WWG 3
 #endif
 enum NormOut { kOutY = 0, kOutHif4 = 1, kOutFp8 = 2 };
 
@@ -45,19 +42,13 @@ __device__ __forceinline__ float wave_sum(float v) {
   return f(p[0]) + f(p[1]);
 }
 
-// Sum over the P threads that share a row (P = 64: one wave; else the whole
-// workgroup). `slot` is LDS of P / 64 floats that no other sum in flight uses.
-template <int P>
+// Sum over a workgroup of 1024 threads. `slot` is LDS of 16 floats that no other
+// sum in flight uses.
 __device__ __forceinline__ float row_sum(float v, float* slot) {
   v = wave_sum(v);
-  if constexpr (P > 64) {
-    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < P / 64; ++i) v += slot[i];
-  }
-  return v;
+  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return row16_sum(slot[threadIdx.x & 15]);
 }
 
 // 8 weights or biases from column `col` (fp32 or bf16), 1 / 0 without one.
@@ -159,16 +150,141 @@ __device__ __forceinline__ void store_item(const NormArgs& a, float (&y)[2][8], 
   }
 }
 
-// Forward. P threads share a row; a lane owns items (16 consecutive elements)
-// t, t + P, ..., the quantizers' own mapping, so 4 aligned lanes hold a HiF4
+// 16 mask bytes as bits, and the inclusive sum over the lanes up to this one.
+__device__ __forceinline__ uint32_t mask_bits(const uint8_t* p) {
+  const uint4 mk = *reinterpret_cast<const uint4*>(p);
+  return nonzero_bytes(mk.x) | (nonzero_bytes(mk.y) << 4) | (nonzero_bytes(mk.z) << 8) |
+         (nonzero_bytes(mk.w) << 12);
+}
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_up((int)v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Sum of up to 16 values in the order of row16_sum over lanes 0, 1, ...
+template <int N>
+__device__ __forceinline__ float tree_sum(const float (&v)[N]) {
+  float t[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t[i] = i < N ? v[i] : 0.0f;
+  const float a = (t[0] + t[1]) + (t[2] + t[3]), b = (t[4] + t[5]) + (t[6] + t[7]);
+  const float c = (t[8] + t[9]) + (t[10] + t[11]), d = (t[12] + t[13]) + (t[14] + t[15]);
+  return (a + b) + (c + d);
+}
+
+// Forward that ends in a quantizer, bf16 rows of up to 8192 columns, many of them.
+// A wave owns a row (its lanes items n * 64 + lane), so nothing in the row loop
+// waits for another wave: the encoders need too many registers for the kernel
+// below to hide its barriers and loads behind other rows. Weight and bias are in
+// LDS as fp32 ([weight, bias][quarter of an item][item] 16-byte pieces, which
+// consecutive lanes read without bank conflicts). The sums are taken in the order
+// of the kernel below: a tree over the lanes for each run of 64 items, then a
+// tree over the runs, so the results are the same bits.
+template <int kItems, int kOut>
+__global__ __launch_bounds__(512) void layer_norm_wave_kernel(NormArgs a) {
+  extern __shared__ float4 affine[];
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int c = a.c;
+  const int items = kOut == kOutFp8 ? a.kp / 16 : (c + 15) / 16;
+  for (int j = threadIdx.x; j < items; j += blockDim.x) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float w[8], b[8];
+      load_w8<true>(a.w, a.w_bf16, j * 16 + 8 * h, c, 1.0f, w);
+      load_w8<true>(a.b, a.w_bf16, j * 16 + 8 * h, c, 0.0f, b);
+      affine[(2 * h) * items + j] = make_float4(w[0], w[1], w[2], w[3]);
+      affine[(2 * h + 1) * items + j] = make_float4(w[4], w[5], w[6], w[7]);
+      affine[(4 + 2 * h) * items + j] = make_float4(b[0], b[1], b[2], b[3]);
+      affine[(5 + 2 * h) * items + j] = make_float4(b[4], b[5], b[6], b[7]);
+    }
+  }
+  uint32_t info[kItems] = {};
+  if (kOut == kOutHif4 && a.mask) {
+    uint32_t run = 0;
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      const int j = n * 64 + lane;
+      const uint32_t m16 = j < items ? mask_bits(a.mask + (size_t)j * 16) : 0u;
+      const uint32_t incl = wave_prefix(__popc(m16), lane);
+      info[n] = (m16 << 16) | ((run + incl - __popc(m16)) & 0xFFFFu);
+      run += (uint32_t)__shfl((int)incl, 63, 64);
+    }
+  }
+  __syncthreads();
+
+  const float fc = (float)c, inv_c = 1.0f / (float)c;
+  const int64_t step = (int64_t)gridDim.x * waves;
+  for (int64_t row = (int64_t)blockIdx.x * waves + (threadIdx.x >> 6); row < a.rows; row += step) {
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.x) + row * a.ld;
+    Run8<uint16_t> r[kItems][2];
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      r[n][0].template load<true>(src, (n * 64 + lane) * 16, c);
+      r[n][1].template load<true>(src, (n * 64 + lane) * 16 + 8, c);
+    }
+    float part[kItems];
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      part[n] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[n] += r[n][0].get(i) + r[n][1].get(i);
+      part[n] = wave_sum(part[n]);
+    }
+    const float mean = tree_sum<kItems>(part) / fc;
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      float q[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        r[n][h].opaque();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float d = r[n][h].get(i) - mean;
+          q[h] = fmaf(d, d, q[h]);
+        }
+      }
+      const int col = (n * 64 + lane) * 16;
+      part[n] = wave_sum((col < c ? q[0] : 0.0f) + (col + 8 < c ? q[1] : 0.0f));
+    }
+    const float rstd = 1.0f / sqrtf(tree_sum<kItems>(part) * inv_c + a.eps);
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      const int j = n * 64 + lane;
+      if (j >= items) continue;  // whole quads / octets of lanes
+      float y[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        r[n][h].opaque();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 w = affine[(2 * h + e) * items + j], b = affine[(4 + 2 * h + e) * items + j];
+          const float* pw = &w.x;
+          const float* pb = &b.x;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[h][4 * e + i] = fmaf((r[n][h].get(4 * e + i) - mean) * rstd, pw[i], pb[i]);
+        }
+      }
+      store_item<uint16_t, kOut, true>(a, y, row, j, c, info[n]);
+    }
+  }
+}
+
+// Forward of the widest rows (over 16384 columns): 1024 threads share a row, a
+// lane owns items (16 consecutive elements) t, t + 1024, ..., the quantizers' own
+// mapping, so 4 aligned lanes hold a HiF4
 // unit and 8 an E4M3 block when the row leaves through one of them. The value
 // quantized is the one kOutY would store (rounded to bf16 for HiF4, to x's type
 // for E4M3), so the codes are those of the two calls in turn.
-template <typename T, int P, int kItems, int kOut, bool kVec>
-__global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a) {
-  constexpr int kRowsPerBlock = P > 64 ? 1 : 4;
+template <typename T, int kItems, int kOut, bool kVec>
+__global__ __launch_bounds__(1024) void layer_norm_wide_kernel(NormArgs a) {
+  constexpr int P = 1024;
   __shared__ float slots[2][P / 64];
-  const int t = P > 64 ? threadIdx.x : (threadIdx.x & 63);
+  const int t = threadIdx.x;
   const int c = a.c;
   const int items = kOut == kOutFp8 ? a.kp / 16 : (c + 15) / 16;
   const T* x = reinterpret_cast<const T*>(a.x);
@@ -183,30 +299,16 @@ __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a
 #pragma unroll
       for (int n = 0; n < kItems; ++n) {
         const int j = n * P + t;
-        uint32_t m16 = 0;
-        if (j < items) {
-          const uint4 mk = *reinterpret_cast<const uint4*>(a.mask + (size_t)j * 16);
-          m16 = nonzero_bytes(mk.x) | (nonzero_bytes(mk.y) << 4) | (nonzero_bytes(mk.z) << 8) |
-                (nonzero_bytes(mk.w) << 12);
+        const uint32_t m16 = j < items ? mask_bits(a.mask + (size_t)j * 16) : 0u;
+        const uint32_t cnt = __popc(m16), incl = wave_prefix(cnt, t & 63);
+        if ((t & 63) == 63) part[t >> 6] = incl;
+        __syncthreads();
+        uint32_t base = run, total = 0;
+        for (int w = 0; w < P / 64; ++w) {
+          if (w < (t >> 6)) base += part[w];
+          total += part[w];
         }
-        const uint32_t cnt = __popc(m16);
-        uint32_t incl = cnt;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const uint32_t o = (uint32_t)__shfl_up((int)incl, d, 64);
-          if ((t & 63) >= d) incl += o;
-        }
-        uint32_t base = run, total = (uint32_t)__shfl((int)incl, 63, 64);
-        if constexpr (P > 64) {
-          if ((t & 63) == 63) part[t >> 6] = incl;
-          __syncthreads();
-          total = 0;
-          for (int w = 0; w < P / 64; ++w) {
-            if (w < (t >> 6)) base += part[w];
-            total += part[w];
-          }
-          __syncthreads();
-        }
+        __syncthreads();
         info[n] = (m16 << 16) | ((base + incl - cnt) & 0xFFFFu);
         run += total;
       }
@@ -214,9 +316,7 @@ __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a
   }
 
   const float inv_c = 1.0f / (float)c;
-  const int64_t step = (int64_t)gridDim.x * kRowsPerBlock;
-  for (int64_t row = (int64_t)blockIdx.x * kRowsPerBlock + (P > 64 ? 0 : threadIdx.x >> 6);
-       row < a.rows; row += step) {
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* src = x + row * a.ld;
     Run8<T> r0[kItems], r1[kItems];
 #pragma unroll
@@ -230,7 +330,7 @@ __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a
     for (int n = 0; n < kItems; ++n)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += r0[n].get(i) + r1[n].get(i);
-    const float mean = row_sum<P>(s, slots[0]) / (float)c;
+    const float mean = row_sum(s, slots[0]) / (float)c;
     float q = 0.0f;
 #pragma unroll
     for (int n = 0; n < kItems; ++n) {
@@ -243,7 +343,7 @@ __global__ __launch_bounds__(P > 64 ? P : 256) void layer_norm_kernel(NormArgs a
         q = fmaf(d1, d1, q);
       }
     }
-    const float var = row_sum<P>(q, slots[1]) * inv_c;
+    const float var = row_sum(q, slots[1]) * inv_c;
     const float rstd = 1.0f / sqrtf(var + a.eps);
     if (kOut == kOutY && t == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -287,19 +387,8 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
   if constexpr (kOut == kOutHif4) {
     if (a.mask) {
       __shared__ uint32_t part[16];
-      uint32_t m16 = 0;
-      if (live) {
-        const uint4 mk = *reinterpret_cast<const uint4*>(a.mask + col);
-        m16 = nonzero_bytes(mk.x) | (nonzero_bytes(mk.y) << 4) | (nonzero_bytes(mk.z) << 8) |
-              (nonzero_bytes(mk.w) << 12);
-      }
-      const uint32_t cnt = __popc(m16);
-      uint32_t incl = cnt;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_up((int)incl, d, 64);
-        if (lane >= d) incl += o;
-      }
+      const uint32_t m16 = live ? mask_bits(a.mask + col) : 0u;
+      const uint32_t cnt = __popc(m16), incl = wave_prefix(cnt, lane);
       uint32_t base = incl - cnt;
       if constexpr (kMulti) {
         if (lane == 63) part[wave] = incl;
@@ -334,39 +423,45 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
   };
 
   const float fc = (float)c, inv_c = 1.0f / (float)c;
-  for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < a.rows; row0 += (int64_t)gridDim.x * R) {
-    Run8<T> x0[R], x1[R];
+  const int64_t step = (int64_t)gridDim.x * R;
+  // rows past the end read the last one again and are not stored
+  Run8<T> n0[R], n1[R];
+  auto load_rows = [&](int64_t row0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      // rows past the end read the last one again and are not stored
-      const int64_t row = min(row0 + r, a.rows - 1);
-      const T* src = reinterpret_cast<const T*>(a.x) + row * a.ld;
-      x0[r].template load<kVec>(src, col, c);
-      x1[r].template load<kVec>(src, col + 8, c);
+      const T* src = reinterpret_cast<const T*>(a.x) + min(row0 + r, a.rows - 1) * a.ld;
+      n0[r].template load<kVec>(src, col, c);
+      n1[r].template load<kVec>(src, col + 8, c);
     }
-    float mean[R], rstd[R];
+  };
+  for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < a.rows; row0 += step) {
+    load_rows(row0);
+    float x[R][2][8], mean[R], rstd[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mean[r] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mean[r] += x0[r].get(i) + x1[r].get(i);
+      for (int i = 0; i < 8; ++i) {
+        x[r][0][i] = n0[r].get(i);
+        x[r][1][i] = n1[r].get(i);
+        mean[r] += x[r][0][i] + x[r][1][i];
+      }
     }
     row_sums(mean, 0);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mean[r] /= fc;
-      x0[r].opaque();
-      x1[r].opaque();
-      float q0 = 0.0f, q1 = 0.0f;
+      float q[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d0 = kVec || col + i < c ? x0[r].get(i) - mean[r] : 0.0f;
-        const float d1 = kVec || col + 8 + i < c ? x1[r].get(i) - mean[r] : 0.0f;
-        q0 = fmaf(d0, d0, q0);
-        q1 = fmaf(d1, d1, q1);
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[r][h][i] -= mean[r];
+          const float d = kVec || col + 8 * h + i < c ? x[r][h][i] : 0.0f;
+          q[h] = fmaf(d, d, q[h]);
+        }
       // kVec: a run is whole or empty
-      rstd[r] = (!kVec || col < c ? q0 : 0.0f) + (!kVec || col + 8 < c ? q1 : 0.0f);
+      rstd[r] = (!kVec || col < c ? q[0] : 0.0f) + (!kVec || col + 8 < c ? q[1] : 0.0f);
     }
     row_sums(rstd, 1);
 #pragma unroll
@@ -380,15 +475,11 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
         if (a.rstd) a.rstd[row] = rstd[r];
       }
       if (!live) continue;  // whole quads / octets of lanes: items is a multiple of 4 / 8
-      x0[r].opaque();
-      x1[r].opaque();
-      float y[2][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[0][i] = fmaf((x0[r].get(i) - mean[r]) * rstd[r], w[0][i], b[0][i]);
-        y[1][i] = fmaf((x1[r].get(i) - mean[r]) * rstd[r], w[1][i], b[1][i]);
-      }
-      store_item<T, kOut, kVec>(a, y, row, t, c, info);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[r][h][i] = fmaf(x[r][h][i] * rstd[r], w[h][i], b[h][i]);
+      store_item<T, kOut, kVec>(a, x[r], row, t, c, info);
     }
   }
 }
@@ -505,16 +596,34 @@ static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   const int items = kOut == kOutFp8 ? a.kp / 16 : (a.c + 15) / 16;
   if (items > 1024) {
     const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 256 * 32);
-    hipLaunchKernelGGL((layer_norm_kernel<T, 1024, 4, kOut, kVec>), dim3(grid), dim3(1024), 0, stream, a);
+    hipLaunchKernelGGL((layer_norm_wide_kernel<T, 4, kOut, kVec>), dim3(grid), dim3(1024), 0, stream, a);
     return hipGetLastError();
   }
   const int waves = (items + 63) / 64;
+  if constexpr (sizeof(T) == 2 && kVec && kOut != kOutY) {
+    if (waves > 1 && waves <= 8 && a.rows >= 256 * 8) {
+      const dim3 grid((unsigned)std::min<int64_t>((a.rows + 7) / 8, 256 * WWG)), block(512);
+      const size_t lds = (size_t)items * 8 * sizeof(float4);
+#define HIF4_WAVE(n) \
+  hipLaunchKernelGGL((layer_norm_wave_kernel<n, kOut>), grid, block, lds, stream, a)
+      switch (waves) {
+        case 2: HIF4_WAVE(2); break;
+        case 3: HIF4_WAVE(3); break;
+        case 4: HIF4_WAVE(4); break;
+        case 5: HIF4_WAVE(5); break;
+        case 6: HIF4_WAVE(6); break;
+        default: HIF4_WAVE(8); break;
+      }
+#undef HIF4_WAVE
+      return hipGetLastError();
+    }
+  }
   // rows at once (fp32 rows fill twice the registers, element loads twice again)
-  constexpr int kMany = !kVec ? 1 : sizeof(T) == 2 ? (kOut == kOutY ? 4 : NQR) : 2;
+  constexpr int kMany = !kVec ? 1 : sizeof(T) == 2 ? 4 : 2;
   const bool many = a.rows >= 256 * 8 * 4;
   const int r = many ? kMany : 1;
   const unsigned grid =
-      (unsigned)std::min<int64_t>((a.rows + r - 1) / r, (int64_t)256 * NORM_WG / waves);
+      (unsigned)std::min<int64_t>((a.rows + r - 1) / r, (int64_t)256 * 64 / waves);
 #define HIF4_NORM(rr, multi)                                                              \
   hipLaunchKernelGGL((layer_norm_rows_kernel<T, rr, kOut, multi, kVec>), dim3(grid), dim3(64 * waves), 0, \
                      stream, a)

@@ -149,6 +149,22 @@ def test_fp8_form_is_the_two_calls(hip, c, dtype):
         assert torch.equal(gs.contiguous().view(torch.uint8), ws.contiguous().view(torch.uint8))
 
 
+@pytest.mark.parametrize("c", [1024, 1088, 2048, 3136, 4096, 5120, 6208, 8192, 13824])
+def test_quantizing_forms_are_the_two_calls_over_many_rows(hip, c):
+    rows = 2100 if c > 4096 else 8200
+    x, w, b = _cuda(_x(rows, c, c), *_affine(c, torch.float32))
+    y, _, _ = hip.layer_norm(x, w, b, eps=EPS)
+    mask = torch.zeros(c, dtype=torch.uint8, device="cuda")
+    mask[torch.randperm(c, generator=torch.Generator().manual_seed(c))[:c // 50].cuda()] = 1
+    for got, want in ((hip.layer_norm_quantize(x, w, b, eps=EPS, mask=mask), hip.quantize(y, mask=mask)),
+                      (hip.layer_norm_quantize(x, w, b, eps=EPS)[:2], hip.quantize(y)[:2]),
+                      (hip.layer_norm_quantize_fp8(x, w, b, eps=EPS), hip.quantize_fp8(y))):
+        for g, r in zip(got, want):
+            assert torch.equal(g.contiguous().view(torch.uint8), r.contiguous().view(torch.uint8))
+    pick = torch.tensor([0, 1, 7, 1000, rows - 2, rows - 1])
+    _check_forward(x.cpu()[pick], w.cpu(), b.cpu(), y[pick.cuda()], None, None, HALF[torch.bfloat16])
+
+
 def _check_backward(dy, x, mean, rstd, w, dx, dw, db):
     """mean and rstd are inputs. A row's two means are off by (A + 4) U of the mean
     of absolute terms (xhat and g round, too); dx adds four roundings of its terms.
