@@ -22,6 +22,7 @@
 //
 // The MFMA's first operand is W, so a lane of the result holds one row of Y
 // (its column index) and runs of 4 consecutive columns.
+#include <algorithm>
 #include <type_traits>
 
 #include "fp8_dev.h"
@@ -47,6 +48,15 @@ __device__ __forceinline__ i32x8_t join(gu32x4_t a, gu32x4_t b) {
 
 __device__ __forceinline__ gf32x16_t mfma32(i32x8_t a, i32x8_t b, gf32x16_t c, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, kFmtE4M3, kFmtE4M3, 0, sa, 0, sb);
+}
+
+// This wave's loads but the newest n have landed, its LDS reads are done.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(n == 0 || n == 10 || n == 18, "one asm a count");
+  if constexpr (n == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  if constexpr (n == 10) asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)" ::: "memory");
+  if constexpr (n == 18) asm volatile("s_waitcnt vmcnt(18) lgkmcnt(0)" ::: "memory");
 }
 
 // 8 codes (two words) as bf16 times the power of two `s`.
@@ -165,46 +175,55 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
   tn = __builtin_amdgcn_readfirstlane(in / gsize);
 }
 
-// Tile kernel. BM x BN of Y a workgroup, kWM x kWN waves. A stage is one block
-// of 128 along K: rows of 128 bytes = 8 chunks of 16, chunk c of row r in slot
+// Tile kernel, for products too small for the one below, and for float32 weight
+// scales. BM x BN of Y a workgroup, kWM x kWN waves. A stage is one block of 128
+// along K: rows of 128 bytes = 8 chunks of 16, chunk c of row r in slot
 // c ^ ((r >> 1) & 7), so that the fragment reads of 16 consecutive rows land in
-// distinct bank groups. Stages reach LDS by direct-to-LDS buffer loads, 8 rows
-// an instruction, with the swizzle applied to the global address; rows past M
-// or N fail the buffer's range check and read as zero. The E8M0 bytes come four
-// blocks (a 32-bit word per row) at a time.
-template <int BM, int BN, int kWM, int kWN, bool kF32Scale, bool kBf16>
+// distinct bank groups. kStages of them are in LDS, brought by direct-to-LDS
+// buffer loads, 8 rows an instruction, with the swizzle applied to the global
+// address; rows past M or N fail the buffer's range check and read as zero. With
+// each stage a wave brings one group of 64 scale words (the 4 bytes that hold the
+// block's). Loads past the last block repeat it, into stages that no one reads.
+//
+// blockIdx.y = s: blocks [s per_split, (s + 1) per_split) of K only, the sums to
+// plane s of `Y` as float32 (few tiles and a long K: the parts are added by
+// gemm_fp8_reduce_kernel in order).
+template <int BM, int BN, int kWM, int kWN, int kStages, bool kF32Scale, bool kFp8, bool kBf16>
 __device__ __forceinline__ void gemm_fp8_tile(
     const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
     const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int64_t M,
-    int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n) {
+    int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n, int per_split) {
   constexpr int kWaves = kWM * kWN;
   constexpr int kTM = BM / kWM / 32, kTN = BN / kWN / 32;  // 32 x 32 blocks of a wave
-  constexpr int kStage = (BM + BN) * 128;
-  constexpr int kScaleRing = (BM + BN) * 4;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStage + 2 * kScaleRing];
+  constexpr int kCodes = (BM + BN) * 128, kStage = kCodes + (BM + BN) * 4;
+  constexpr int kGroups = (kF32Scale ? BM : BM + BN) / 64;  // of 64 scale words
+  static_assert(kGroups <= kWaves, "one group a wave");
+  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage + 256];  // + a sink
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / kWN, wn = wave % kWN;
-
   int64_t m0, n0;
   tile_of(blockIdx.x, tiles_m, tiles_n, m0, n0);
   m0 *= BM;
   n0 *= BN;
+  const int kb0 = (int)blockIdx.y * per_split, kb1 = min(kb0 + per_split, K / 128);
 
   const int mrows = (int)min((int64_t)BM, M - m0), nrows = (int)min((int64_t)BN, N - n0);
   const __amdgpu_buffer_rsrc_t rx =
       __builtin_amdgcn_make_buffer_rsrc((void*)(X + m0 * K), (short)0, mrows * K, kRsrc3);
   const __amdgpu_buffer_rsrc_t rw =
       __builtin_amdgcn_make_buffer_rsrc((void*)(W + n0 * K), (short)0, nrows * K, kRsrc3);
-  const __amdgpu_buffer_rsrc_t rxs = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(XS + m0 * ldxs), (short)0, (int)(mrows * ldxs), kRsrc3);
-  const __amdgpu_buffer_rsrc_t rws = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)((const uint8_t*)WS + (n0 >> w_shift) * ldws), (short)0,
-      (int)((((nrows - 1) >> w_shift) + 1) * ldws), kRsrc3);
+  // this wave's scale words: X rows (groups 0 ..), then W rows; waves without a
+  // group read X's first row into the sink
+  const bool has = wave < kGroups, of_x = wave < BM / 64 || !has;
+  const uint32_t srow = has ? (of_x ? wave * 64 + lane : ((wave - BM / 64) * 64 + lane) >> w_shift) : 0u;
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(of_x ? XS + m0 * ldxs : (const uint8_t*)WS + (n0 >> w_shift) * ldws), (short)0,
+      (int)(of_x ? mrows * ldxs : (((nrows - 1) >> w_shift) + 1) * ldws), kRsrc3);
+  const uint32_t soff = srow * (uint32_t)(of_x ? ldxs : ldws);
 
-  // LDS: [stage][X rows, then W rows], then [ring slot][X words, then W words]
-  constexpr int kLoads = (BM + BN) / 8 / kWaves;   // per wave and stage
+  constexpr int kLoads = (BM + BN) / 8 / kWaves;  // of codes, per wave and stage
   constexpr int kXLoads = BM / 8 / kWaves;
   static_assert((BM + BN) % (8 * kWaves) == 0 && BM % (8 * kWaves) == 0, "whole loads a wave");
   uint32_t voff[kLoads];
@@ -214,32 +233,22 @@ __device__ __forceinline__ void gemm_fp8_tile(
                     (lane >> 3);
     voff[i] = (uint32_t)row * (uint32_t)K + (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
   }
-  auto load_stage = [&](int kb) {
-    char* base = lds + (kb & 1) * kStage;
+  auto load_stage = [&](int kb, int slot) {
+    char* base = lds + slot * kStage;
+    const int blk = min(kb, kb1 - 1);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       if (i < kXLoads)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rx, (glds_void_t*)(base + (wave * kXLoads + i) * 1024), 16, voff[i], kb * 128, 0, 0);
+            rx, (glds_void_t*)(base + (wave * kXLoads + i) * 1024), 16, voff[i], blk * 128, 0, 0);
       else
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rw, (glds_void_t*)(base + BM * 128 + (wave * (kLoads - kXLoads) + i - kXLoads) * 1024),
-            16, voff[i], kb * 128, 0, 0);
+            16, voff[i], blk * 128, 0, 0);
     }
-  };
-  // scale words of blocks 4g .. 4g + 3: 64 rows an instruction
-  auto load_scales = [&](int g) {
-    char* base = lds + 2 * kStage + (g & 1) * kScaleRing;
-    for (int r = wave; r < (kF32Scale ? BM : BM + BN) / 64; r += kWaves) {
-      if (r < BM / 64)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (glds_void_t*)(base + r * 256), 4,
-                                                 (uint32_t)(r * 64 + lane) * (uint32_t)ldxs, 4 * g,
-                                                 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rws, (glds_void_t*)(base + r * 256), 4,
-            (uint32_t)(((r - BM / 64) * 64 + lane) >> w_shift) * (uint32_t)ldws, 4 * g, 0, 0);
-    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs, (glds_void_t*)(has ? base + kCodes + wave * 256 : lds + kStages * kStage), 4, soff,
+        (blk >> 2) * 4, 0, 0);
   };
 
   gf32x16_t acc[kTN][kTM];
@@ -252,42 +261,39 @@ __device__ __forceinline__ void gemm_fp8_tile(
 
   const int frow = lane & 31, fhalf = lane >> 5, fsw = (frow >> 1) & 7;
   const int xrow = wm * (BM / kWM) + frow, wrow = wn * (BN / kWN) + frow;
-  uint32_t sxw[kTM], sww[kTN];
   const float* wsf = reinterpret_cast<const float*>(WS) +
                      (int64_t)((n0 + wn * (BN / kWN)) >> 7) * ldws;  // kF32Scale: one block row
-  const int KB = K / 128;
-  load_scales(0);
-  load_stage(0);
-  for (int kb = 0; kb < KB; ++kb) {
-    // stage kb has landed for this wave; after the barrier for all, and every
-    // wave has read the buffer that stage kb + 1 goes into
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load_stage(kb0 + s, s);
+  int slot = 0;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    // stage kb has landed for this wave (the loads of the kStages - 2 after it may
+    // be in flight); after the barrier for all, and every wave has read the stage
+    // that is loaded next
+    wait_loads<(kStages - 2) * (kLoads + 1)>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (kb + 1 < KB) {
-      if (((kb + 1) & 3) == 0) load_scales((kb + 1) >> 2);
-      load_stage(kb + 1);
-    }
-    if ((kb & 3) == 0) {
-      const char* sb = lds + 2 * kStage + ((kb >> 2) & 1) * kScaleRing;
+    load_stage(kb + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+    const char* const stage = lds + slot * kStage;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    uint32_t sxw[kTM], sww[kTN];
 #pragma unroll
-      for (int j = 0; j < kTM; ++j)
-        sxw[j] = *reinterpret_cast<const uint32_t*>(sb + (xrow + j * 32) * 4);
-      if constexpr (!kF32Scale) {
+    for (int j = 0; j < kTM; ++j)
+      sxw[j] = *reinterpret_cast<const uint32_t*>(stage + kCodes + (xrow + j * 32) * 4);
+    if constexpr (!kF32Scale) {
 #pragma unroll
-        for (int i = 0; i < kTN; ++i)
-          sww[i] = *reinterpret_cast<const uint32_t*>(sb + (BM + wrow + i * 32) * 4);
-      }
+      for (int i = 0; i < kTN; ++i)
+        sww[i] = *reinterpret_cast<const uint32_t*>(stage + kCodes + (BM + wrow + i * 32) * 4);
     }
     const int sh = 8 * (kb & 3);
-    const char* xs = lds + (kb & 1) * kStage + xrow * 128;
-    const char* ws = lds + (kb & 1) * kStage + (BM + wrow) * 128;
+    const char* xs = stage + xrow * 128;
+    const char* ws = stage + (BM + wrow) * 128;
     float wscale = 0.0f;
     if constexpr (kF32Scale) wscale = wsf[kb];
     auto chunk = [&](const char* row, int c) {
       return *reinterpret_cast<const gu32x4_t*>(row + ((c ^ fsw) * 16));
     };
-    if constexpr (kBf16) {
+    if constexpr (kFp8) {
       // half s of the block: lanes 0..31 chunks 4s, 4s + 1, lanes 32..63 the next two
       auto frag = [&](const char* row, int s) {
         return join(chunk(row, 4 * s + 2 * fhalf), chunk(row, 4 * s + 2 * fhalf + 1));
@@ -386,18 +392,44 @@ __device__ __forceinline__ void gemm_fp8_tile(
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   static_assert(kWaves * kStageBytes<kBf16, kTN> <= (int)sizeof(lds), "epilogue stage");
-  store_tile<kBf16, kTN, kTM>(acc, lds + wave * kStageBytes<kBf16, kTN>, Y, m0 + wm * (BM / kWM),
+  char* const y = reinterpret_cast<char*>(Y) + (int64_t)blockIdx.y * M * N * (kBf16 ? 2 : 4);
+  store_tile<kBf16, kTN, kTM>(acc, lds + wave * kStageBytes<kBf16, kTN>, y, m0 + wm * (BM / kWM),
                               n0 + wn * (BN / kWN), M, N, lane);
 }
 
 // (The body is a device function: the host pass cannot instantiate it.)
-template <int BM, int BN, int kWM, int kWN, bool kF32Scale, bool kBf16>
+template <int BM, int BN, int kWM, int kWN, int kStages, bool kF32Scale, bool kFp8, bool kBf16>
 __global__ __launch_bounds__(kWM* kWN * 64) void gemm_fp8_tile_kernel(
     const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
     const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int64_t M,
-    int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n) {
-  gemm_fp8_tile<BM, BN, kWM, kWN, kF32Scale, kBf16>(X, XS, ldxs, W, WS, ldws, w_shift, M, N, K, Y,
-                                                    tiles_m, tiles_n);
+    int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n, int per_split) {
+  gemm_fp8_tile<BM, BN, kWM, kWN, kStages, kF32Scale, kFp8, kBf16>(
+      X, XS, ldxs, W, WS, ldws, w_shift, M, N, K, Y, tiles_m, tiles_n, per_split);
+}
+
+// Y = sum of `splits` float32 planes, in order; 4 elements a thread.
+template <bool kBf16>
+__global__ __launch_bounds__(256) void gemm_fp8_reduce_kernel(const float* __restrict__ parts,
+                                                              int splits, int64_t total,
+                                                              void* __restrict__ Y) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= total) return;
+  if (i + 4 <= total && (total & 3) == 0) {
+    gf32x4_t s = *reinterpret_cast<const gf32x4_t*>(parts + i);
+    for (int p = 1; p < splits; ++p) s += *reinterpret_cast<const gf32x4_t*>(parts + p * total + i);
+    if constexpr (kBf16)
+      *reinterpret_cast<gu32x2_t*>(reinterpret_cast<uint16_t*>(Y) + i) =
+          gu32x2_t{f32x2_to_bf16x2(s[0], s[1]), f32x2_to_bf16x2(s[2], s[3])};
+    else
+      *reinterpret_cast<gf32x4_t*>(reinterpret_cast<float*>(Y) + i) = s;
+  } else {
+    for (int64_t e = i; e < min(i + 4, total); ++e) {
+      float s = parts[e];
+      for (int p = 1; p < splits; ++p) s += parts[p * total + e];
+      if constexpr (kBf16) reinterpret_cast<uint16_t*>(Y)[e] = (uint16_t)f32_to_bf16(s);
+      else reinterpret_cast<float*>(Y)[e] = s;
+    }
+  }
 }
 
 // Large products with E8M0 scales on both sides. 256 x 256 of Y a workgroup, 4
@@ -673,38 +705,69 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
   }
 }
 
+// Which kernel, from the sizes alone.
+enum GemmKind { kSkinny, kSmall, kMiddle, kLarge };
+struct GemmPlan {
+  GemmKind kind;
+  int splits, per_split;  // of K's blocks
+};
+static GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k) {
+  const int64_t kb = k / 128;
+  const auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
+  if (m <= 64) return {kSkinny, 1, (int)kb};
+  if (tiles(256) >= 256) return {kLarge, 1, (int)kb};
+  if (tiles(128) >= 256) return {kMiddle, 1, (int)kb};
+  // parts of at least 4 blocks, while the chip (two workgroups a CU) has room
+  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles(64), kb / 4));
+  const int64_t per = (kb + splits - 1) / splits;
+  return {kSmall, (int)((kb + per - 1) / per), (int)per};
+}
+
 template <bool kF32Scale, bool kBf16>
 static hipError_t launch_gemm(const uint8_t* x, const uint8_t* xs, int64_t ldxs, const uint8_t* w,
                               const void* ws, int64_t ldws, int w_shift, int64_t m, int64_t n,
-                              int64_t k, void* y, hipStream_t stream) {
-  if (m <= 64) {
-    const dim3 grid((unsigned)((n + 15) / 16)), block(kSkinnyWaves * 64);
-#define HIF4_SKINNY(mb)                                                                          \
-  hipLaunchKernelGGL((gemm_fp8_skinny_kernel<mb, kF32Scale, kBf16>), grid, block, 0, stream, x,  \
-                     xs, ldxs, w, ws, ldws, w_shift, (int)m, n, (int)k, y)
-    if (m <= 16) HIF4_SKINNY(1);
-    else if (m <= 32) HIF4_SKINNY(2);
-    else HIF4_SKINNY(4);
-#undef HIF4_SKINNY
-    return hipGetLastError();
-  }
-#define HIF4_TILED(bm, bn, wm, wn)                                                               \
+                              int64_t k, void* y, void* workspace, hipStream_t stream) {
+  const GemmPlan plan = plan_gemm(m, n, k);
+#define HIF4_TILED(bm, bn, wm, wn, st, bf16, out)                                                \
   do {                                                                                           \
     const uint32_t tm = (uint32_t)((m + bm - 1) / bm), tn = (uint32_t)((n + bn - 1) / bn);       \
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<bm, bn, wm, wn, kF32Scale, kBf16>), dim3(tm * tn),  \
-                       dim3(wm * wn * 64), 0, stream, x, xs, ldxs, w, ws, ldws, w_shift, m, n,   \
-                       (int)k, y, tm, tn);                                                       \
+    hipLaunchKernelGGL((gemm_fp8_tile_kernel<bm, bn, wm, wn, st, kF32Scale, kBf16, bf16>),       \
+                       dim3(tm * tn, plan.splits), dim3(wm * wn * 64), 0, stream, x, xs, ldxs,   \
+                       w, ws, ldws, w_shift, m, n, (int)k, out, tm, tn, plan.per_split);         \
   } while (0)
-  if ((m + 255) / 256 * ((n + 255) / 256) >= 256) {
-    if constexpr (kF32Scale) {
-      HIF4_TILED(256, 256, 2, 4);
-    } else {
-      const uint32_t tm = (uint32_t)((m + 255) / 256), tn = (uint32_t)((n + 255) / 256);
-      hipLaunchKernelGGL(gemm_fp8_big_kernel<kBf16>, dim3(tm * tn), dim3(256), 0, stream, x, xs,
-                         ldxs, w, (const uint8_t*)ws, ldws, w_shift, m, n, (int)k, y, tm, tn);
-    }
+#define HIF4_SKINNY(mb)                                                                          \
+  hipLaunchKernelGGL((gemm_fp8_skinny_kernel<mb, kF32Scale, kBf16>),                             \
+                     dim3((unsigned)((n + 15) / 16)), dim3(kSkinnyWaves * 64), 0, stream, x, xs, \
+                     ldxs, w, ws, ldws, w_shift, (int)m, n, (int)k, y)
+  switch (plan.kind) {
+    case kSkinny:
+      if (m <= 16) HIF4_SKINNY(1);
+      else if (m <= 32) HIF4_SKINNY(2);
+      else HIF4_SKINNY(4);
+      break;
+    case kLarge:
+      if constexpr (kF32Scale) {
+        HIF4_TILED(256, 256, 2, 4, 2, kBf16, y);
+      } else {
+        const uint32_t tm = (uint32_t)((m + 255) / 256), tn = (uint32_t)((n + 255) / 256);
+        hipLaunchKernelGGL(gemm_fp8_big_kernel<kBf16>, dim3(tm * tn), dim3(256), 0, stream, x, xs,
+                           ldxs, w, (const uint8_t*)ws, ldws, w_shift, m, n, (int)k, y, tm, tn);
+      }
+      break;
+    case kMiddle: HIF4_TILED(128, 128, 2, 2, 2, kBf16, y); break;
+    case kSmall:
+      if (plan.splits == 1) {
+        HIF4_TILED(64, 64, 2, 2, 4, kBf16, y);
+        break;
+      }
+      HIF4_TILED(64, 64, 2, 2, 4, false, workspace);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(gemm_fp8_reduce_kernel<kBf16>, dim3((unsigned)((m * n + 1023) / 1024)),
+                         dim3(256), 0, stream, (const float*)workspace, plan.splits, m * n, y);
+      break;
   }
-  else HIF4_TILED(128, 128, 2, 2);
+#undef HIF4_SKINNY
 #undef HIF4_TILED
   return hipGetLastError();
 }
@@ -717,18 +780,17 @@ hipError_t hif4_launch_gemm_fp8(const uint8_t* x, const uint8_t* xs, int64_t ldx
                                 const void* ws, int64_t ldws, bool ws_f32, int w_block, int64_t m,
                                 int64_t n, int64_t k, void* y, bool y_bf16, void* workspace,
                                 hipStream_t stream) {
-  (void)workspace;
   const int shift = w_block == 128 ? 7 : 0;
   if (ws_f32) {
-    return y_bf16 ? launch_gemm<true, true>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, stream)
-                  : launch_gemm<true, false>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, stream);
+    return y_bf16 ? launch_gemm<true, true>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, workspace, stream)
+                  : launch_gemm<true, false>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, workspace, stream);
   }
-  return y_bf16 ? launch_gemm<false, true>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, stream)
-                : launch_gemm<false, false>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, stream);
+  return y_bf16 ? launch_gemm<false, true>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, workspace, stream)
+                : launch_gemm<false, false>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, workspace, stream);
 }
 
-// No launch needs scratch at present.
 size_t hif4_gemm_fp8_ws_bytes(int64_t m, int64_t n, int64_t k) {
-  (void)m, (void)n, (void)k;
-  return 0;
+  if (m == 0 || n == 0 || k == 0) return 0;
+  const GemmPlan p = plan_gemm(m, n, k);
+  return p.splits == 1 ? 0 : (size_t)p.splits * (size_t)m * (size_t)n * sizeof(float);
 }

@@ -18,9 +18,6 @@
 
 namespace hif4 {
 
-#ifndef WWG
-#define WWG 3
-#endif
 enum NormOut { kOutY = 0, kOutHif4 = 1, kOutFp8 = 2 };
 
 // Sum over the lanes of a wave, the same bits in every lane: DPP moves inside
@@ -602,7 +599,7 @@ static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   const int waves = (items + 63) / 64;
   if constexpr (sizeof(T) == 2 && kVec && kOut != kOutY) {
     if (waves > 1 && waves <= 8 && a.rows >= 256 * 8) {
-      const dim3 grid((unsigned)std::min<int64_t>((a.rows + 7) / 8, 256 * WWG)), block(512);
+      const dim3 grid((unsigned)std::min<int64_t>((a.rows + 7) / 8, 256 * 8)), block(512);
       const size_t lds = (size_t)items * 8 * sizeof(float4);
 #define HIF4_WAVE(n) \
   hipLaunchKernelGGL((layer_norm_wave_kernel<n, kOut>), grid, block, lds, stream, a)
