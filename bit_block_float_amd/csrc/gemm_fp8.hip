@@ -16,7 +16,6 @@
 //    with the power-of-two scale applied; below 2^-126 bf16 is subnormal and
 //    may round) and multiplied by the bf16 forms, whose products and sums are
 //    full fp32: a float32 result is asked for where the last bits count.
-//  - up to 64 rows (bound by reading W) always the latter.
 // A weight whose scales are float32 (one per 128 x 128) keeps sx in the
 // operands and adds each block's partial sum times sw with one FMA per output.
 //
@@ -48,6 +47,10 @@ __device__ __forceinline__ i32x8_t join(gu32x4_t a, gu32x4_t b) {
 
 __device__ __forceinline__ gf32x16_t mfma32(i32x8_t a, i32x8_t b, gf32x16_t c, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, kFmtE4M3, kFmtE4M3, 0, sa, 0, sb);
+}
+
+__device__ __forceinline__ gf32x4_t mfma16(i32x8_t a, i32x8_t b, gf32x4_t c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, kFmtE4M3, kFmtE4M3, 0, sa, 0, sb);
 }
 
 // This wave's loads but the newest n have landed, its LDS reads are done.
@@ -634,74 +637,96 @@ void gemm_fp8_big_kernel(const uint8_t* __restrict__ X, const uint8_t* __restric
   gemm_fp8_big<kBf16>(X, XS, ldxs, W, WS, ldws, w_shift, M, N, K, Y, tiles_m, tiles_n);
 }
 
-// Few rows: bound by reading W once. A workgroup owns 16 columns of Y; its
-// waves take the K blocks in turn, W straight from memory into the MFMA's
-// operand registers, and their sums meet in LDS in a fixed order. Rows past M
-// or N repeat the last one and are not stored.
-constexpr int kSkinnyWaves = 8;
-template <int MB, bool kF32Scale, bool kBf16>
+// Up to 16 rows: bound by reading W once. A workgroup owns `cols` <= 16 columns of
+// Y; its waves take the K blocks in turn, W straight from memory into the MFMA's
+// operand registers, and their sums meet in LDS in a fixed order. Rows past M or
+// the workgroup's columns repeat the last one and are not stored.
+//
+// What a CU can have in flight to memory sets the pace, so the columns are cut to
+// give every CU the same share: cols is the least that leaves as many workgroups
+// a CU as 16 would. Measured, one row: n = 5120, k = 13824, 320 workgroups of 16
+// columns 17.9 us, 512 of 10 15.3 us; n = 13824, k = 5120, 864 of 16 14.5 us, 988
+// of 14 13.6 us. (16 rows against tiles, n = k = 5120: 10.9 and 12.0 us; 24 rows
+// the other way about, 14.3 and 12.0 us.)
+constexpr int kSkinnyRows = 16;
+constexpr int kSkinnyWaves = 16;
+template <bool kF32Scale, bool kBf16>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
     const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
     const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int M,
-    int64_t N, int K, void* __restrict__ Y) {
-  __shared__ gf32x4_t part[kSkinnyWaves][MB][64];
+    int64_t N, int K, int cols, void* __restrict__ Y) {
+  __shared__ gf32x4_t part[kSkinnyWaves][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kq = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int64_t wr = min(n0 + r16, N - 1);
-  const uint8_t* wp = W + wr * K + kq * 32;
+  const int64_t n0 = (int64_t)blockIdx.x * cols, n1 = min(n0 + cols, N);
+  const int64_t wr = min(n0 + r16, n1 - 1);
+  const int xr = min(r16, M - 1);
+  // of each block lane group kq takes bytes 16 kq and 64 + 16 kq on, of both operands
+  const uint8_t* wp = W + wr * K + kq * 16;
+  const uint8_t* xp = X + (int64_t)xr * K + kq * 16;
   const uint8_t* wsb = (const uint8_t*)WS + (wr >> w_shift) * ldws;
-  const float* wsf = (const float*)WS + (n0 >> 7) * ldws;
-  const uint8_t* xp[MB];
-  const uint8_t* xsb[MB];
-#pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    const int xr = min(b * 16 + r16, M - 1);
-    xp[b] = X + (int64_t)xr * K + kq * 32;
-    xsb[b] = XS + (int64_t)xr * ldxs;
-  }
-  gf32x4_t acc[MB];
-#pragma unroll
-  for (int b = 0; b < MB; ++b) acc[b] = gf32x4_t{0, 0, 0, 0};
+  const uint8_t* xsb = XS + (int64_t)xr * ldxs;
+  // float32 scales: the columns lie in one block row, or two
+  const float* wsf0 = (const float*)WS + (n0 >> 7) * ldws;
+  const float* wsf1 = (const float*)WS + ((n1 - 1) >> 7) * ldws;
+  const int64_t border = ((n1 - 1) >> 7) << 7;  // first column of the second
+  gf32x4_t acc = {0, 0, 0, 0};
   const int KB = K / 128;
-  for (int kb = wave; kb < KB; kb += kSkinnyWaves) {
-    const gu32x4_t* w = reinterpret_cast<const gu32x4_t*>(wp + (int64_t)kb * 128);
-    const gu32x4_t wa = w[0], wb = w[1];
-    const float sw = kF32Scale ? 1.0f : e8m0_f32(wsb[kb]);
-    const gbf16x8_t fw[4] = {widen(wa.x, wa.y, sw), widen(wa.z, wa.w, sw), widen(wb.x, wb.y, sw),
-                             widen(wb.z, wb.w, sw)};
+  // kU blocks at a time, their loads all in flight before the first product (past
+  // the end the last block again, not used)
+  constexpr int kU = 4;
+  for (int kb = wave; kb < KB; kb += kU * kSkinnyWaves) {
+    gu32x4_t w[kU][2], x[kU][2];
+    uint32_t sw[kU], sx[kU];
+    float swf0[kU], swf1[kU];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      const gu32x4_t* x = reinterpret_cast<const gu32x4_t*>(xp[b] + (int64_t)kb * 128);
-      const gu32x4_t xa = x[0], xb = x[1];
-      const float sx = e8m0_f32(xsb[b][kb]);
-      gf32x4_t p = kF32Scale ? gf32x4_t{0, 0, 0, 0} : acc[b];
-      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[0], widen(xa.x, xa.y, sx), p, 0, 0, 0);
-      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[1], widen(xa.z, xa.w, sx), p, 0, 0, 0);
-      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[2], widen(xb.x, xb.y, sx), p, 0, 0, 0);
-      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[3], widen(xb.z, xb.w, sx), p, 0, 0, 0);
-      if constexpr (kF32Scale) {
-        const float swf = wsf[kb];
+    for (int u = 0; u < kU; ++u) {
+      const int k = min(kb + u * kSkinnyWaves, KB - 1);
+      w[u][0] = *reinterpret_cast<const gu32x4_t*>(wp + (int64_t)k * 128);
+      w[u][1] = *reinterpret_cast<const gu32x4_t*>(wp + (int64_t)k * 128 + 64);
+      x[u][0] = *reinterpret_cast<const gu32x4_t*>(xp + (int64_t)k * 128);
+      x[u][1] = *reinterpret_cast<const gu32x4_t*>(xp + (int64_t)k * 128 + 64);
+      sx[u] = xsb[k];
+      sw[u] = kF32Scale ? (uint32_t)kUnitScale : wsb[k];
+      swf0[u] = kF32Scale ? wsf0[k] : 1.0f;
+      swf1[u] = kF32Scale ? wsf1[k] : 1.0f;
+    }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[b][r] = fmaf(p[r], swf, acc[b][r]);
+    for (int u = 0; u < kU; ++u) {
+      if (kb + u * kSkinnyWaves >= KB) break;  // uniform
+      gf32x4_t p = kF32Scale ? gf32x4_t{0, 0, 0, 0} : acc;
+      if constexpr (kBf16) {
+        p = mfma16(join(w[u][0], w[u][1]), join(x[u][0], x[u][1]), p, (int)sw[u], (int)sx[u]);
       } else {
-        acc[b] = p;
+        const float fw = e8m0_f32(sw[u]), fx = e8m0_f32(sx[u]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[u][h].x, w[u][h].y, fw),
+                                                      widen(x[u][h].x, x[u][h].y, fx), p, 0, 0, 0);
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[u][h].z, w[u][h].w, fw),
+                                                      widen(x[u][h].z, x[u][h].w, fx), p, 0, 0, 0);
+        }
+      }
+      if constexpr (kF32Scale) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[r] = fmaf(p[r], n0 + kq * 4 + r < border ? swf0[u] : swf1[u], acc[r]);
+      } else {
+        acc = p;
       }
     }
   }
-#pragma unroll
-  for (int b = 0; b < MB; ++b) part[wave][b][lane] = acc[b];
+  part[wave][lane] = acc;
   __syncthreads();
-  const bool vec = (N & 3) == 0 && ((uintptr_t)Y & 15) == 0;
-  for (int b = wave; b < MB; b += kSkinnyWaves) {
-    gf32x4_t s = part[0][b][lane];
+  if (wave == 0) {
+    gf32x4_t s = part[0][lane];
 #pragma unroll
-    for (int w = 1; w < kSkinnyWaves; ++w) s += part[w][b][lane];
-    const int row = b * 16 + r16;
+    for (int w = 1; w < kSkinnyWaves; ++w) s += part[w][lane];
+    const bool vec = (N & 3) == 0 && (cols & 3) == 0 && ((uintptr_t)Y & 15) == 0;
     const int64_t col = n0 + kq * 4;
-    if (row < M && col < N)
-      store4<kBf16>(Y, (int64_t)row * N + col, (int)col, (int)N, vec, s[0], s[1], s[2], s[3]);
+    if (r16 < M && col < n1)
+      store4<kBf16>(Y, (int64_t)r16 * N + col, (int)col, (int)n1, vec, s[0], s[1], s[2], s[3]);
   }
 }
 
@@ -714,7 +739,7 @@ struct GemmPlan {
 static GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k) {
   const int64_t kb = k / 128;
   const auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
-  if (m <= 64) return {kSkinny, 1, (int)kb};
+  if (m <= kSkinnyRows) return {kSkinny, 1, (int)kb};
   if (tiles(256) >= 256) return {kLarge, 1, (int)kb};
   if (tiles(128) >= 256) return {kMiddle, 1, (int)kb};
   // parts of at least 4 blocks, while the chip (two workgroups a CU) has room
@@ -735,15 +760,14 @@ static hipError_t launch_gemm(const uint8_t* x, const uint8_t* xs, int64_t ldxs,
                        dim3(tm * tn, plan.splits), dim3(wm * wn * 64), 0, stream, x, xs, ldxs,   \
                        w, ws, ldws, w_shift, m, n, (int)k, out, tm, tn, plan.per_split);         \
   } while (0)
-#define HIF4_SKINNY(mb)                                                                          \
-  hipLaunchKernelGGL((gemm_fp8_skinny_kernel<mb, kF32Scale, kBf16>),                             \
-                     dim3((unsigned)((n + 15) / 16)), dim3(kSkinnyWaves * 64), 0, stream, x, xs, \
-                     ldxs, w, ws, ldws, w_shift, (int)m, n, (int)k, y)
+  constexpr int64_t kCus = 256;
+  const int64_t per_cu = (n + 16 * kCus - 1) / (16 * kCus);
+  const int cols = (int)((n + kCus * per_cu - 1) / (kCus * per_cu));  // 1 .. 16
   switch (plan.kind) {
     case kSkinny:
-      if (m <= 16) HIF4_SKINNY(1);
-      else if (m <= 32) HIF4_SKINNY(2);
-      else HIF4_SKINNY(4);
+      hipLaunchKernelGGL((gemm_fp8_skinny_kernel<kF32Scale, kBf16>),
+                         dim3((unsigned)((n + cols - 1) / cols)), dim3(kSkinnyWaves * 64), 0,
+                         stream, x, xs, ldxs, w, ws, ldws, w_shift, (int)m, n, (int)k, cols, y);
       break;
     case kLarge:
       if constexpr (kF32Scale) {
@@ -767,7 +791,6 @@ static hipError_t launch_gemm(const uint8_t* x, const uint8_t* xs, int64_t ldxs,
                          dim3(256), 0, stream, (const float*)workspace, plan.splits, m * n, y);
       break;
   }
-#undef HIF4_SKINNY
 #undef HIF4_TILED
   return hipGetLastError();
 }
