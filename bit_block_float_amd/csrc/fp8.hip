@@ -234,7 +234,8 @@ hipError_t hif4_launch_quantize_fp8(const void* x, bool bf16, int64_t rows, int6
                                     int block_rows, uint8_t* codes, uint8_t* scales, int64_t lds,
                                     uint8_t* codes_t, uint8_t* scales_t, int64_t lds_t,
                                     hipStream_t stream) {
-  const bool vec = ((uintptr_t)x & 15) == 0 && ld % (bf16 ? 8 : 4) == 0 && k % 8 == 0;
+  const bool vec = ((uintptr_t)x & 15) == 0 && ld % (bf16 ? 8 : 4) == 0 &&
+                   k % (bf16 ? 8 : 4) == 0;
 #define HIF4_QUANTIZE(T, v)                                                                     \
   launch_quantize<T, v>((const T*)x, rows, k, ld, block_rows, codes, scales, lds, codes_t,       \
                         scales_t, lds_t, stream)

@@ -57,8 +57,9 @@ __device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
 // 8 consecutive elements of a row of c >= 1, from column col; elements at or past
 // c are zero. The loads are unconditional, from clamped addresses (a load behind
 // a branch is waited for at the branch's end, one after the other). kVec: rows
-// are 16-byte aligned and c % 8 == 0, so a run is whole or empty: one (bf16) or
-// two (fp32) 16-byte loads. Otherwise element by element.
+// are 16-byte aligned and c is a multiple of 8 (bf16) or 4 (fp32), so 16-byte
+// pieces are whole or empty: one (bf16) or two (fp32) loads. Otherwise element by
+// element.
 template <typename T>
 struct Run8;
 template <>
@@ -112,11 +113,12 @@ struct Run8<float> {
   template <bool kVec>
   __device__ __forceinline__ void load(const float* row, int col, int c) {
     if constexpr (kVec) {
-      const float4* p = reinterpret_cast<const float4*>(row + (col < c ? col : 0));
-      const float4 a = p[0], b = p[1];
+      const float4 a = *reinterpret_cast<const float4*>(row + (col < c ? col : 0));
+      const float4 b = *reinterpret_cast<const float4*>(row + (col + 4 < c ? col + 4 : 0));
       v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
       v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-      keep_if(col < c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = col + (i & 4) < c ? v[i] : 0.0f;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = row[min(col + i, c - 1)];

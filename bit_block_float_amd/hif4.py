@@ -81,6 +81,11 @@ def lib():
         L.hif4_linear_fp8_workspace_bytes.restype = sz
         L.hif4_linear_fp8.argtypes = [p, p, i64, p, p, i64, i, i64, i64, i64, i64, p, i, p, sz, p]
         L.hif4_linear_fp8.restype = i
+        L.hif4_linear_fp8_backward_workspace_bytes.argtypes = [i64, i64, i64]
+        L.hif4_linear_fp8_backward_workspace_bytes.restype = sz
+        L.hif4_linear_fp8_backward.argtypes = [p, i, i64, p, p, i64, p, p, i64, i, i64, i64, i64, i64,
+                                               p, i, p, i, p, sz, p]
+        L.hif4_linear_fp8_backward.restype = i
         L.hif4_layer_norm.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, i64, p, p, p]
         L.hif4_layer_norm.restype = i
         L.hif4_layer_norm_quantize.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, i64, p, p, p, p]
@@ -617,24 +622,42 @@ def linear_fp8(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=No
     return y
 
 
+def linear_fp8_backward_workspace_bytes(m, n, k):
+    return int(lib().hif4_linear_fp8_backward_workspace_bytes(m, n, k))
+
+
 def linear_fp8_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype=None,
-                        dw_dtype=torch.float32, stream=None):
+                        dw_dtype=torch.float32, workspace=None, stream=None):
     """Gradients of Y = X W^T through the quantizers (taken as the identity):
     dX [m][k] = Q(dY) W and dW [n][k] = Q(dY^T) X for dy [m][n] (bf16 or fp32),
-    with X^T and W^T quantized along m and n (quantize_fp8(..., transposed=True),
-    the weight with block_rows=128 or 1). dX is of dy's type unless dx_dtype says
-    otherwise."""
+    with X^T and W^T quantized along m and n (quantize_fp8(..., transposed=True);
+    the weight's scales as linear_fp8 takes them). dX is of dy's type unless
+    dx_dtype says otherwise."""
     _check_rows(dy, "dy")
     _check_codes(xt_codes, "xt_codes")
     _check_codes(wt_codes, "wt_codes")
-    m, n = dy.shape
-    if xt_codes.shape[1] != _up128(m) or wt_codes.shape != (xt_codes.shape[0], _up128(n)):
-        raise ValueError(f"dy is {m} x {n}: xt_codes must be [k][{_up128(m)}], wt_codes [k][{_up128(n)}]")
-    if xt_scales.dtype == torch.float32:
-        raise ValueError("xt_scales must be float8_e8m0fnu, one per 1 x 128")
-    codes, scales, codes_t, scales_t = quantize_fp8_both(dy, stream=stream)
-    dx = linear_fp8(codes, scales, wt_codes, wt_scales, y_dtype=dx_dtype or dy.dtype, stream=stream)
-    dw = linear_fp8(codes_t, scales_t, xt_codes, xt_scales, y_dtype=dw_dtype, stream=stream)
+    (m, n), k = dy.shape, xt_codes.shape[0]
+    mp, np_ = _up128(m), _up128(n)
+    if xt_codes.shape[1] != mp or wt_codes.shape != (k, np_):
+        raise ValueError(f"dy is {m} x {n}: xt_codes must be [k][{mp}], wt_codes [k][{np_}]")
+    dx_dtype = dy.dtype if dx_dtype is None else dx_dtype
+    if dx_dtype not in _DTYPE or dw_dtype not in _DTYPE:
+        raise ValueError("dx_dtype and dw_dtype must be float32 or bfloat16")
+    with _On(dy, stream, xt_codes, xt_scales, wt_codes, wt_scales, workspace) as st:
+        _check_scales(xt_scales, "xt_scales", k, mp // FP8_BLOCK)
+        kind, block_rows, ldwt = _weight_scales(wt_scales, k, np_ // FP8_BLOCK, "wt_scales")
+        dx = torch.empty((m, k), dtype=dx_dtype, device=dy.device)
+        dw = torch.empty((n, k), dtype=dw_dtype, device=dy.device)
+        if workspace is None:
+            workspace = torch.empty((linear_fp8_backward_workspace_bytes(m, n, k),),
+                                    dtype=torch.uint8, device=dy.device)
+        _ok(lib().hif4_linear_fp8_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt_codes),
+                                           _at(xt_scales), _scale_ld(xt_scales), _at(wt_codes),
+                                           _at(wt_scales), ldwt, kind, block_rows, m, n, k, _at(dx),
+                                           _DTYPE[dx_dtype], _at(dw), _DTYPE[dw_dtype],
+                                           _at(workspace),
+                                           workspace.numel() * workspace.element_size(), st),
+            "hif4_linear_fp8_backward")
     return dx, dw
 
 

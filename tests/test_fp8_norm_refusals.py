@@ -75,6 +75,29 @@ def test_linear_fp8(L):
         assert L.hif4_linear_fp8_workspace_bytes(*args) == 0
 
 
+def test_linear_fp8_backward(L):
+    ws = L.hif4_linear_fp8_backward_workspace_bytes(300, 200, 640)
+    # dY's codes and scales along both sides at least
+    assert ws >= 300 * 256 + 300 * 4 + 200 * 384 + 200 * 4 and ws % 256 == 0
+    for args in ((-1, 8, 128), (8, -1, 128), (1 << 23, 8, 8), (8, 8, BIG)):
+        assert L.hif4_linear_fp8_backward_workspace_bytes(*args) == 0
+
+    def f(dy=A, dt=1, ld=200, xc=A, xs=A, ldx=4, wc=A, wsc=A, ldw=4, kind=0, br=128, m=300, n=200, k=640, dx=A,
+          dxt=1, dw=A, dwt=0, wsp=A, nb=ws):
+        return L.hif4_linear_fp8_backward(dy, dt, ld, xc, xs, ldx, wc, wsc, ldw, kind, br, m, n, k, dx, dxt, dw, dwt,
+                                          wsp, nb, None)
+
+    assert f(m=-1) == SHAPE and f(k=-1) == SHAPE and f(ld=199) == SHAPE and f(k=BIG) == SHAPE
+    assert f(dt=2) == DTYPE and f(dxt=2) == DTYPE and f(dwt=2) == DTYPE and f(kind=2) == DTYPE
+    assert f(br=2) == ARG and f(kind=1, br=1) == ARG
+    for name in ("dy", "xc", "xs", "wc", "wsc"):
+        assert f(**{name: None}) == NULL
+    assert f(wsp=None) == WORKSPACE and f(nb=ws - 1) == WORKSPACE and f(wsp=A + 128) == ALIGN
+    assert f(ldx=2) == SHAPE and f(ldw=1) == SHAPE and f(ldx=6) == ALIGN
+    assert f(dx=A + 8) == ALIGN and f(dw=A + 4) == ALIGN and f(dy=A + 1) == ALIGN
+    assert f(dx=None, dw=None, dy=A, wsp=None) == OK
+
+
 def test_layer_norm(L):
     def f(x=A, dt=1, rows=4, c=100, ld=100, w=A, b=A, wd=0, eps=1e-6, y=A, ldy=100, mean=A, rstd=A):
         return L.hif4_layer_norm(x, dt, rows, c, ld, w, b, wd, eps, y, ldy, mean, rstd, None)

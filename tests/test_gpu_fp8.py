@@ -37,7 +37,7 @@ def _check_quantized(x, codes, scales, block_rows):
     assert torch.equal(got, rc), (x.shape, block_rows, (got != rc).nonzero()[:4])
 
 
-SHAPES = [(1, 1), (1, 128), (3, 127), (5, 129), (127, 16), (128, 128), (129, 257), (64, 1000),
+SHAPES = [(1, 1), (130, 132), (7, 1300), (1, 128), (3, 127), (5, 129), (127, 16), (128, 128), (129, 257), (64, 1000),
           (300, 640), (1, 5120)]
 
 
@@ -168,6 +168,15 @@ def test_linear_shapes(hip, m, kind):
 
 
 @pytest.mark.parametrize("kind", ["tiles", "rows", "f32"])
+@pytest.mark.parametrize("m,n", [(1, 4097), (3, 5003), (16, 13824), (7, 8200)])
+def test_linear_few_rows_many_columns(hip, m, n, kind):
+    """Workgroups whose columns are not 16, and lie in two scale blocks."""
+    args, xv, wv = _linear_case(hip, m, n, 384, kind, seed=n)
+    for out in (torch.float32, torch.bfloat16):
+        _check_product(hip.linear_fp8(*args, y_dtype=out), xv, wv)
+
+
+@pytest.mark.parametrize("kind", ["tiles", "rows", "f32"])
 @pytest.mark.parametrize("m,n,k", [(4100, 4099, 128), (4352, 4096, 640), (2048, 9000, 384)])
 def test_linear_many_tiles(hip, m, n, k, kind):
     """Enough tiles for the large-tile kernel, ragged at both ends."""
@@ -264,6 +273,27 @@ def test_linear_backward(hip, m, n, k, dtype):
                    ref64.fp8_values(_bytes(wt[0]), _bytes(wt[1]), 128))
     _check_product(dw, ref64.fp8_values(*ref64.fp8_quantize(dy.T)),
                    ref64.fp8_values(_bytes(xt[0]), _bytes(xt[1])))
+
+
+@pytest.mark.parametrize("m,n,k", [(0, 40, 64), (30, 0, 64), (30, 40, 0)])
+def test_linear_backward_empty(hip, m, n, k):
+    dy = torch.ones((m, n), device="cuda")
+    xt = hip.quantize_fp8(torch.ones((m, k), device="cuda"), transposed=True)
+    wt = hip.quantize_fp8(torch.ones((n, k), device="cuda"), block_rows=128, transposed=True)
+    dx, dw = hip.linear_fp8_backward(dy, *xt, *wt)
+    assert dx.shape == (m, k) and dw.shape == (n, k)
+    assert bool((dx == 0).all()) and bool((dw == 0).all())
+
+
+def test_linear_backward_with_float_scales(hip):
+    """W^T as a checkpoint's codes and float32 scales transposed."""
+    m, n, k = 70, 300, 260
+    dy = _x(m, n, 3) * 1e-3
+    xt = hip.quantize_fp8(_x(m, k, 4).cuda(), transposed=True)
+    wc, ws = hip.quantize_fp8(_x(n, k, 5, spread=0.2).cuda(), block_rows=128, transposed=True)
+    s32 = torch.rand(ws.shape, device="cuda") + 0.5
+    dx, _ = hip.linear_fp8_backward(dy.cuda(), *xt, wc, s32, dx_dtype=torch.float32)
+    _check_product(dx, ref64.fp8_values(*ref64.fp8_quantize(dy)), ref64.fp8_values(_bytes(wc), s32.cpu(), 128))
 
 
 def test_linear_backward_against_differences(hip):
