@@ -562,23 +562,29 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
   }
 }
 
-// Sums the workgroups' parts: 64 columns a workgroup, 16 runs of parts each
-// added by one wave, the 16 sums added in order.
+// Sums the workgroups' parts: 32 columns a workgroup; its 32 half waves take the
+// parts in turn, 8 loads in flight each, and their sums are added in order.
 __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(const float* __restrict__ parts,
                                                                 int n_parts, int c, void* dw,
                                                                 void* db, bool w_bf16) {
-  __shared__ float sums[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, half = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + lane, cols = 2 * (int64_t)c;
+  const float* p = parts + min(col, cols - 1);
   float s = 0.0f;
-  if (col < 2 * (int64_t)c)
-    for (int p = wave; p < n_parts; p += 16) s += parts[(int64_t)p * 2 * c + col];
-  sums[wave][lane] = s;
+  for (int p0 = half; p0 < n_parts; p0 += 8 * 32) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = p[min(p0 + u * 32, n_parts - 1) * cols];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s += p0 + u * 32 < n_parts ? v[u] : 0.0f;
+  }
+  sums[half][lane] = s;
   __syncthreads();
-  if (wave == 0 && col < 2 * (int64_t)c) {
+  if (half == 0 && col < cols) {
     s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) s += sums[w][lane];
+    for (int w = 0; w < 32; ++w) s += sums[w][lane];
     void* out = col < c ? dw : db;
     const int64_t i = col < c ? col : col - c;
     if (out) {
@@ -696,7 +702,7 @@ hipError_t hif4_launch_layer_norm_backward(const NormBackArgs& a, bool x_bf16, v
     e = x_bf16 ? launch_norm_backward<uint16_t, false>(a, grid, stream)
                : launch_norm_backward<float, false>(a, grid, stream);
   if (e != hipSuccess || !a.parts) return e;
-  hipLaunchKernelGGL(layer_norm_parts_kernel, dim3((unsigned)((2 * (int64_t)a.c + 63) / 64)),
+  hipLaunchKernelGGL(layer_norm_parts_kernel, dim3((unsigned)((2 * (int64_t)a.c + 31) / 32)),
                      dim3(1024), 0, stream, a.parts, grid, a.c, dw, db, a.w_bf16);
   return hipGetLastError();
 }

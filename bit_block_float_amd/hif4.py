@@ -9,6 +9,7 @@ Tensors: bf16 inputs are torch.bfloat16 on the GPU; codes are uint8
 for bit; masks are uint8.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -590,6 +591,7 @@ def dequantize_fp8(codes, scales, k=None, out_dtype=torch.float32, out=None, str
     return out
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
 def linear_fp8_workspace_bytes(m, n, k):
     return int(lib().hif4_linear_fp8_workspace_bytes(m, n, k))
 
@@ -622,6 +624,7 @@ def linear_fp8(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=No
     return y
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
 def linear_fp8_backward_workspace_bytes(m, n, k):
     return int(lib().hif4_linear_fp8_backward_workspace_bytes(m, n, k))
 
@@ -741,6 +744,7 @@ def layer_norm_quantize_fp8(x, weight=None, bias=None, eps=1e-6, codes=None, sca
     return codes, scales
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
 def layer_norm_backward_workspace_bytes(rows, c):
     return int(lib().hif4_layer_norm_backward_workspace_bytes(rows, c))
 
