@@ -116,7 +116,7 @@ hif4_status hif4_layer_norm_quantize_fp8(const void* x, int x_dtype, int64_t row
 
 size_t hif4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t c) {
   if (rows < 0 || rows >= (int64_t(1) << 31) || c < 1 || c > kMaxC) return 0;
-  return align256((size_t)hif4_layer_norm_backward_parts(rows) * 2 * (size_t)c * sizeof(float));
+  return align256((size_t)hif4_layer_norm_backward_parts(rows, c) * 2 * (size_t)c * sizeof(float));
 }
 
 hif4_status hif4_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx,

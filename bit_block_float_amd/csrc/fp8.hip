@@ -24,7 +24,7 @@ __device__ __forceinline__ uint32_t max16_u32(uint32_t v) {  // over 16 aligned 
 // lanes a block; the block maximum is formed with DPP moves. One item a thread
 // and no loop, as in quantize_kernel: workgroups retire and are replaced on
 // whichever CUs run ahead.
-template <typename T, bool kVec>
+template <typename T, int kRows>
 __global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(
     const T* __restrict__ x, int64_t ld, int k, uint32_t items_per_row, FastDiv item_div,
     uint32_t total_items, uint4* __restrict__ codes, uint8_t* __restrict__ scales,
@@ -35,8 +35,8 @@ __global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(
   const uint32_t j = it - row * items_per_row;
   const T* src = x + (int64_t)row * ld;
   Run8<T> r0, r1;
-  r0.template load<kVec>(src, (int)j * 16, k);
-  r1.template load<kVec>(src, (int)j * 16 + 8, k);
+  r0.template load<kRows>(src, (int)j * 16, k);
+  r1.template load<kRows>(src, (int)j * 16 + 8, k);
   const uint32_t e = e8m0_of(max8_u32(max(r0.abs_max(), r1.abs_max())));
   const uint2 c0 = r0.encode(e), c1 = r1.encode(e);
   const uint4 w = make_uint4(c0.x, c0.y, c1.x, c1.y);
@@ -48,9 +48,9 @@ __global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(
 // columns 8 (t % 16) .. + 7: a row's 128 columns are 16 consecutive lanes, and
 // the 8 rows of a column are 8 consecutive bytes of the transposed codes,
 // which go through LDS to leave as whole 128-byte lines.
-//  kTile: one scale for the tile; else one per row (kRows) or column (kCols).
-//  kRows: codes [rows][ceil(k/128)*128]; kCols: codes_t [k][ceil(rows/128)*128].
-template <typename T, bool kTile, bool kRows, bool kCols, bool kVec>
+//  kTile: one scale for the tile; else one per row (kAlong) or column (kCols).
+//  kAlong: codes [rows][ceil(k/128)*128]; kCols: codes_t [k][ceil(rows/128)*128].
+template <typename T, bool kTile, bool kAlong, bool kCols, int kRows>
 __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
     const T* __restrict__ x, int64_t ld, int64_t rows, int k, uint32_t tiles_k,
     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t lds,
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
   Run8<T> v[8];
 #pragma unroll
   for (int r = 0; r < 8; ++r)
-    v[r].template load<kVec>(x + min(row0 + r, rows - 1) * ld, col0, k);
+    v[r].template load<kRows>(x + min(row0 + r, rows - 1) * ld, col0, k);
 #pragma unroll
   for (int r = 0; r < 8; ++r) v[r].keep_if(row0 + r < rows);
   uint32_t e_tile = 0;
@@ -99,7 +99,7 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
       e_col[i] = e8m0_of(max(max(part[0][c], part[1][c]), max(part[2][c], part[3][c])));
     }
   }
-  if constexpr (kRows) {
+  if constexpr (kAlong) {
     const int64_t kp = (int64_t)tiles_k * 128;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(256) void dequantize_fp8_kernel(
   }
 }
 
-template <typename T, bool kVec>
+template <typename T, int kRows>
 static hipError_t launch_quantize(const T* x, int64_t rows, int64_t k, int64_t ld, int block_rows,
                                   uint8_t* codes, uint8_t* scales, int64_t lds, uint8_t* codes_t,
                                   uint8_t* scales_t, int64_t lds_t, hipStream_t stream) {
@@ -199,7 +199,7 @@ static hipError_t launch_quantize(const T* x, int64_t rows, int64_t k, int64_t l
     for (int64_t r0 = 0; r0 < rows; r0 += max_rows) {
       const int64_t nr = rows - r0 < max_rows ? rows - r0 : max_rows;
       const uint32_t total = (uint32_t)(nr * ipr);
-      hipLaunchKernelGGL((quantize_fp8_rows_kernel<T, kVec>), dim3((total + 255) / 256), dim3(256),
+      hipLaunchKernelGGL((quantize_fp8_rows_kernel<T, kRows>), dim3((total + 255) / 256), dim3(256),
                          0, stream, x + r0 * ld, ld, (int)k, ipr, fd, total,
                          reinterpret_cast<uint4*>(codes + r0 * kp), scales + r0 * lds, lds);
       const hipError_t e = hipGetLastError();
@@ -211,7 +211,7 @@ static hipError_t launch_quantize(const T* x, int64_t rows, int64_t k, int64_t l
   const dim3 grid((unsigned)tiles), block(256);
   const uint32_t tk = (uint32_t)tiles_k;
 #define HIF4_TILE(tile, r, c)                                                                     \
-  hipLaunchKernelGGL((quantize_fp8_tile_kernel<T, tile, r, c, kVec>), grid, block, 0, stream, x,  \
+  hipLaunchKernelGGL((quantize_fp8_tile_kernel<T, tile, r, c, kRows>), grid, block, 0, stream, x,  \
                      ld, rows, (int)k, tk, codes, scales, lds, codes_t, scales_t, lds_t)
   if (block_rows == 1) {
     if (codes) HIF4_TILE(false, true, true);
@@ -234,13 +234,14 @@ hipError_t hif4_launch_quantize_fp8(const void* x, bool bf16, int64_t rows, int6
                                     int block_rows, uint8_t* codes, uint8_t* scales, int64_t lds,
                                     uint8_t* codes_t, uint8_t* scales_t, int64_t lds_t,
                                     hipStream_t stream) {
-  const bool vec = ((uintptr_t)x & 15) == 0 && ld % (bf16 ? 8 : 4) == 0 &&
-                   k % (bf16 ? 8 : 4) == 0;
-#define HIF4_QUANTIZE(T, v)                                                                     \
-  launch_quantize<T, v>((const T*)x, rows, k, ld, block_rows, codes, scales, lds, codes_t,       \
-                        scales_t, lds_t, stream)
-  if (bf16) return vec ? HIF4_QUANTIZE(uint16_t, true) : HIF4_QUANTIZE(uint16_t, false);
-  return vec ? HIF4_QUANTIZE(float, true) : HIF4_QUANTIZE(float, false);
+  const int64_t piece = bf16 ? 8 : 4;
+  const bool vec = ((uintptr_t)x & 15) == 0 && ld % piece == 0 && k % piece == 0;
+#define HIF4_QUANTIZE(T, mode)                                                                  \
+  launch_quantize<T, mode>((const T*)x, rows, k, ld, block_rows, codes, scales, lds, codes_t,    \
+                           scales_t, lds_t, stream)
+  if (vec) return bf16 ? HIF4_QUANTIZE(uint16_t, kAligned) : HIF4_QUANTIZE(float, kAligned);
+  if (k >= 8) return bf16 ? HIF4_QUANTIZE(uint16_t, kAny) : HIF4_QUANTIZE(float, kAny);
+  return bf16 ? HIF4_QUANTIZE(uint16_t, kTiny) : HIF4_QUANTIZE(float, kTiny);
 #undef HIF4_QUANTIZE
 }
 

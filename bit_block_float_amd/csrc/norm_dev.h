@@ -43,6 +43,6 @@ struct NormBackArgs {
 }  // namespace hif4
 
 hipError_t hif4_launch_layer_norm(const hif4::NormArgs& a, bool x_bf16, int out, hipStream_t stream);
-int hif4_layer_norm_backward_parts(int64_t rows);
+int hif4_layer_norm_backward_parts(int64_t rows, int64_t c);
 hipError_t hif4_launch_layer_norm_backward(const hif4::NormBackArgs& a, bool x_bf16, void* dw,
                                            void* db, hipStream_t stream);
