@@ -233,6 +233,16 @@ hif4_status hif4_linear_fp8_backward(const void* dy, int dy_dtype, int64_t lddy,
         dw ? (uint8_t*)ws + p.scales_t : nullptr, p.lds_t, stream));
     if (st != HIF4_OK) return st;
   }
+  if (dx && dw && m > 0 && n > 0 && k > 0) {
+    // the longer tiles (fp32 dW's, where dX is bf16) first
+    return launched(hif4_launch_gemm_fp8_two(
+        Fp8Product{codes_t, (const uint8_t*)(ws + p.scales_t), p.lds_t, xt_codes, xt_scales, ldxt,
+                   false, 1, n, k, p.mp, dw, dw_dtype == HIF4_BF16},
+        Fp8Product{codes, codes + p.scales, p.lds, wt_codes, wt_scales, ldwt,
+                   wt_scale_type == HIF4_SCALE_F32, (int)wt_block_rows, m, k, p.np, dx,
+                   dx_dtype == HIF4_BF16},
+        ws + p.product, stream));
+  }
   if (dx) {
     st = run_linear(codes, codes + p.scales, p.lds, wt_codes, wt_scales, ldwt, wt_scale_type,
                     wt_block_rows, m, k, p.np, dx, dx_dtype, ws + p.product, stream);

@@ -247,3 +247,18 @@ hipError_t hif4_launch_gemm_fp8(const uint8_t* x, const uint8_t* xs, int64_t ldx
                                 const void* ws, int64_t ldws, bool ws_f32, int w_block, int64_t m,
                                 int64_t n, int64_t k, void* y, bool y_bf16, void* workspace,
                                 hipStream_t stream);
+// A product of the two-product launcher (sizes above 0).
+struct Fp8Product {
+  const uint8_t *x, *xs;
+  int64_t ldxs;
+  const uint8_t* w;
+  const void* ws;
+  int64_t ldws;
+  bool ws_f32;
+  int w_block;
+  int64_t m, n, k;
+  void* y;
+  bool y_bf16;
+};
+hipError_t hif4_launch_gemm_fp8_two(const Fp8Product& a, const Fp8Product& b, void* workspace,
+                                    hipStream_t stream);

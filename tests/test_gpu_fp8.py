@@ -364,3 +364,22 @@ def test_stream_of_its_own(hip):
         del xq
     s.synchronize()
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("m,n,k,dtype", [(4100, 4196, 4097, torch.bfloat16), (4224, 4096, 4099, torch.float32)])
+def test_linear_backward_large(hip, m, n, k, dtype):
+    """Both products large enough for one launch of the two: the same as one by one."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dy = (1e-3 * torch.randn((m, n), generator=g, device="cuda")).to(dtype)
+    xt = hip.quantize_fp8(torch.randn((m, k), generator=g, device="cuda"), transposed=True)
+    wt = hip.quantize_fp8(0.02 * torch.randn((n, k), generator=g, device="cuda"), block_rows=128, transposed=True)
+    dx, dw = hip.linear_fp8_backward(dy, *xt, *wt)
+    codes, scales, codes_t, scales_t = hip.quantize_fp8_both(dy)
+    assert torch.equal(dx, hip.linear_fp8(codes, scales, *wt, y_dtype=dtype))
+    assert torch.equal(dw, hip.linear_fp8(codes_t, scales_t, *xt))
+    rows = torch.tensor([0, 1000, m - 1])
+    _check_product(dx[rows.cuda()], ref64.fp8_values(_bytes(codes), _bytes(scales))[rows],
+                   ref64.fp8_values(_bytes(wt[0]), _bytes(wt[1]), 128))
+    rows = torch.tensor([0, 2047, n - 1])
+    _check_product(dw[rows.cuda()], ref64.fp8_values(_bytes(codes_t), _bytes(scales_t))[rows],
+                   ref64.fp8_values(_bytes(xt[0]), _bytes(xt[1])))
