@@ -56,10 +56,10 @@ __device__ __forceinline__ gf32x4_t mfma16(i32x8_t a, i32x8_t b, gf32x4_t c, int
 // This wave's loads but the newest n have landed, its LDS reads are done.
 template <int n>
 __device__ __forceinline__ void wait_loads() {
-  static_assert(n == 0 || n == 10 || n == 18, "one asm a count");
+  static_assert(n == 0 || n == 5 || n == 10, "one asm a count");
   if constexpr (n == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  if constexpr (n == 5) asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)" ::: "memory");
   if constexpr (n == 10) asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)" ::: "memory");
-  if constexpr (n == 18) asm volatile("s_waitcnt vmcnt(18) lgkmcnt(0)" ::: "memory");
 }
 
 // 8 codes (two words) as bf16 times the power of two `s`.
@@ -754,20 +754,34 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
   }
 }
 
-// Which kernel, from the sizes alone.
-enum GemmKind { kSkinny, kSmall, kMiddle, kLarge };
+// Which kernel, from the sizes alone. Measured at k = 5120, bf16 Y (the same order
+// with fp32), in us:
+//   m x n           64 x 64   128, 2 a CU   128, 1 a CU   256 x 256
+//   512 x 5120         32          31            26           50
+//   512 x 13824        69          40            52           51
+//   1024 x 5120        53          38            50           51
+//   2048 x 5120        98          68            76           53
+//   1024 x 13824      133          77           104           59
+// A round of 256 tiles of 256 x 256 costs 4/3 of one of 512 tiles of 128 x 128.
+// Splitting K pays for its second kernel from some 16 blocks a part: 300 x 700 x
+// 13824 30 us whole, 20 in 2 parts, 16 in 4, 19 in 9; 200 x 2048 x 2048 8.0 us
+// whole, 9.5 in 2.
+enum GemmKind { kSkinny, kSmall, kOneRound, kMiddle, kLarge };
 struct GemmPlan {
   GemmKind kind;
   int splits, per_split;  // of K's blocks
 };
+constexpr int64_t kCus = 256;
 static GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k) {
   const int64_t kb = k / 128;
   const auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
   if (m <= kSkinnyRows) return {kSkinny, 1, (int)kb};
-  if (tiles(256) >= 256) return {kLarge, 1, (int)kb};
-  if (tiles(128) >= 256) return {kMiddle, 1, (int)kb};
-  // parts of at least 4 blocks, while the chip (two workgroups a CU) has room
-  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles(64), kb / 4));
+  const int64_t t128 = tiles(128);
+  if (4 * ((tiles(256) + kCus - 1) / kCus) < 3 * ((t128 + 2 * kCus - 1) / (2 * kCus)))
+    return {kLarge, 1, (int)kb};
+  if (t128 > kCus) return {kMiddle, 1, (int)kb};
+  if (t128 >= kCus / 2) return {kOneRound, 1, (int)kb};
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kCus / tiles(64), kb / 16));
   const int64_t per = (kb + splits - 1) / splits;
   return {kSmall, (int)((kb + per - 1) / per), (int)per};
 }
@@ -791,7 +805,6 @@ static hipError_t launch_gemm(const uint8_t* x, const uint8_t* xs, int64_t ldxs,
                        dim3(tm * tn, plan.splits), dim3(wm * wn * 64), 0, stream, x, xs, ldxs,   \
                        w, ws, ldws, w_shift, m, n, (int)k, out, tm, tn, plan.per_split);         \
   } while (0)
-  constexpr int64_t kCus = 256;
   const int64_t per_cu = (n + 16 * kCus - 1) / (16 * kCus);
   const int cols = (int)((n + kCus * per_cu - 1) / (kCus * per_cu));  // 1 .. 16
   switch (plan.kind) {
@@ -810,6 +823,7 @@ static hipError_t launch_gemm(const uint8_t* x, const uint8_t* xs, int64_t ldxs,
       }
       break;
     case kMiddle: HIF4_TILED(128, 128, 2, 2, 2, kBf16, y); break;
+    case kOneRound: HIF4_TILED(128, 128, 2, 4, 3, kBf16, y); break;
     case kSmall:
       if (plan.splits == 1) {
         HIF4_TILED(64, 64, 2, 2, 4, kBf16, y);

@@ -177,14 +177,16 @@ def test_linear_few_rows_many_columns(hip, m, n, kind):
 
 
 @pytest.mark.parametrize("kind", ["tiles", "rows", "f32"])
-@pytest.mark.parametrize("m,n,k", [(4100, 4099, 128), (4352, 4096, 640), (2048, 9000, 384)])
+@pytest.mark.parametrize("m,n,k", [(4100, 4099, 128), (4352, 4096, 640), (2048, 9000, 384), (2300, 4099, 256),
+                                   (2100, 1300, 512), (1400, 3001, 640), (1290, 1700, 896), (650, 330, 4224)])
 def test_linear_many_tiles(hip, m, n, k, kind):
-    """Enough tiles for the large-tile kernel, ragged at both ends."""
+    """Every tile kernel (256, 128 by two and by one a CU, 64 whole and with K split),
+    ragged at both ends."""
     args, xv, wv = _linear_case(hip, m, n, k, kind, seed=3)
     y = hip.linear_fp8(*args)
-    rows = torch.tensor([0, 1, 31, 32, 127, 128, 255, 256, 1000, 2047, m - 2, m - 1])
+    rows = torch.tensor([0, 1, 31, 32, 127, 128, 255, 256, min(1000, m - 3), m // 2, m - 2, m - 1])
     _check_product(y[rows.cuda()], xv[rows], wv)
-    cols = torch.tensor([0, 5, 63, 64, 255, 256, 2000, 4000, n - 1])
+    cols = torch.tensor([0, 5, 63, 64, 255, 256, n // 2, min(4000, n - 2), n - 1])
     _check_product(y[:, cols.cuda()], xv, wv[cols])
 
 
