@@ -652,7 +652,7 @@ void gemm_fp8_big_kernel(GemmArgs a) {
 // Two products in one launch, `first` workgroups of the first: the CUs that the
 // first one's last round of tiles leaves idle begin with the second. Measured on
 // the two gradients of an 8192 x 5120 x 5120 layer (400 tiles of fp32 dW, 640 of
-// bf16 dX): two launches PAIR_A us, one PAIR_B us.
+// bf16 dX), best of nine: two launches 353 + 188 us, one 487 us.
 template <bool kBf16A, bool kBf16B>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_fp8_pair_kernel(GemmArgs a, GemmArgs b, uint32_t first) {

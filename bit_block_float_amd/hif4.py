@@ -473,7 +473,7 @@ def _up128(v):
 
 def _empty_scales(rows, blocks, device):
     full = torch.empty((rows, (blocks + 3) // 4 * 4), dtype=torch.float8_e8m0fnu, device=device)
-    return full[:, :blocks]
+    return full if blocks % 4 == 0 else full[:, :blocks]
 
 
 def _check_out(t, name, shape, dtype):
@@ -686,11 +686,11 @@ def layer_norm(x, weight=None, bias=None, eps=1e-6, y=None, stream=None):
     wd = _check_affine(weight, bias, c)
     with _On(x, stream, weight, bias, y) as st:
         if y is None:
-            y = torch.empty((rows, c), dtype=x.dtype, device=x.device)
+            y = x.new_empty((rows, c))
         elif y.dtype != x.dtype or y.shape != x.shape or (c > 1 and y.stride(1) != 1):
             raise ValueError("y must have x's dtype and shape and unit column stride")
-        mean = torch.empty((rows,), dtype=torch.float32, device=x.device)
-        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        mean = x.new_empty((rows,), dtype=torch.float32)
+        rstd = torch.empty_like(mean)
         _ok(lib().hif4_layer_norm(_at(x), _DTYPE[x.dtype], rows, c, _ld(x), _at(weight),
                                   _at(bias), wd, float(eps), _at(y), _ld(y), _at(mean),
                                   _at(rstd), st), "hif4_layer_norm")
@@ -762,10 +762,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, workspace=None, stream=N
             raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(rows,)}")
     wd = _check_affine(weight, None, c)
     with _On(x, stream, dy, mean, rstd, weight, workspace) as st:
-        dx = torch.empty((rows, c), dtype=x.dtype, device=x.device)
-        wdt = weight.dtype if weight is not None else torch.float32
-        dweight = torch.empty((c,), dtype=wdt, device=x.device)
-        dbias = torch.empty((c,), dtype=wdt, device=x.device)
+        dx = x.new_empty((rows, c))
+        dweight = torch.empty_like(weight) if weight is not None else mean.new_empty((c,))
+        dbias = torch.empty_like(dweight)
         if workspace is None:
             need = max(layer_norm_backward_workspace_bytes(rows, c), 1)
             workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
