@@ -264,8 +264,9 @@ __device__ __forceinline__ void gemm_fp8_tile(
 
   const int frow = lane & 31, fhalf = lane >> 5, fsw = (frow >> 1) & 7;
   const int xrow = wm * (BM / kWM) + frow, wrow = wn * (BN / kWN) + frow;
+  // kF32Scale: the wave's one block row (the last one where all its columns are past N)
   const float* wsf = reinterpret_cast<const float*>(WS) +
-                     (int64_t)((n0 + wn * (BN / kWN)) >> 7) * ldws;  // kF32Scale: one block row
+                     (min(n0 + wn * (BN / kWN), N - 1) >> 7) * ldws;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) load_stage(kb0 + s, s);
   int slot = 0;

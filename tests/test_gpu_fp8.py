@@ -190,6 +190,20 @@ def test_linear_many_tiles(hip, m, n, k, kind):
     _check_product(y[:, cols.cuda()], xv, wv[cols])
 
 
+@pytest.mark.parametrize("n", [5248, 5121, 5250])
+def test_linear_float_scales_end_inside_a_tile(hip, n):
+    """Tiles of 256 columns of which the last block row of scales covers only the first half:
+    the rows behind it belong to others."""
+    m, k = 2048, 256
+    (xc, xs, wc, ws), xv, wv = _linear_case(hip, m, n, k, "f32", seed=n)
+    more = torch.full((ws.shape[0] + 4, ws.shape[1]), float("nan"), device="cuda")
+    more[:ws.shape[0]] = ws
+    rows = torch.tensor([0, 255, 256, 1000, m - 1])
+    for out in (torch.float32, torch.bfloat16):
+        y = hip.linear_fp8(xc, xs, wc, more[:ws.shape[0]], y_dtype=out)
+        _check_product(y[rows.cuda()], xv[rows], wv)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 5120, 13824), (16, 1280, 13824), (300, 700, 13824)])
 def test_linear_long_sum(hip, m, n, k):
     args, xv, wv = _linear_case(hip, m, n, k, "tiles", seed=9)
