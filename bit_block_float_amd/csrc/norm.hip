@@ -178,7 +178,7 @@ __device__ __forceinline__ float tree_sum(const float (&v)[N]) {
   return (a + b) + (c + d);
 }
 
-// Forward that ends in a quantizer, bf16 rows of up to 8192 columns, many of them.
+// Forward that ends in a quantizer, many bf16 rows of 4097 to 6144 columns.
 // A wave owns a row (its lanes items n * 64 + lane), so nothing in the row loop
 // waits for another wave: the encoders need too many registers for the kernel
 // below to hide its barriers and loads behind other rows. Weight and bias are in
@@ -600,58 +600,67 @@ __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(const float* __r
   }
 }
 
+// Which forward kernel, by measurement on bf16 rows (us).
+// Rows at once of layer_norm_rows_kernel, to the type itself unless named:
+//   rows x columns     1      2      4
+//   256 x 5120        7.5    7.5
+//   512 x 13824      15.0   11.4
+//   2048 x 5120      15.1   12.9   12.7
+//   8192 x 5120        36     35     42
+//   57600 x 1024       40     37     89
+//   57600 x 5120      271    235    247
+//   57600 x 13824     774    674    656
+//   fp32 57600 x 5120 582    561    744
+//   HiF4 57600 x 8192 348    323    403
+// so two, from two rows a CU on. Rows that are not 16-byte aligned (5119 columns):
+// bf16 292 and 267, fp32 641 and 759, so fp32 takes one there.
+// A wave per row against it, into a quantizer: HiF4 57600 x 5120 215 and 315,
+// 57600 x 6144 295 and 349, 2048 x 5120 12.5 and 17.8, 1024 x 5120 11.5 and 10.2;
+// but 57600 x 4096 185 and 163, 57600 x 8192 486 and 323 (E4M3 the same way: 176 and
+// 213, 226 and 258, 144 and 139, 329 and 286): workgroups of 5 and 6 waves leave the
+// SIMDs of a CU unevenly filled, 4 and 8 do not.
 template <typename T, int kOut, int kRows>
 static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   const int items = kOut == kOutFp8 ? a.kp / 16 : (a.c + 15) / 16;
+  const int waves = (items + 63) / 64;
+#define HIF4_NORM(rr, multi, grid, waves)                                                  \
+  hipLaunchKernelGGL((layer_norm_rows_kernel<T, rr, kOut, multi, kRows>), dim3(grid),      \
+                     dim3(64 * (waves)), 0, stream, a)
   if constexpr (kRows == kTiny) {  // c < 8
-    const unsigned tiny = (unsigned)std::min<int64_t>(a.rows, 256 * 64);
-    hipLaunchKernelGGL((layer_norm_rows_kernel<T, 1, kOut, false, kTiny>), dim3(tiny), dim3(64), 0,
-                       stream, a);
+    HIF4_NORM(1, false, (unsigned)std::min<int64_t>(a.rows, 256 * 64), 1);
     return hipGetLastError();
   } else {
-  if (items > 1024) {
-    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 256 * 32);
-    hipLaunchKernelGGL((layer_norm_wide_kernel<T, 4, kOut, kRows>), dim3(grid), dim3(1024), 0, stream, a);
-    return hipGetLastError();
-  }
-  const int waves = (items + 63) / 64;
-  if constexpr (sizeof(T) == 2 && kRows == kAligned && kOut != kOutY) {
-    if (waves > 1 && waves <= 8 && a.rows >= 256 * 8) {
-      const dim3 grid((unsigned)std::min<int64_t>((a.rows + 7) / 8, 256 * 8)), block(512);
-      const size_t lds = (size_t)items * 8 * sizeof(float4);
-#define HIF4_WAVE(n) \
-  hipLaunchKernelGGL((layer_norm_wave_kernel<n, kOut>), grid, block, lds, stream, a)
-      switch (waves) {
-        case 2: HIF4_WAVE(2); break;
-        case 3: HIF4_WAVE(3); break;
-        case 4: HIF4_WAVE(4); break;
-        case 5: HIF4_WAVE(5); break;
-        case 6: HIF4_WAVE(6); break;
-        default: HIF4_WAVE(8); break;
-      }
-#undef HIF4_WAVE
+    if (items > 1024) {
+      const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 256 * 32);
+      hipLaunchKernelGGL((layer_norm_wide_kernel<T, 4, kOut, kRows>), dim3(grid), dim3(1024), 0,
+                         stream, a);
       return hipGetLastError();
     }
-  }
-  // rows at once (fp32 rows fill twice the registers, shifted ones more)
-  constexpr int kMany = kRows != kAligned ? 1 : sizeof(T) == 2 ? 4 : 2;
-  const bool many = a.rows >= 256 * 8 * 4;
-  const int r = many ? kMany : 1;
-  const unsigned grid =
-      (unsigned)std::min<int64_t>((a.rows + r - 1) / r, (int64_t)256 * 64 / waves);
-#define HIF4_NORM(rr, multi)                                                              \
-  hipLaunchKernelGGL((layer_norm_rows_kernel<T, rr, kOut, multi, kRows>), dim3(grid), dim3(64 * waves), 0, \
-                     stream, a)
-  if (many) {
-    if (waves > 1) HIF4_NORM(kMany, true);
-    else HIF4_NORM(kMany, false);
-  } else {
-    if (waves > 1) HIF4_NORM(1, true);
-    else HIF4_NORM(1, false);
+    if constexpr (sizeof(T) == 2 && kRows == kAligned && kOut != kOutY) {
+      if ((waves == 5 || waves == 6) && a.rows >= 256 * 8) {
+        const dim3 grid((unsigned)std::min<int64_t>((a.rows + 7) / 8, 256 * 8)), block(512);
+        const size_t lds = (size_t)items * 8 * sizeof(float4);
+        if (waves == 5)
+          hipLaunchKernelGGL((layer_norm_wave_kernel<5, kOut>), grid, block, lds, stream, a);
+        else
+          hipLaunchKernelGGL((layer_norm_wave_kernel<6, kOut>), grid, block, lds, stream, a);
+        return hipGetLastError();
+      }
+    }
+    constexpr int kMany = kRows == kAligned || sizeof(T) == 2 ? 2 : 1;
+    const int r = a.rows >= 256 * 2 ? kMany : 1;
+    const unsigned grid =
+        (unsigned)std::min<int64_t>((a.rows + r - 1) / r, (int64_t)256 * 64 / waves);
+    if (r == kMany) {
+      if (waves > 1) HIF4_NORM(kMany, true, grid, waves);
+      else HIF4_NORM(kMany, false, grid, 1);
+    } else {
+      if (waves > 1) HIF4_NORM(1, true, grid, waves);
+      else HIF4_NORM(1, false, grid, 1);
+    }
+    return hipGetLastError();
   }
 #undef HIF4_NORM
-  return hipGetLastError();
-  }
 }
 
 // Runs of 8 columns a thread, and threads a workgroup, of the backward.

@@ -117,6 +117,16 @@ def test_forward_strides_and_surroundings(hip, ld, offset, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [511, 512, 513, 2051])
+@pytest.mark.parametrize("c", [5, 1003, 1024, 4104, 5119])
+def test_forward_rows_at_once(hip, c, rows, dtype):
+    """Workgroups that take two rows, the last of them one."""
+    x, (w, b) = _x(rows, c, rows, dtype), _affine(c, torch.bfloat16)
+    y, mean, rstd = hip.layer_norm(*_cuda(x, w, b), eps=EPS)
+    _check_forward(x, w, b, y, mean, rstd, HALF[dtype])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("c", [64, 192, 1024, 1088, 2048, 5120, 8192, 13824, 16448])
 def test_quantizing_forms_are_the_two_calls(hip, c, dtype):
     for rows, wd in ((1, None), (70, torch.float32)):
@@ -149,7 +159,7 @@ def test_fp8_form_is_the_two_calls(hip, c, dtype):
         assert torch.equal(gs.contiguous().view(torch.uint8), ws.contiguous().view(torch.uint8))
 
 
-@pytest.mark.parametrize("c", [1024, 1088, 2048, 3136, 4096, 5120, 6208, 8192, 13824])
+@pytest.mark.parametrize("c", [1024, 1088, 2048, 3136, 4096, 4160, 5120, 5184, 6144, 6208, 8192, 13824])
 def test_quantizing_forms_are_the_two_calls_over_many_rows(hip, c):
     rows = 2100 if c > 4096 else 8200
     x, w, b = _cuda(_x(rows, c, c), *_affine(c, torch.float32))
