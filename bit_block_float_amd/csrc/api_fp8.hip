@@ -137,9 +137,10 @@ hif4_status run_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t 
     const size_t bytes = (size_t)m * (size_t)n * (y_dtype == HIF4_BF16 ? 2 : 4);
     return launched(hif4_launch_zero(y, bytes, stream));
   }
-  return launched(hif4_launch_gemm_fp8(x_codes, x_scales, ldxs, w_codes, w_scales, ldws,
-                                       w_scale_type == HIF4_SCALE_F32, (int)w_block_rows, m, n, k,
-                                       y, y_dtype == HIF4_BF16, workspace, stream));
+  return launched(hif4_launch_gemm_fp8(
+      Fp8Product{x_codes, x_scales, ldxs, w_codes, w_scales, ldws, w_scale_type == HIF4_SCALE_F32,
+                 (int)w_block_rows, m, n, k, y, y_dtype == HIF4_BF16},
+      workspace, stream));
 }
 
 }  // namespace

@@ -243,11 +243,7 @@ hipError_t hif4_launch_dequantize_fp8(const uint8_t* codes, const void* scales, 
                                       int block_rows, int64_t lds, int64_t rows, int64_t k,
                                       void* out, bool out_bf16, hipStream_t stream);
 size_t hif4_gemm_fp8_ws_bytes(int64_t m, int64_t n, int64_t k);
-hipError_t hif4_launch_gemm_fp8(const uint8_t* x, const uint8_t* xs, int64_t ldxs, const uint8_t* w,
-                                const void* ws, int64_t ldws, bool ws_f32, int w_block, int64_t m,
-                                int64_t n, int64_t k, void* y, bool y_bf16, void* workspace,
-                                hipStream_t stream);
-// A product of the two-product launcher (sizes above 0).
+// A product Y = X W^T (sizes above 0).
 struct Fp8Product {
   const uint8_t *x, *xs;
   int64_t ldxs;
@@ -260,5 +256,6 @@ struct Fp8Product {
   void* y;
   bool y_bf16;
 };
+hipError_t hif4_launch_gemm_fp8(const Fp8Product& p, void* workspace, hipStream_t stream);
 hipError_t hif4_launch_gemm_fp8_two(const Fp8Product& a, const Fp8Product& b, void* workspace,
                                     hipStream_t stream);

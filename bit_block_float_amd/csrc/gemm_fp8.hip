@@ -62,6 +62,14 @@ __device__ __forceinline__ void wait_loads() {
   if constexpr (n == 10) asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)" ::: "memory");
 }
 
+// Direct-to-LDS loads of 16 (4) bytes a lane, to `dst` + 16 (4) * lane.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t voff, int off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (glds_void_t*)dst, 16, voff, off, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char* dst, uint32_t voff, int off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (glds_void_t*)dst, 4, voff, off, 0, 0);
+}
+
 // 8 codes (two words) as bf16 times the power of two `s`.
 __device__ __forceinline__ gbf16x8_t widen(uint32_t lo, uint32_t hi, float s) {
   const bf16x8_words_t w = {
@@ -178,6 +186,20 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
   tn = __builtin_amdgcn_readfirstlane(in / gsize);
 }
 
+// A product, cut into tiles_m x tiles_n tiles of Y.
+struct GemmArgs {
+  const uint8_t *x, *xs;
+  int64_t ldxs;
+  const uint8_t* w;
+  const void* ws;  // E8M0 bytes, or float32
+  int64_t ldws;
+  int w_shift;
+  int64_t m, n;
+  int k;
+  void* y;
+  uint32_t tiles_m, tiles_n;
+};
+
 // Tile kernel, for products too small for the one below, and for float32 weight
 // scales. BM x BN of Y a workgroup, kWM x kWN waves. A stage is one block of 128
 // along K: rows of 128 bytes = 8 chunks of 16, chunk c of row r in slot
@@ -188,29 +210,34 @@ __device__ __forceinline__ void tile_of(uint32_t t, uint32_t tiles_m, uint32_t t
 // each stage a wave brings one group of 64 scale words (the 4 bytes that hold the
 // block's). Loads past the last block repeat it, into stages that no one reads.
 //
-// blockIdx.y = s: blocks [s per_split, (s + 1) per_split) of K only, the sums to
-// plane s of `Y` as float32 (few tiles and a long K: the parts are added by
+// Part `split`: blocks [split per_split, (split + 1) per_split) of K only, the sums
+// to that plane of Y as float32 (few tiles and a long K: the parts are added by
 // gemm_fp8_reduce_kernel in order).
+template <int BM, int BN, int kStages>
+constexpr int kTileLds = kStages * (BM + BN) * (128 + 4) + 256;  // stages, a sink for idle scale loads
 template <int BM, int BN, int kWM, int kWN, int kStages, bool kF32Scale, bool kFp8, bool kBf16>
-__device__ __forceinline__ void gemm_fp8_tile(
-    const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
-    const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int64_t M,
-    int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n, int per_split) {
+__device__ __forceinline__ void gemm_fp8_tile(const GemmArgs& a, uint32_t tile, int split,
+                                              int per_split, char* const lds) {
+  const uint8_t* __restrict__ const X = a.x;
+  const uint8_t* __restrict__ const XS = a.xs;
+  const uint8_t* __restrict__ const W = a.w;
+  const void* __restrict__ const WS = a.ws;
+  const int64_t ldxs = a.ldxs, ldws = a.ldws, M = a.m, N = a.n;
+  const int w_shift = a.w_shift, K = a.k;
   constexpr int kWaves = kWM * kWN;
   constexpr int kTM = BM / kWM / 32, kTN = BN / kWN / 32;  // 32 x 32 blocks of a wave
   constexpr int kCodes = (BM + BN) * 128, kStage = kCodes + (BM + BN) * 4;
   constexpr int kGroups = (kF32Scale ? BM : BM + BN) / 64;  // of 64 scale words
   static_assert(kGroups <= kWaves, "one group a wave");
-  __shared__ __attribute__((aligned(1024))) char lds[kStages * kStage + 256];  // + a sink
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / kWN, wn = wave % kWN;
   int64_t m0, n0;
-  tile_of(blockIdx.x, tiles_m, tiles_n, m0, n0);
+  tile_of(tile, a.tiles_m, a.tiles_n, m0, n0);
   m0 *= BM;
   n0 *= BN;
-  const int kb0 = (int)blockIdx.y * per_split, kb1 = min(kb0 + per_split, K / 128);
+  const int kb0 = split * per_split, kb1 = min(kb0 + per_split, K / 128);
 
   const int mrows = (int)min((int64_t)BM, M - m0), nrows = (int)min((int64_t)BN, N - n0);
   const __amdgpu_buffer_rsrc_t rx =
@@ -242,16 +269,12 @@ __device__ __forceinline__ void gemm_fp8_tile(
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       if (i < kXLoads)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rx, (glds_void_t*)(base + (wave * kXLoads + i) * 1024), 16, voff[i], blk * 128, 0, 0);
+        load_lds16(rx, base + (wave * kXLoads + i) * 1024, voff[i], blk * 128);
       else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rw, (glds_void_t*)(base + BM * 128 + (wave * (kLoads - kXLoads) + i - kXLoads) * 1024),
-            16, voff[i], blk * 128, 0, 0);
+        load_lds16(rw, base + BM * 128 + (wave * (kLoads - kXLoads) + i - kXLoads) * 1024, voff[i],
+                   blk * 128);
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rs, (glds_void_t*)(has ? base + kCodes + wave * 256 : lds + kStages * kStage), 4, soff,
-        (blk >> 2) * 4, 0, 0);
+    load_lds4(rs, has ? base + kCodes + wave * 256 : lds + kStages * kStage, soff, (blk >> 2) * 4);
   };
 
   gf32x16_t acc[kTN][kTM];
@@ -395,20 +418,30 @@ __device__ __forceinline__ void gemm_fp8_tile(
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  static_assert(kWaves * kStageBytes<kBf16, kTN> <= (int)sizeof(lds), "epilogue stage");
-  char* const y = reinterpret_cast<char*>(Y) + (int64_t)blockIdx.y * M * N * (kBf16 ? 2 : 4);
+  static_assert(kWaves * kStageBytes<kBf16, kTN> <= kTileLds<BM, BN, kStages>, "epilogue stage");
+  char* const y = reinterpret_cast<char*>(a.y) + split * M * N * (kBf16 ? 2 : 4);
   store_tile<kBf16, kTN, kTM>(acc, lds + wave * kStageBytes<kBf16, kTN>, y, m0 + wm * (BM / kWM),
                               n0 + wn * (BN / kWN), M, N, lane);
 }
 
-// (The body is a device function: the host pass cannot instantiate it.)
 template <int BM, int BN, int kWM, int kWN, int kStages, bool kF32Scale, bool kFp8, bool kBf16>
-__global__ __launch_bounds__(kWM* kWN * 64) void gemm_fp8_tile_kernel(
-    const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
-    const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int64_t M,
-    int64_t N, int K, void* __restrict__ Y, uint32_t tiles_m, uint32_t tiles_n, int per_split) {
-  gemm_fp8_tile<BM, BN, kWM, kWN, kStages, kF32Scale, kFp8, kBf16>(
-      X, XS, ldxs, W, WS, ldws, w_shift, M, N, K, Y, tiles_m, tiles_n, per_split);
+__global__ __launch_bounds__(kWM* kWN * 64) void gemm_fp8_tile_kernel(GemmArgs a, int per_split) {
+  __shared__ __attribute__((aligned(1024))) char lds[kTileLds<BM, BN, kStages>];
+  gemm_fp8_tile<BM, BN, kWM, kWN, kStages, kF32Scale, kFp8, kBf16>(a, blockIdx.x, (int)blockIdx.y,
+                                                                  per_split, lds);
+}
+
+// Two products in one launch, the first with `first` tiles: few tiles leave CUs idle
+// that the second's can have.
+template <int BM, int BN, int kWM, int kWN, int kStages, bool kBf16A, bool kBf16B>
+__global__ __launch_bounds__(kWM* kWN * 64) void gemm_fp8_tile_pair_kernel(GemmArgs a, GemmArgs b,
+                                                                           uint32_t first) {
+  __shared__ __attribute__((aligned(1024))) char lds[kTileLds<BM, BN, kStages>];
+  if (blockIdx.x < first)
+    gemm_fp8_tile<BM, BN, kWM, kWN, kStages, false, kBf16A, kBf16A>(a, blockIdx.x, 0, a.k / 128, lds);
+  else
+    gemm_fp8_tile<BM, BN, kWM, kWN, kStages, false, kBf16B, kBf16B>(b, blockIdx.x - first, 0,
+                                                                    b.k / 128, lds);
 }
 
 // Y = sum of `splits` float32 planes, in order; 4 elements a thread.
@@ -453,24 +486,12 @@ constexpr int kBigSlot = 2 * 256 * 128;
 constexpr int kBigScaleRing = 2 * 256 * 4;
 constexpr int kBigLds = 2 * kBigSlot + 2 * kBigScaleRing + 1024;  // + a sink for idle scale loads
 
-struct GemmArgs {
-  const uint8_t *x, *xs;
-  int64_t ldxs;
-  const uint8_t *w, *ws;
-  int64_t ldws;
-  int w_shift;
-  int64_t m, n;
-  int k;
-  void* y;
-  uint32_t tiles_m, tiles_n;
-};
-
 template <bool kBf16>
 __device__ __forceinline__ void gemm_fp8_big(const GemmArgs& a, uint32_t tile, char* const lds) {
   const uint8_t* __restrict__ const X = a.x;
   const uint8_t* __restrict__ const XS = a.xs;
   const uint8_t* __restrict__ const W = a.w;
-  const uint8_t* __restrict__ const WS = a.ws;
+  const uint8_t* __restrict__ const WS = (const uint8_t*)a.ws;
   const int64_t ldxs = a.ldxs, ldws = a.ldws, M = a.m, N = a.n;
   const int w_shift = a.w_shift, K = a.k;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -787,112 +808,118 @@ static GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k) {
   return {kSmall, (int)((kb + per - 1) / per), (int)per};
 }
 
-static GemmArgs large_args(const uint8_t* x, const uint8_t* xs, int64_t ldxs, const uint8_t* w,
-                           const void* ws, int64_t ldws, int w_shift, int64_t m, int64_t n,
-                           int64_t k, void* y) {
-  return GemmArgs{x, xs, ldxs, w, (const uint8_t*)ws, ldws, w_shift, m, n, (int)k, y,
-                  (uint32_t)((m + 255) / 256), (uint32_t)((n + 255) / 256)};
+static GemmArgs gemm_args(const Fp8Product& p, int64_t tile, void* y) {
+  return GemmArgs{p.x, p.xs, p.ldxs, p.w, p.ws, p.ldws, p.w_block == 128 ? 7 : 0, p.m, p.n, (int)p.k,
+                  y, (uint32_t)((p.m + tile - 1) / tile), (uint32_t)((p.n + tile - 1) / tile)};
+}
+
+// The tile kernels by kind: tile rows and columns, waves both ways, stages.
+#define HIF4_SMALL 64, 64, 2, 2, 4
+#define HIF4_ONE_ROUND 128, 128, 2, 4, 3
+#define HIF4_MIDDLE 128, 128, 2, 2, 2
+#define HIF4_LARGE_F32 256, 256, 2, 4, 2
+
+template <int BM, int BN, int kWM, int kWN, int kStages, bool kF32Scale, bool kFp8, bool kBf16>
+static void launch_tiles(const Fp8Product& p, const GemmPlan& plan, void* y, hipStream_t stream) {
+  const GemmArgs a = gemm_args(p, BM, y);
+  hipLaunchKernelGGL((gemm_fp8_tile_kernel<BM, BN, kWM, kWN, kStages, kF32Scale, kFp8, kBf16>),
+                     dim3(a.tiles_m * a.tiles_n, plan.splits), dim3(kWM * kWN * 64), 0, stream, a,
+                     plan.per_split);
 }
 
 template <bool kF32Scale, bool kBf16>
-static hipError_t launch_gemm(const uint8_t* x, const uint8_t* xs, int64_t ldxs, const uint8_t* w,
-                              const void* ws, int64_t ldws, int w_shift, int64_t m, int64_t n,
-                              int64_t k, void* y, void* workspace, hipStream_t stream) {
-  const GemmPlan plan = plan_gemm(m, n, k);
-#define HIF4_TILED(bm, bn, wm, wn, st, bf16, out)                                                \
-  do {                                                                                           \
-    const uint32_t tm = (uint32_t)((m + bm - 1) / bm), tn = (uint32_t)((n + bn - 1) / bn);       \
-    hipLaunchKernelGGL((gemm_fp8_tile_kernel<bm, bn, wm, wn, st, kF32Scale, kBf16, bf16>),       \
-                       dim3(tm * tn, plan.splits), dim3(wm * wn * 64), 0, stream, x, xs, ldxs,   \
-                       w, ws, ldws, w_shift, m, n, (int)k, out, tm, tn, plan.per_split);         \
-  } while (0)
-  const int64_t per_cu = (n + 16 * kCus - 1) / (16 * kCus);
-  const int cols = (int)((n + kCus * per_cu - 1) / (kCus * per_cu));  // 1 .. 16
+static hipError_t launch_gemm(const Fp8Product& p, void* workspace, hipStream_t stream) {
+  const GemmPlan plan = plan_gemm(p.m, p.n, p.k);
   switch (plan.kind) {
-    case kSkinny:
+    case kSkinny: {
+      const int64_t per_cu = (p.n + 16 * kCus - 1) / (16 * kCus);
+      const int cols = (int)((p.n + kCus * per_cu - 1) / (kCus * per_cu));  // 1 .. 16
       hipLaunchKernelGGL((gemm_fp8_skinny_kernel<kF32Scale, kBf16>),
-                         dim3((unsigned)((n + cols - 1) / cols)), dim3(kSkinnyWaves * 64), 0,
-                         stream, x, xs, ldxs, w, ws, ldws, w_shift, (int)m, n, (int)k, cols, y);
+                         dim3((unsigned)((p.n + cols - 1) / cols)), dim3(kSkinnyWaves * 64), 0,
+                         stream, p.x, p.xs, p.ldxs, p.w, p.ws, p.ldws, p.w_block == 128 ? 7 : 0,
+                         (int)p.m, p.n, (int)p.k, cols, p.y);
       break;
+    }
     case kLarge:
       if constexpr (kF32Scale) {
-        HIF4_TILED(256, 256, 2, 4, 2, kBf16, y);
+        launch_tiles<HIF4_LARGE_F32, true, kBf16, kBf16>(p, plan, p.y, stream);
       } else {
-        const GemmArgs a = large_args(x, xs, ldxs, w, ws, ldws, w_shift, m, n, k, y);
+        const GemmArgs a = gemm_args(p, 256, p.y);
         hipLaunchKernelGGL(gemm_fp8_big_kernel<kBf16>, dim3(a.tiles_m * a.tiles_n), dim3(256), 0,
                            stream, a);
       }
       break;
-    case kMiddle: HIF4_TILED(128, 128, 2, 2, 2, kBf16, y); break;
-    case kOneRound: HIF4_TILED(128, 128, 2, 4, 3, kBf16, y); break;
+    case kMiddle: launch_tiles<HIF4_MIDDLE, kF32Scale, kBf16, kBf16>(p, plan, p.y, stream); break;
+    case kOneRound: launch_tiles<HIF4_ONE_ROUND, kF32Scale, kBf16, kBf16>(p, plan, p.y, stream); break;
     case kSmall:
       if (plan.splits == 1) {
-        HIF4_TILED(64, 64, 2, 2, 4, kBf16, y);
+        launch_tiles<HIF4_SMALL, kF32Scale, kBf16, kBf16>(p, plan, p.y, stream);
         break;
       }
-      HIF4_TILED(64, 64, 2, 2, 4, false, workspace);
+      launch_tiles<HIF4_SMALL, kF32Scale, kBf16, false>(p, plan, workspace, stream);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
-      hipLaunchKernelGGL(gemm_fp8_reduce_kernel<kBf16>, dim3((unsigned)((m * n + 1023) / 1024)),
-                         dim3(256), 0, stream, (const float*)workspace, plan.splits, m * n, y);
+      hipLaunchKernelGGL(gemm_fp8_reduce_kernel<kBf16>, dim3((unsigned)((p.m * p.n + 1023) / 1024)),
+                         dim3(256), 0, stream, (const float*)workspace, plan.splits, p.m * p.n, p.y);
       break;
   }
-#undef HIF4_TILED
   return hipGetLastError();
+}
+
+// Two products with E8M0 scales in one launch. false: not launched (too many tiles).
+template <bool kBf16A, bool kBf16B>
+static bool launch_pair(const Fp8Product& a, const Fp8Product& b, GemmKind kind, hipStream_t stream) {
+  const int64_t tile = kind == kLarge ? 256 : kind == kSmall ? 64 : 128;
+  const GemmArgs ga = gemm_args(a, tile, a.y), gb = gemm_args(b, tile, b.y);
+  const uint64_t first = (uint64_t)ga.tiles_m * ga.tiles_n;
+  const uint64_t all = first + (uint64_t)gb.tiles_m * gb.tiles_n;
+  if (all >= (1ull << 31)) return false;
+#define HIF4_PAIR(kernel, threads)                                                        \
+  hipLaunchKernelGGL((kernel), dim3((unsigned)all), dim3(threads), 0, stream, ga, gb, (uint32_t)first)
+  switch (kind) {
+    case kLarge: HIF4_PAIR((gemm_fp8_pair_kernel<kBf16A, kBf16B>), 256); return true;
+    case kOneRound:
+    case kMiddle: HIF4_PAIR((gemm_fp8_tile_pair_kernel<HIF4_MIDDLE, kBf16A, kBf16B>), 256); return true;
+    case kSmall: HIF4_PAIR((gemm_fp8_tile_pair_kernel<HIF4_SMALL, kBf16A, kBf16B>), 256); return true;
+    default: return false;
+  }
+#undef HIF4_PAIR
 }
 
 }  // namespace hif4
 
 using namespace hif4;
 
-hipError_t hif4_launch_gemm_fp8(const uint8_t* x, const uint8_t* xs, int64_t ldxs, const uint8_t* w,
-                                const void* ws, int64_t ldws, bool ws_f32, int w_block, int64_t m,
-                                int64_t n, int64_t k, void* y, bool y_bf16, void* workspace,
-                                hipStream_t stream) {
-  const int shift = w_block == 128 ? 7 : 0;
-  if (ws_f32) {
-    return y_bf16 ? launch_gemm<true, true>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, workspace, stream)
-                  : launch_gemm<true, false>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, workspace, stream);
-  }
-  return y_bf16 ? launch_gemm<false, true>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, workspace, stream)
-                : launch_gemm<false, false>(x, xs, ldxs, w, ws, ldws, shift, m, n, k, y, workspace, stream);
+hipError_t hif4_launch_gemm_fp8(const Fp8Product& p, void* workspace, hipStream_t stream) {
+  if (p.ws_f32)
+    return p.y_bf16 ? launch_gemm<true, true>(p, workspace, stream)
+                    : launch_gemm<true, false>(p, workspace, stream);
+  return p.y_bf16 ? launch_gemm<false, true>(p, workspace, stream)
+                  : launch_gemm<false, false>(p, workspace, stream);
 }
 
-// Two independent products, in one launch where both are large with E8M0 scales.
+// Two independent products, in one launch where both have E8M0 scales and take the
+// same kernel whole (two that fill the CUs once with one tile each: the kernel that
+// has two a CU). Measured on the two gradients of a layer, two launches and one, us:
+//   1024 x 1024 x 1024         11.0    7.7
+//   1001 x 1300 x 640 (fp32)   13.5   11.1
+//   2048 x 2048 x 2048         32.5   30.1 (as two rounds of one a CU: 35.3)
+//   2100 x 2200 x 2111         63.9   53.7 (as tiles of 256: 61.1)
+//   8192 x 5120 x 5120          541    487
+// but with tiles that suit only one of them: 200 x 2048 x 2048 13.6 and 15.6,
+// 4096 x 2048 x 2048 61.7 and 79.8.
 hipError_t hif4_launch_gemm_fp8_two(const Fp8Product& a, const Fp8Product& b, void* workspace,
                                     hipStream_t stream) {
-  const auto large = [](const Fp8Product& p) {
-    return !p.ws_f32 && p.m > 0 && p.n > 0 && p.k > 0 && plan_gemm(p.m, p.n, p.k).kind == kLarge;
-  };
-  if (large(a) && large(b)) {
-    const auto args = [](const Fp8Product& p) {
-      return large_args(p.x, p.xs, p.ldxs, p.w, p.ws, p.ldws, p.w_block == 128 ? 7 : 0, p.m, p.n,
-                        p.k, p.y);
-    };
-    const GemmArgs ga = args(a), gb = args(b);
-    const uint64_t first = (uint64_t)ga.tiles_m * ga.tiles_n, all = first + (uint64_t)gb.tiles_m * gb.tiles_n;
-    if (all < (1ull << 31)) {
-#define HIF4_PAIR(ba, bb)                                                                       \
-  hipLaunchKernelGGL((gemm_fp8_pair_kernel<ba, bb>), dim3((unsigned)all), dim3(256), 0, stream, \
-                     ga, gb, (uint32_t)first)
-      if (a.y_bf16) {
-        if (b.y_bf16) HIF4_PAIR(true, true);
-        else HIF4_PAIR(true, false);
-      } else {
-        if (b.y_bf16) HIF4_PAIR(false, true);
-        else HIF4_PAIR(false, false);
-      }
-#undef HIF4_PAIR
-      return hipGetLastError();
-    }
+  const GemmPlan pa = plan_gemm(a.m, a.n, a.k), pb = plan_gemm(b.m, b.n, b.k);
+  if (!a.ws_f32 && !b.ws_f32 && pa.kind == pb.kind && pa.splits == 1 && pb.splits == 1) {
+    const bool done = a.y_bf16 ? (b.y_bf16 ? launch_pair<true, true>(a, b, pa.kind, stream)
+                                           : launch_pair<true, false>(a, b, pa.kind, stream))
+                               : (b.y_bf16 ? launch_pair<false, true>(a, b, pa.kind, stream)
+                                           : launch_pair<false, false>(a, b, pa.kind, stream));
+    if (done) return hipGetLastError();
   }
-  for (const Fp8Product* p : {&a, &b}) {
-    const hipError_t e = hif4_launch_gemm_fp8(p->x, p->xs, p->ldxs, p->w, p->ws, p->ldws, p->ws_f32,
-                                              p->w_block, p->m, p->n, p->k, p->y, p->y_bf16,
-                                              workspace, stream);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  const hipError_t e = hif4_launch_gemm_fp8(a, workspace, stream);
+  return e != hipSuccess ? e : hif4_launch_gemm_fp8(b, workspace, stream);
 }
 
 size_t hif4_gemm_fp8_ws_bytes(int64_t m, int64_t n, int64_t k) {

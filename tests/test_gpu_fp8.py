@@ -382,9 +382,12 @@ def test_stream_of_its_own(hip):
     assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("m,n,k,dtype", [(4100, 4196, 4097, torch.bfloat16), (4224, 4096, 4099, torch.float32)])
-def test_linear_backward_large(hip, m, n, k, dtype):
-    """Both products large enough for one launch of the two: the same as one by one."""
+@pytest.mark.parametrize("m,n,k,dtype", [(4100, 4196, 4097, torch.bfloat16), (4224, 4096, 4099, torch.float32),
+                                         (2100, 2200, 2111, torch.bfloat16), (2176, 2200, 2112, torch.float32),
+                                         (1400, 1300, 1500, torch.bfloat16), (1401, 1300, 1501, torch.float32),
+                                         (500, 450, 300, torch.bfloat16), (70, 33, 129, torch.float32)])
+def test_linear_backward_in_one_launch(hip, m, n, k, dtype):
+    """Both products by one kernel (each kind of tile): the same as one by one."""
     g = torch.Generator(device="cuda").manual_seed(5)
     dy = (1e-3 * torch.randn((m, n), generator=g, device="cuda")).to(dtype)
     xt = hip.quantize_fp8(torch.randn((m, k), generator=g, device="cuda"), transposed=True)
@@ -393,9 +396,9 @@ def test_linear_backward_large(hip, m, n, k, dtype):
     codes, scales, codes_t, scales_t = hip.quantize_fp8_both(dy)
     assert torch.equal(dx, hip.linear_fp8(codes, scales, *wt, y_dtype=dtype))
     assert torch.equal(dw, hip.linear_fp8(codes_t, scales_t, *xt))
-    rows = torch.tensor([0, 1000, m - 1])
+    rows = torch.tensor([0, 31, 64, m // 4, m // 2, m - 1])
     _check_product(dx[rows.cuda()], ref64.fp8_values(_bytes(codes), _bytes(scales))[rows],
                    ref64.fp8_values(_bytes(wt[0]), _bytes(wt[1]), 128))
-    rows = torch.tensor([0, 2047, n - 1])
+    rows = torch.tensor([0, 32, n // 4, n // 2 - 1, n - 1])
     _check_product(dw[rows.cuda()], ref64.fp8_values(_bytes(codes_t), _bytes(scales_t))[rows],
                    ref64.fp8_values(_bytes(xt[0]), _bytes(xt[1])))
