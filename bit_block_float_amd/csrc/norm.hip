@@ -722,13 +722,20 @@ hipError_t hif4_launch_layer_norm(const NormArgs& a, bool x_bf16, int out, hipSt
 }
 
 // Workgroups of the backward: up to 4096 columns 16 waves a CU, beyond two
-// workgroups a CU; one a row for few rows. Measured (bf16, with the sums of the
-// parts): 57600 x 1280, 3 waves, 2 workgroups a CU 146 us, 5 95 us; 57600 x 5120,
-// 5 waves of two runs, 2 workgroups 330 us, 3 414 us.
+// workgroups a CU. Measured (bf16, with the sums of the parts): 57600 x 1280, 3
+// waves, 2 workgroups a CU 146 us, 5 95 us; 57600 x 5120, 5 waves of two runs, 2
+// workgroups 330 us, 3 414 us.
+// Fewer rows: the least k <= 8 with 64 k^2 >= rows each, which weighs a workgroup's
+// rows in turn against the parts to be written and read again. Measured, us, at
+// 1, 2, 3, 4 and 8 rows each: 100 x 1003 8.5, 8.0, 8.5, 9.6, 12.1; 777 x 1003 15.7,
+// 11.7, 10.8, 10.1, 12.5; 1024 x 5120 28.4, 28.3, 25.2, 20.5, 21.2; 4096 x 1024
+// 27.4, 27.4, 22.2, 18.3, 15.3.
 int hif4_layer_norm_backward_parts(int64_t rows, int64_t c) {
   const int64_t waves = backward_threads(c) / 64;
   const int64_t per_cu = backward_runs(c) == 1 ? std::max<int64_t>(2, 16 / waves) : 2;
-  return (int)std::min<int64_t>(std::max<int64_t>(rows, 1), 256 * per_cu);
+  int64_t k = 1;
+  while (k < 8 && 64 * k * k < rows) ++k;
+  return (int)std::min<int64_t>((std::max<int64_t>(rows, 1) + k - 1) / k, 256 * per_cu);
 }
 
 hipError_t hif4_launch_layer_norm_backward(const NormBackArgs& a, bool x_bf16, void* dw, void* db,
