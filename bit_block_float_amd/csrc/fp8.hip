@@ -11,6 +11,9 @@
 // writes 1 + 1/128 per element; the tile kernel reads a 128 x 128 tile once
 // for any of its outputs (codes along the rows, codes along the columns, or
 // both, which is what the two products of a linear layer's backward read).
+// Measured, bf16: rows 57600 x 5120 150 us (5.9 TB/s; a copy of as many bytes
+// runs at 5.0); 13824 x 5120 in tiles, codes of the transpose, 39 us (5.4 TB/s);
+// 8192 x 5120 both ways 36 us (4.7 TB/s).
 #include "fp8_dev.h"
 
 namespace hif4 {
@@ -136,7 +139,8 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
 }
 
 // Codes back to values: 8 elements a thread. The scale of element (r, j) is
-// scales[r / block_rows][j / 128].
+// scales[r / block_rows][j / 128]. Bound: HBM, 1 byte in and 2 or 4 out: 57600 x 5120
+// to bf16 145 us (6.1 TB/s), to fp32 391 us (3.8 TB/s).
 template <bool kF32Scale, bool kBf16>
 __global__ __launch_bounds__(256) void dequantize_fp8_kernel(
     const uint8_t* __restrict__ codes, const void* __restrict__ scales, int row_shift, int64_t row0,

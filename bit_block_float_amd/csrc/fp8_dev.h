@@ -230,8 +230,6 @@ __device__ __forceinline__ uint2 encode_column(const Run8<float> (&v)[8], int i,
   return e == 255u ? make_uint2(kFp8NaN4, kFp8NaN4) : r;
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
 }  // namespace hif4
 
 // Internal (hidden) host launchers; argument checks happen in api_fp8.hip.

@@ -185,7 +185,10 @@ __device__ __forceinline__ float tree_sum(const float (&v)[N]) {
 // LDS as fp32 ([weight, bias][quarter of an item][item] 16-byte pieces, which
 // consecutive lanes read without bank conflicts). The sums are taken in the order
 // of the kernel below: a tree over the lanes for each run of 64 items, then a
-// tree over the runs, so the results are the same bits.
+// tree over the runs, so the results are the same bits. Bound: VALU issue (HiF4:
+// 26 instructions an element, which at 4 cycles each fill 86% of the SIMDs' time; the
+// plain norm of the kernel below has 13). Measured on 57600 x 5120: HiF4 215 to 245 us
+// (3.3 TB/s), E4M3 176 us (5.0 TB/s, what a copy reaches).
 template <int kItems, int kOut>
 __global__ __launch_bounds__(512) void layer_norm_wave_kernel(NormArgs a) {
   extern __shared__ float4 affine[];
@@ -278,8 +281,8 @@ __global__ __launch_bounds__(512) void layer_norm_wave_kernel(NormArgs a) {
 
 // Forward of the widest rows (over 16384 columns): 1024 threads share a row, a
 // lane owns items (16 consecutive elements) t, t + 1024, ..., the quantizers' own
-// mapping, so 4 aligned lanes hold a HiF4
-// unit and 8 an E4M3 block when the row leaves through one of them. The value
+// mapping, so 4 aligned lanes hold a HiF4 unit and 8 an E4M3 block when the row
+// leaves through one of them. The value
 // quantized is the one kOutY would store (rounded to bf16 for HiF4, to x's type
 // for E4M3), so the codes are those of the two calls in turn.
 template <typename T, int kItems, int kOut, int kRows>
@@ -375,7 +378,10 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(NormArgs a) {
 // times the waves that a row's items of 16 columns fill) own one item each, of R
 // rows at a time: weight and bias stay in registers for all rows, where the
 // kernel above reads them again for each (57600 x 5120: they are twice x's own
-// bytes), and two barriers serve R rows. Everything else is as above.
+// bytes), and two barriers serve R rows. Everything else is as above. Bound: HBM, a
+// row read and written once: 57600 x 5120 bf16 235 us (5.0 TB/s, what a copy reaches),
+// 57600 x 13824 675 us (4.7 TB/s); 77 x 1003 fp32 4.8 us and 509 x 5120 to E4M3 5.5 us,
+// which are a launch and the latency of one read.
 template <typename T, int R, int kOut, bool kMulti, int kRows>
 __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
   __shared__ float slots[2][R][16];
@@ -490,7 +496,9 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
 // Backward. A workgroup walks rows blockIdx.x, + gridDim.x, ...; a thread owns
 // the same kRuns runs of 8 columns in every row and keeps their weight and its
 // part of dw and db in registers. The parts of all workgroups go to `parts`
-// ([gridDim.x][2][c]) and are added in a fixed order by the kernel below.
+// ([gridDim.x][2][c]) and are added in a fixed order by the kernel below. Bound: HBM,
+// x and dy read and dx written once: 57600 x 5120 bf16 323 us (5.5 TB/s), 57600 x
+// 13824 907 us (5.3 TB/s), 777 x 1003 fp32 8.2 us.
 template <typename T, int kRuns, bool kSums, int kRows>
 __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs a) {
   __shared__ float sums[2][2][16];
@@ -569,7 +577,8 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
 }
 
 // Sums the workgroups' parts: 32 columns a workgroup; its 32 half waves take the
-// parts in turn, 8 loads in flight each, and their sums are added in order.
+// parts in turn, 8 loads in flight each, and their sums are added in order (512
+// parts of 5120 columns 5.5 us).
 __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(const float* __restrict__ parts,
                                                                 int n_parts, int c, void* dw,
                                                                 void* db, bool w_bf16) {

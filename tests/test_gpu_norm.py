@@ -117,6 +117,24 @@ def test_forward_strides_and_surroundings(hip, ld, offset, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("c", [30001, 65535, 65536])
+def test_widest_rows(hip, c, dtype):
+    x, (w, b) = _x(3, c, c, dtype), _affine(c, torch.float32)
+    xd, wd, bd = _cuda(x, w, b)
+    y, mean, rstd = hip.layer_norm(xd, wd, bd, eps=EPS)
+    _check_forward(x, w, b, y, mean, rstd, HALF[dtype])
+    got, want = hip.layer_norm_quantize_fp8(xd, wd, bd, eps=EPS), hip.quantize_fp8(y)
+    if c % 64 == 0:
+        got = (*got, *hip.layer_norm_quantize(xd, wd, bd, eps=EPS)[:2])
+        want = (*want, *hip.quantize(y.to(torch.bfloat16))[:2])
+    for g, r in zip(got, want):
+        assert torch.equal(g.contiguous().view(torch.uint8), r.contiguous().view(torch.uint8))
+    dy = _x(3, c, c + 1, dtype, offset=0.0)
+    dx, dw, db = hip.layer_norm_backward(dy.cuda(), xd, mean, rstd, weight=wd)
+    _check_backward(dy, x, mean.cpu(), rstd.cpu(), w, dx, dw, db)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows", [511, 512, 513, 2051])
 @pytest.mark.parametrize("c", [5, 1003, 1024, 4104, 5119])
 def test_forward_rows_at_once(hip, c, rows, dtype):
