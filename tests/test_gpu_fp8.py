@@ -204,6 +204,19 @@ def test_linear_float_scales_end_inside_a_tile(hip, n):
         _check_product(y[rows.cuda()], xv[rows], wv)
 
 
+def test_linear_few_rows_more_columns_than_a_grid(hip):
+    """More columns than workgroups of 1024 threads for 16 columns can be launched for."""
+    m, n = 3, (1 << 26) + 5
+    xc, xs = hip.quantize_fp8(_x(m, 128, 1).cuda())
+    wc = torch.randint(0, 0x70, (n, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.full(((n + 127) // 128, 4), 120, dtype=torch.uint8, device="cuda")
+    f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    y = hip.linear_fp8(xc, xs, wc.view(f8), ws.view(e8)[:, :1], y_dtype=torch.bfloat16)
+    cols = torch.tensor([0, 1, 1 << 20, (1 << 25) + 77, (1 << 26) - 1, 1 << 26, n - 1]).cuda()
+    wv = ref64.fp8_values(wc[cols].cpu(), ws[:len(cols), :1].cpu())
+    _check_product(y[:, cols], ref64.fp8_values(_bytes(xc), _bytes(xs)), wv)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 5120, 13824), (16, 1280, 13824), (300, 700, 13824)])
 def test_linear_long_sum(hip, m, n, k):
     args, xv, wv = _linear_case(hip, m, n, k, "tiles", seed=9)
