@@ -39,6 +39,25 @@ __device__ __forceinline__ float wave_sum(float v) {
   return f(p[0]) + f(p[1]);
 }
 
+// Sum over aligned groups of 8, 16, 32 or 64 lanes: the steps of wave_sum that stay
+// inside one (so the same bits as over 64 lanes of which the others hold zero).
+template <int kLanes>
+__device__ __forceinline__ float lanes_sum(float v) {
+  auto f = [](uint32_t u) { return __uint_as_float(u); };
+  if constexpr (kLanes == 64) return wave_sum(v);
+  if constexpr (kLanes == 8) {
+    v += f(dpp<kDppQuadXor1>(__float_as_uint(v)));
+    v += f(dpp<kDppQuadXor2>(__float_as_uint(v)));
+    return v + f(dpp<kDppHalfMirror>(__float_as_uint(v)));
+  }
+  v = row16_sum(v);
+  if constexpr (kLanes == 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(p[0]) + f(p[1]);
+  }
+  return v;
+}
+
 // Sum over a workgroup of 1024 threads. `slot` is LDS of 16 floats that no other
 // sum in flight uses.
 __device__ __forceinline__ float row_sum(float v, float* slot) {
@@ -382,11 +401,18 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(NormArgs a) {
 // row read and written once: 57600 x 5120 bf16 235 us (5.0 TB/s, what a copy reaches),
 // 57600 x 13824 675 us (4.7 TB/s); 77 x 1003 fp32 4.8 us and 509 x 5120 to E4M3 5.5 us,
 // which are a launch and the latency of one read.
-template <typename T, int R, int kOut, bool kMulti, int kRows>
+//
+// Rows of up to 512 columns leave most lanes of a wave without an item: groups of
+// kLanes = 8, 16 or 32 lanes take a row each (kMulti: a row is the workgroup's, of
+// several waves).
+template <typename T, int R, int kOut, bool kMulti, int kRows, int kLanes>
 __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
   __shared__ float slots[2][R][16];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  static_assert(!kMulti || kLanes == 64, "whole waves share a row");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = kMulti ? threadIdx.x : threadIdx.x & (kLanes - 1);  // the item
   const int waves = kMulti ? (int)(blockDim.x >> 6) : 1;
+  const int groups = kMulti ? 1 : (int)blockDim.x / kLanes, group = kMulti ? 0 : (int)threadIdx.x / kLanes;
   const int c = a.c, col = t * 16;
   const int items = kOut == kOutFp8 ? a.kp / 16 : (c + 15) / 16;
   const bool live = t < items;
@@ -398,6 +424,7 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
       const uint32_t m16 = live ? mask_bits(a.mask + col) : 0u;
       const uint32_t cnt = __popc(m16), incl = wave_prefix(cnt, lane);
       uint32_t base = incl - cnt;
+      if constexpr (kLanes < 64) base -= (uint32_t)__shfl((int)base, 0, kLanes);
       if constexpr (kMulti) {
         if (lane == 63) part[wave] = incl;
         __syncthreads();
@@ -417,7 +444,7 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
   // sums over the row's threads, R at once; `slot` turns between the two
   auto row_sums = [&](float (&v)[R], int slot) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = wave_sum(v[r]);
+    for (int r = 0; r < R; ++r) v[r] = lanes_sum<kLanes>(v[r]);
     if constexpr (kMulti) {
       if (lane == 0) {
 #pragma unroll
@@ -431,18 +458,18 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
   };
 
   const float fc = (float)c, inv_c = 1.0f / (float)c;
-  const int64_t step = (int64_t)gridDim.x * R;
+  const int64_t step = (int64_t)gridDim.x * groups * R;
   // rows past the end read the last one again and are not stored
   Run8<T> n0[R], n1[R];
   auto load_rows = [&](int64_t row0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const T* src = reinterpret_cast<const T*>(a.x) + min(row0 + r, a.rows - 1) * a.ld;
+      const T* src = reinterpret_cast<const T*>(a.x) + min(row0 + r * groups + group, a.rows - 1) * a.ld;
       n0[r].template load<kRows>(src, col, c);
       n1[r].template load<kRows>(src, col + 8, c);
     }
   };
-  for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < a.rows; row0 += step) {
+  for (int64_t row0 = (int64_t)blockIdx.x * groups * R; row0 < a.rows; row0 += step) {
     load_rows(row0);
     float x[R][2][8], mean[R], rstd[R];
 #pragma unroll
@@ -477,8 +504,8 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
     for (int r = 0; r < R; ++r) rstd[r] = 1.0f / sqrtf(rstd[r] * inv_c + a.eps);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t row = row0 + r;
-      if (row >= a.rows) break;  // uniform
+      const int64_t row = row0 + r * groups + group;
+      if (row >= a.rows) break;  // whole groups
       if (kOut == kOutY && t == 0) {
         if (a.mean) a.mean[row] = mean[r];
         if (a.rstd) a.rstd[row] = rstd[r];
@@ -623,6 +650,10 @@ __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(const float* __r
 //   HiF4 57600 x 8192 348    323    403
 // so two, from two rows a CU on. Rows that are not 16-byte aligned (5119 columns):
 // bf16 292 and 267, fp32 641 and 759, so fp32 takes one there.
+// Rows of up to 512 columns, a wave each and 8, 16 or 32 lanes each: bf16 2300000 x 128
+// 650 and 254 (to HiF4 1289 and 191, to E4M3 885 and 184), 1000000 x 64 291 and 54,
+// 500000 x 256 171 and 116, 200000 x 512 93 and 96 (to HiF4 126 and 71); 5000 x 128
+// and fewer the same.
 // A wave per row against it, into a quantizer: HiF4 57600 x 5120 215 and 315,
 // 57600 x 6144 295 and 349, 2048 x 5120 12.5 and 17.8, 1024 x 5120 11.5 and 10.2;
 // but 57600 x 4096 185 and 163, 57600 x 8192 486 and 323 (E4M3 the same way: 176 and
@@ -632,13 +663,29 @@ template <typename T, int kOut, int kRows>
 static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   const int items = kOut == kOutFp8 ? a.kp / 16 : (a.c + 15) / 16;
   const int waves = (items + 63) / 64;
-#define HIF4_NORM(rr, multi, grid, waves)                                                  \
-  hipLaunchKernelGGL((layer_norm_rows_kernel<T, rr, kOut, multi, kRows>), dim3(grid),      \
+#define HIF4_NORM(rr, multi, grid, waves, lanes)                                             \
+  hipLaunchKernelGGL((layer_norm_rows_kernel<T, rr, kOut, multi, kRows, lanes>), dim3(grid), \
                      dim3(64 * (waves)), 0, stream, a)
+  const auto narrow_grid = [&](int lanes) {  // workgroups of 4 waves
+    const int64_t at_once = 256 / lanes;
+    return (unsigned)std::min<int64_t>((a.rows + at_once - 1) / at_once, 256 * 16);
+  };
   if constexpr (kRows == kTiny) {  // c < 8
-    HIF4_NORM(1, false, (unsigned)std::min<int64_t>(a.rows, 256 * 64), 1);
+    HIF4_NORM(1, false, narrow_grid(8), 4, 8);
     return hipGetLastError();
   } else {
+    if (items <= 8) {
+      HIF4_NORM(1, false, narrow_grid(8), 4, 8);
+      return hipGetLastError();
+    }
+    if (items <= 16) {
+      HIF4_NORM(1, false, narrow_grid(16), 4, 16);
+      return hipGetLastError();
+    }
+    if (items <= 32) {
+      HIF4_NORM(1, false, narrow_grid(32), 4, 32);
+      return hipGetLastError();
+    }
     if (items > 1024) {
       const unsigned grid = (unsigned)std::min<int64_t>(a.rows, 256 * 32);
       hipLaunchKernelGGL((layer_norm_wide_kernel<T, 4, kOut, kRows>), dim3(grid), dim3(1024), 0,
@@ -661,11 +708,11 @@ static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
     const unsigned grid =
         (unsigned)std::min<int64_t>((a.rows + r - 1) / r, (int64_t)256 * 64 / waves);
     if (r == kMany) {
-      if (waves > 1) HIF4_NORM(kMany, true, grid, waves);
-      else HIF4_NORM(kMany, false, grid, 1);
+      if (waves > 1) HIF4_NORM(kMany, true, grid, waves, 64);
+      else HIF4_NORM(kMany, false, grid, 1, 64);
     } else {
-      if (waves > 1) HIF4_NORM(1, true, grid, waves);
-      else HIF4_NORM(1, false, grid, 1);
+      if (waves > 1) HIF4_NORM(1, true, grid, waves, 64);
+      else HIF4_NORM(1, false, grid, 1, 64);
     }
     return hipGetLastError();
   }

@@ -136,7 +136,7 @@ def test_widest_rows(hip, c, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("rows", [511, 512, 513, 2051])
-@pytest.mark.parametrize("c", [5, 1003, 1024, 4104, 5119])
+@pytest.mark.parametrize("c", [5, 9, 127, 128, 130, 256, 500, 512, 1003, 1024, 4104, 5119])
 def test_forward_rows_at_once(hip, c, rows, dtype):
     """Workgroups that take two rows, the last of them one."""
     x, (w, b) = _x(rows, c, rows, dtype), _affine(c, torch.bfloat16)
@@ -177,7 +177,7 @@ def test_fp8_form_is_the_two_calls(hip, c, dtype):
         assert torch.equal(gs.contiguous().view(torch.uint8), ws.contiguous().view(torch.uint8))
 
 
-@pytest.mark.parametrize("c", [1024, 1088, 2048, 3136, 4096, 4160, 5120, 5184, 6144, 6208, 8192, 13824])
+@pytest.mark.parametrize("c", [64, 128, 192, 256, 448, 512, 576, 1024, 1088, 2048, 3136, 4096, 4160, 5120, 5184, 6144, 6208, 8192, 13824])
 def test_quantizing_forms_are_the_two_calls_over_many_rows(hip, c):
     rows = 2100 if c > 4096 else 8200
     x, w, b = _cuda(_x(rows, c, c), *_affine(c, torch.float32))
