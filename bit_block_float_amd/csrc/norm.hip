@@ -603,6 +603,69 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
   }
 }
 
+// The same for rows of up to 256 columns: groups of kLanes = 16 or 32 lanes take a
+// row each (above, a wave would have most lanes without a run, and a row a barrier).
+// The groups' sums are added in order before they leave as the workgroup's part.
+// Measured with the parts' sum, us, the kernel above and this one: 1000000 x 128 bf16
+// 328 and 153 (5.0 TB/s), 500000 x 256 196 and 152, 23025 x 106 fp32 24.9 and 12.5,
+// 1000 x 128 7.4 and 6.7, 77 x 200 8.3 and 8.8.
+template <typename T, bool kSums, int kRows, int kLanes>
+__global__ __launch_bounds__(256) void layer_norm_backward_narrow_kernel(NormBackArgs a) {
+  constexpr int kGroups = 256 / kLanes, kCols = kLanes * 8;
+  __shared__ float sums[kSums ? kGroups : 1][2][kCols];
+  const int t = threadIdx.x & (kLanes - 1), group = threadIdx.x / kLanes, c = a.c, col = t * 8;
+  const float inv_c = 1.0f / (float)c;
+  float w[8], dw[8], db[8];
+  load_w8<kRows>(a.w, a.w_bf16, col, c, 1.0f, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.0f;
+  for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.rows;
+       row0 += (int64_t)gridDim.x * kGroups) {
+    const bool live = row0 + group < a.rows;
+    const int64_t row = live ? row0 + group : a.rows - 1;  // read again, not stored or summed
+    Run8<T> xr, dr;
+    xr.template load<kRows>(reinterpret_cast<const T*>(a.x) + row * a.ldx, col, c);
+    dr.template load<kRows>(reinterpret_cast<const T*>(a.dy) + row * a.lddy, col, c);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float xhat = (xr.get(i) - mean) * rstd, d = dr.get(i);
+      const float g = d * w[i];
+      s1 += g;
+      s2 = fmaf(g, xhat, s2);
+      if constexpr (kSums) {
+        dw[i] = live ? fmaf(d, xhat, dw[i]) : dw[i];
+        db[i] = live ? db[i] + d : db[i];
+      }
+    }
+    s1 = lanes_sum<kLanes>(s1) * inv_c;
+    s2 = lanes_sum<kLanes>(s2) * inv_c;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float xhat = (xr.get(i) - mean) * rstd;
+      v[i] = (dr.get(i) * w[i] - s1 - xhat * s2) * rstd;
+    }
+    if (live) store_run8<kRows>(reinterpret_cast<T*>(a.dx) + row * a.lddx + col, c - col, v);
+  }
+  if constexpr (kSums) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sums[group][0][col + i] = dw[i];
+      sums[group][1][col + i] = db[i];
+    }
+    __syncthreads();
+    float* p = a.parts + (int64_t)blockIdx.x * 2 * c;
+    for (int j = threadIdx.x; j < 2 * c; j += 256) {
+      const int which = j >= c, at = which ? j - c : j;
+      float s = sums[0][which][at];
+      for (int g = 1; g < kGroups; ++g) s += sums[g][which][at];
+      p[j] = s;
+    }
+  }
+}
+
 // Sums the workgroups' parts: 32 columns a workgroup; its 32 half waves take the
 // parts in turn, 8 loads in flight each, and their sums are added in order (512
 // parts of 5120 columns 5.5 us).
@@ -733,6 +796,21 @@ template <typename T, int kRows>
 static hipError_t launch_norm_backward(const NormBackArgs& a, int grid, hipStream_t stream) {
   const int kr = backward_runs(a.c);
   const int threads = backward_threads(a.c);
+#define HIF4_NARROW(lanes)                                                                         \
+  do {                                                                                             \
+    if (a.parts)                                                                                   \
+      hipLaunchKernelGGL((layer_norm_backward_narrow_kernel<T, true, kRows, lanes>), dim3(grid),   \
+                         dim3(256), 0, stream, a);                                                 \
+    else                                                                                           \
+      hipLaunchKernelGGL((layer_norm_backward_narrow_kernel<T, false, kRows, lanes>), dim3(grid),  \
+                         dim3(256), 0, stream, a);                                                 \
+    return hipGetLastError();                                                                      \
+  } while (0)
+  if (a.c <= 128) HIF4_NARROW(16);
+  if constexpr (kRows != kTiny) {
+    if (a.c <= 256) HIF4_NARROW(32);
+  }
+#undef HIF4_NARROW
 #define HIF4_BACK(k)                                                                               \
   do {                                                                                             \
     if (a.parts)                                                                                   \
@@ -742,15 +820,13 @@ static hipError_t launch_norm_backward(const NormBackArgs& a, int grid, hipStrea
       hipLaunchKernelGGL((layer_norm_backward_kernel<T, k, false, kRows>), dim3(grid), dim3(threads), 0,  \
                          stream, a);                                                               \
   } while (0)
-  if constexpr (kRows == kTiny) {
-    HIF4_BACK(1);
-    return hipGetLastError();
-  }
-  switch (kr) {
-    case 1: HIF4_BACK(1); break;
-    case 2: HIF4_BACK(2); break;
-    case 4: HIF4_BACK(4); break;
-    default: HIF4_BACK(8); break;
+  if constexpr (kRows != kTiny) {  // (c < 8 has returned)
+    switch (kr) {
+      case 1: HIF4_BACK(1); break;
+      case 2: HIF4_BACK(2); break;
+      case 4: HIF4_BACK(4); break;
+      default: HIF4_BACK(8); break;
+    }
   }
 #undef HIF4_BACK
   return hipGetLastError();
@@ -787,11 +863,13 @@ hipError_t hif4_launch_layer_norm(const NormArgs& a, bool x_bf16, int out, hipSt
 // 11.7, 10.8, 10.1, 12.5; 1024 x 5120 28.4, 28.3, 25.2, 20.5, 21.2; 4096 x 1024
 // 27.4, 27.4, 22.2, 18.3, 15.3.
 int hif4_layer_norm_backward_parts(int64_t rows, int64_t c) {
-  const int64_t waves = backward_threads(c) / 64;
+  const int64_t at_once = c <= 128 ? 16 : c <= 256 ? 8 : 1;  // rows a workgroup has in hand
+  const int64_t waves = c <= 256 ? 4 : backward_threads(c) / 64;
   const int64_t per_cu = backward_runs(c) == 1 ? std::max<int64_t>(2, 16 / waves) : 2;
+  const int64_t turns = (std::max<int64_t>(rows, 1) + at_once - 1) / at_once;
   int64_t k = 1;
-  while (k < 8 && 64 * k * k < rows) ++k;
-  return (int)std::min<int64_t>((std::max<int64_t>(rows, 1) + k - 1) / k, 256 * per_cu);
+  while (k < 8 && 64 * k * k < turns) ++k;
+  return (int)std::min<int64_t>((turns + k - 1) / k, 256 * per_cu);
 }
 
 hipError_t hif4_launch_layer_norm_backward(const NormBackArgs& a, bool x_bf16, void* dw, void* db,

@@ -237,6 +237,18 @@ def test_backward(hip, c, dtype):
         assert all(torch.equal(p, q) for p, q in zip((dx, dw, db), again))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("c", [3, 8, 100, 128, 129, 250, 256, 257])
+@pytest.mark.parametrize("rows", [15, 17, 1025, 9001])
+def test_backward_narrow_rows(hip, rows, c, dtype):
+    x, dy = _x(rows, c, c, dtype), _x(rows, c, c + 50, dtype, offset=0.0)
+    w, _ = _affine(c, torch.float32)
+    xc, dyc, wc = _cuda(x, dy, w)
+    _, mean, rstd = hip.layer_norm(xc, wc, None, eps=EPS)
+    dx, dw, db = hip.layer_norm_backward(dyc, xc, mean, rstd, weight=wc)
+    _check_backward(dy, x, mean.cpu(), rstd.cpu(), w, dx, dw, db)
+
+
 def test_backward_strides(hip):
     rows, c = 41, 1003
     x, dy = _x(rows, c, 1, torch.float32), _x(rows, c, 2, torch.float32, 0.0)
