@@ -84,15 +84,18 @@ hif4_status hif4_dequantize_fp8(const uint8_t* codes, const void* scales, int sc
                                              out_dtype == HIF4_BF16, stream));
 }
 
-size_t hif4_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  if (m < 0 || n < 0 || k < 0 || m >= (int64_t(1) << 31) || n >= (int64_t(1) << 31) || k > kMaxK)
-    return 0;
-  return hif4_gemm_fp8_ws_bytes(m, n, k);
-}
-
 }  // extern "C"
 
 namespace {
+
+// The sizes that a product takes.
+bool linear_sizes(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n < 0 || k < 0 || k % 128 != 0 || m >= (int64_t(1) << 31) ||
+      n >= (int64_t(1) << 31) || k > kMaxK)
+    return false;
+  // the grid of the smallest tile
+  return (m + 63) / 64 * ((n + 63) / 64) < (int64_t(1) << 31);
+}
 
 // Argument checks of a product, and the product of checked arguments.
 hif4_status check_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t ldxs,
@@ -100,11 +103,7 @@ hif4_status check_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_
                          int w_scale_type, int64_t w_block_rows, int64_t m, int64_t n, int64_t k,
                          const void* y, int y_dtype, const void* workspace,
                          size_t workspace_bytes) {
-  if (m < 0 || n < 0 || k < 0 || k % 128 != 0 || m >= (int64_t(1) << 31) ||
-      n >= (int64_t(1) << 31) || k > kMaxK)
-    return HIF4_ERR_SHAPE;
-  // the grid of the smallest tile
-  if ((m + 63) / 64 * ((n + 63) / 64) >= (int64_t(1) << 31)) return HIF4_ERR_SHAPE;
+  if (!linear_sizes(m, n, k)) return HIF4_ERR_SHAPE;
   if (y_dtype != HIF4_F32 && y_dtype != HIF4_BF16) return HIF4_ERR_DTYPE;
   if (w_scale_type != HIF4_SCALE_E8M0 && w_scale_type != HIF4_SCALE_F32) return HIF4_ERR_DTYPE;
   if (w_block_rows != 1 && w_block_rows != 128) return HIF4_ERR_ARG;
@@ -119,7 +118,7 @@ hif4_status check_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_
       !aligned(w_scales, 4) || ldxs % 4 != 0 ||
       (w_scale_type == HIF4_SCALE_E8M0 && ldws % 4 != 0))
     return HIF4_ERR_ALIGN;
-  const size_t need = hif4_linear_fp8_workspace_bytes(m, n, k);
+  const size_t need = hif4_gemm_fp8_ws_bytes(m, n, k);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return HIF4_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return HIF4_ERR_ALIGN;
@@ -147,6 +146,10 @@ hif4_status run_linear(const uint8_t* x_codes, const uint8_t* x_scales, int64_t 
 
 extern "C" {
 
+size_t hif4_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  return linear_sizes(m, n, k) ? hif4_gemm_fp8_ws_bytes(m, n, k) : 0;
+}
+
 hif4_status hif4_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, int64_t ldxs,
                             const uint8_t* w_codes, const void* w_scales, int64_t ldws,
                             int w_scale_type, int64_t w_block_rows, int64_t m, int64_t n, int64_t k,
@@ -165,6 +168,12 @@ hif4_status hif4_linear_fp8(const uint8_t* x_codes, const uint8_t* x_scales, int
 // scales [m][lds], its transposed codes [n][mp] and scales [n][lds_t], and what
 // the larger product needs.
 namespace {
+// The sizes that a backward takes: those of dY's quantization and of both products.
+bool backward_sizes(int64_t m, int64_t n, int64_t k) {
+  if (m < 0 || n < 0 || k < 0 || m > kMaxK || n > kMaxK || k >= (int64_t(1) << 31)) return false;
+  return linear_sizes(m, k, up128(n)) && linear_sizes(n, k, up128(m));
+}
+
 struct BackwardParts {
   int64_t np, mp, lds, lds_t;
   size_t scales, codes_t, scales_t, product, total;
@@ -179,16 +188,15 @@ BackwardParts backward_parts(int64_t m, int64_t n, int64_t k) {
   p.codes_t = p.scales + align256((size_t)m * (size_t)p.lds);
   p.scales_t = p.codes_t + align256((size_t)n * (size_t)p.mp);
   p.product = p.scales_t + align256((size_t)n * (size_t)p.lds_t);
-  const size_t a = hif4_linear_fp8_workspace_bytes(m, k, p.np);
-  const size_t b = hif4_linear_fp8_workspace_bytes(n, k, p.mp);
+  const size_t a = hif4_gemm_fp8_ws_bytes(m, k, p.np);
+  const size_t b = hif4_gemm_fp8_ws_bytes(n, k, p.mp);
   p.total = p.product + align256(a > b ? a : b);
   return p;
 }
 }  // namespace
 
 size_t hif4_linear_fp8_backward_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-  if (m < 0 || n < 0 || k < 0 || m > kMaxK || n > kMaxK || k >= (int64_t(1) << 31)) return 0;
-  return backward_parts(m, n, k).total;
+  return backward_sizes(m, n, k) ? backward_parts(m, n, k).total : 0;
 }
 
 hif4_status hif4_linear_fp8_backward(const void* dy, int dy_dtype, int64_t lddy,
@@ -198,7 +206,7 @@ hif4_status hif4_linear_fp8_backward(const void* dy, int dy_dtype, int64_t lddy,
                                      int64_t m, int64_t n, int64_t k, void* dx, int dx_dtype,
                                      void* dw, int dw_dtype, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream) {
-  if (k < 0 || k >= (int64_t(1) << 31) || m > kMaxK) return HIF4_ERR_SHAPE;
+  if (!backward_sizes(m, n, k)) return HIF4_ERR_SHAPE;
   hif4_status st = check_quantize(dy, dy_dtype, m, n, lddy, 1);
   if (st != HIF4_OK) return st;
   if ((dx_dtype != HIF4_F32 && dx_dtype != HIF4_BF16) ||

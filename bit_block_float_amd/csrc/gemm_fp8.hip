@@ -802,7 +802,7 @@ struct GemmPlan {
   int splits, per_split;  // of K's blocks
 };
 constexpr int64_t kCus = 256;
-static GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k) {
+static GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k) {  // k a multiple of 128, above 0
   const int64_t kb = k / 128;
   const auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
   // (a grid has fewer than 2^32 threads: 1024 for 16 columns)

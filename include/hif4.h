@@ -509,7 +509,8 @@ HIF4_EXPORT size_t hif4_linear_fp8_backward_workspace_bytes(int64_t m, int64_t n
  *         (block_rows 1).
  *  dx     [m][k] of dx_dtype or NULL (wt_* unused); dw [n][k] of dw_dtype or
  *         NULL (xt_* unused); contiguous, 16-byte aligned. m, n, k >= 0, m and
- *         n at most 2^22; m = 0 gives dW = 0, n = 0 gives dX = 0.
+ *         n at most 2^22, and hif4_linear_fp8's limits for both products;
+ *         m = 0 gives dW = 0, n = 0 gives dX = 0.
  *  workspace >= hif4_linear_fp8_backward_workspace_bytes(m, n, k), 256-byte
  *         aligned.
  */

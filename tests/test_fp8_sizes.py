@@ -1,0 +1,27 @@
+"""Size queries of the 8-bit linear layer, on the CPU: 0 bytes for what the calls refuse."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+
+    from bit_block_float_amd import build, hif4
+    if not os.path.exists(hif4.LIB_PATH):
+        build.build()
+    return hif4.lib()
+
+
+@pytest.mark.parametrize("m,n,k", [(100, 100, 64), (300, 300, 1), (300, 300, 64), (300, 300, 127), (300, 300, 4200),
+                                   (300, 700, 13825), (1, 1, 64), (5120, 5120, 5119), (1 << 30, 1 << 30, 128)])
+def test_a_refused_product_needs_no_workspace(L, m, n, k):
+    a = 0x100000  # never dereferenced
+    assert L.hif4_linear_fp8(a, a, 1 << 16, a, a, 1 << 16, 0, 128, m, n, k, a, 0, a, 1 << 50, None) == 2  # shape
+    assert L.hif4_linear_fp8_workspace_bytes(m, n, k) == 0
+
+
+def test_a_split_product_needs_its_planes(L):
+    parts = L.hif4_linear_fp8_workspace_bytes(300, 700, 13824) / (300 * 700 * 4)
+    assert parts == int(parts) and 2 <= parts <= 13824 // 128
+    assert L.hif4_linear_fp8_workspace_bytes(300, 700, 128) == 0
+    assert L.hif4_linear_fp8_workspace_bytes(300, 700, 0) == 0
