@@ -93,8 +93,9 @@ bool linear_sizes(int64_t m, int64_t n, int64_t k) {
   if (m < 0 || n < 0 || k < 0 || k % 128 != 0 || m >= (int64_t(1) << 31) ||
       n >= (int64_t(1) << 31) || k > kMaxK)
     return false;
-  // the grid of the smallest tile
-  return (m + 63) / 64 * ((n + 63) / 64) < (int64_t(1) << 31);
+  // Grids have fewer than 2^32 threads: 256 a tile of 128 x 128 (smaller tiles are
+  // for products of few tiles, larger ones have no more threads for their size).
+  return (m + 127) / 128 * ((n + 127) / 128) < (int64_t(1) << 24);
 }
 
 // Argument checks of a product, and the product of checked arguments.

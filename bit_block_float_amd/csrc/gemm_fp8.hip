@@ -882,7 +882,7 @@ static bool launch_pair(const Fp8Product& a, const Fp8Product& b, GemmKind kind,
   const GemmArgs ga = gemm_args(a, tile, a.y), gb = gemm_args(b, tile, b.y);
   const uint64_t first = (uint64_t)ga.tiles_m * ga.tiles_n;
   const uint64_t all = first + (uint64_t)gb.tiles_m * gb.tiles_n;
-  if (all >= (1ull << 31)) return false;
+  if (all >= (1ull << 24)) return false;  // a grid has fewer than 2^32 threads
 #define HIF4_PAIR(kernel, threads)                                                        \
   hipLaunchKernelGGL((kernel), dim3((unsigned)all), dim3(threads), 0, stream, ga, gb, (uint32_t)first)
   switch (kind) {

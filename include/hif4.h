@@ -478,8 +478,9 @@ HIF4_EXPORT size_t hif4_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t
  *          [ceil(n/128)][ldws] (128), or float [ceil(n/128)][ldws] with
  *          HIF4_SCALE_F32 and w_block_rows 128 (a checkpoint's own scales;
  *          HIF4_ERR_ARG with w_block_rows 1).
- *  m, n    >= 0, below 2^31.  k >= 0, k % 128 == 0 (pad with zero codes), at
- *          most 2^22; k = 0 gives Y = 0.
+ *  m, n    >= 0, below 2^31, ceil(m/128) ceil(n/128) < 2^24.
+ *  k       >= 0, k % 128 == 0 (pad with zero codes), at most 2^22; k = 0 gives
+ *          Y = 0.
  *  y       [m][n] contiguous of y_dtype, 16-byte aligned.
  *  workspace >= hif4_linear_fp8_workspace_bytes(m, n, k), 256-byte aligned.
  *  Precision: a float32 Y is a full fp32 sum of exact products. A bf16 Y comes

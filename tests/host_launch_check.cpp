@@ -90,7 +90,8 @@ static std::vector<int64_t> around(std::initializer_list<int64_t> borders) {
 // A product's size query and the call: a refused size needs 0 bytes, and a call
 // that is given what the query says is launched.
 static void linear_sizes() {
-  const auto rows = around({1, 16, 17, 64, 65, 128, 129, 256, 1024, 2048, 5120, 57600});
+  const auto rows = around({1, 16, 17, 64, 65, 128, 129, 256, 1024, 2048, 5120, 57600, 1 << 20,
+                            (int64_t)1 << 31});
   const auto ks = around({0, 1, 64, 128, 256, 2048, 4096, 5120, 8192, 13824, 1 << 22});
   for (int64_t m : rows)
     for (int64_t n : rows)
@@ -112,10 +113,12 @@ static void linear_sizes() {
 }
 
 static void linear_backward_sizes() {
-  const auto sizes = around({1, 17, 64, 128, 129, 1024, 2048, 8192});
+  const auto sizes = around({1, 17, 64, 128, 129, 1024, 2048, 8192, 1 << 18});
+  auto ks = sizes;
+  for (int64_t k : around({(int64_t)1 << 30, ((int64_t)1 << 31) - 128, (int64_t)1 << 31})) ks.push_back(k);
   for (int64_t m : sizes)
     for (int64_t n : sizes)
-      for (int64_t k : sizes) {
+      for (int64_t k : ks) {
         const size_t need = hif4_linear_fp8_backward_workspace_bytes(m, n, k);
         const int64_t big = 1 << 17;
         const hif4_status st = hif4_linear_fp8_backward(

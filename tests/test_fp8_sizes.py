@@ -13,7 +13,8 @@ def L():
 
 
 @pytest.mark.parametrize("m,n,k", [(100, 100, 64), (300, 300, 1), (300, 300, 64), (300, 300, 127), (300, 300, 4200),
-                                   (300, 700, 13825), (1, 1, 64), (5120, 5120, 5119), (1 << 30, 1 << 30, 128)])
+                                   (300, 700, 13825), (1, 1, 64), (5120, 5120, 5119), (1 << 30, 1 << 30, 128),
+                                   (1 << 19, 1 << 19, 128), (128, (1 << 31) - 1, 128)])
 def test_a_refused_product_needs_no_workspace(L, m, n, k):
     a = 0x100000  # never dereferenced
     assert L.hif4_linear_fp8(a, a, 1 << 16, a, a, 1 << 16, 0, 128, m, n, k, a, 0, a, 1 << 50, None) == 2  # shape
