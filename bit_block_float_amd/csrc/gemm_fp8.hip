@@ -805,8 +805,8 @@ constexpr int64_t kCus = 256;
 static GemmPlan plan_gemm(int64_t m, int64_t n, int64_t k) {  // k a multiple of 128, above 0
   const int64_t kb = k / 128;
   const auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
-  // (a grid has fewer than 2^32 threads: 1024 for 16 columns)
-  if (m <= kSkinnyRows && n < (int64_t(1) << 26)) return {kSkinny, 1, (int)kb};
+  // (a grid has fewer than 2^32 threads: 1024 for 16 columns, so 2^22 - 1 workgroups)
+  if (m <= kSkinnyRows && n <= (int64_t(1) << 26) - 16) return {kSkinny, 1, (int)kb};
   const int64_t t128 = tiles(128);
   if (4 * ((tiles(256) + kCus - 1) / kCus) < 3 * ((t128 + 2 * kCus - 1) / (2 * kCus)))
     return {kLarge, 1, (int)kb};

@@ -90,7 +90,7 @@ static std::vector<int64_t> around(std::initializer_list<int64_t> borders) {
 // A product's size query and the call: a refused size needs 0 bytes, and a call
 // that is given what the query says is launched.
 static void linear_sizes() {
-  const auto rows = around({1, 16, 17, 64, 65, 128, 129, 256, 1024, 2048, 5120, 57600, 1 << 20,
+  const auto rows = around({1, 16, 17, 64, 65, 128, 129, 256, 1024, 2048, 5120, 57600, 1 << 20, (1 << 26) - 16, 1 << 26,
                             (int64_t)1 << 31});
   const auto ks = around({0, 1, 64, 128, 256, 2048, 4096, 5120, 8192, 13824, 1 << 22});
   for (int64_t m : rows)
