@@ -53,9 +53,10 @@ __global__ __launch_bounds__(256) void quantize_fp8_rows_kernel(
 // which go through LDS to leave as whole 128-byte lines.
 //  kTile: one scale for the tile; else one per row (kAlong) or column (kCols).
 //  kAlong: codes [rows][ceil(k/128)*128]; kCols: codes_t [k][ceil(rows/128)*128].
+//  row_tile0: the launch's first row of tiles.
 template <typename T, bool kTile, bool kAlong, bool kCols, int kRows>
 __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
-    const T* __restrict__ x, int64_t ld, int64_t rows, int k, uint32_t tiles_k,
+    const T* __restrict__ x, int64_t ld, int64_t rows, int k, int64_t row_tile0, uint32_t tiles_k,
     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t lds,
     uint8_t* __restrict__ codes_t, uint8_t* __restrict__ scales_t, int64_t lds_t) {
   constexpr int kPitch = 128 + 16;  // 16-byte reads stay aligned, columns spread over banks
@@ -63,8 +64,9 @@ __global__ __launch_bounds__(256) void quantize_fp8_tile_kernel(
   __shared__ uint32_t part[4][kTile ? 1 : 128];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cg = tid & 15, rg = tid >> 4;
-  const int64_t tr = blockIdx.x / tiles_k;
-  const int tk = (int)(blockIdx.x - tr * tiles_k);
+  const uint32_t in = blockIdx.x / tiles_k;
+  const int64_t tr = row_tile0 + in;
+  const int tk = (int)(blockIdx.x - in * tiles_k);
   const int64_t row0 = tr * 128 + rg * 8;
   const int col0 = tk * 128 + cg * 8;
   Run8<T> v[8];
@@ -211,23 +213,30 @@ static hipError_t launch_quantize(const T* x, int64_t rows, int64_t k, int64_t l
     }
     return hipSuccess;
   }
-  const int64_t tiles = (rows + 127) / 128 * tiles_k;
-  const dim3 grid((unsigned)tiles), block(256);
+  const int64_t tiles_m = (rows + 127) / 128;
+  const int64_t max_tiles_m = ((int64_t)1 << 23) / tiles_k;  // a grid has fewer than 2^32 threads
+  const dim3 block(256);
   const uint32_t tk = (uint32_t)tiles_k;
+  for (int64_t t0 = 0; t0 < tiles_m; t0 += max_tiles_m) {
+    const int64_t nt = tiles_m - t0 < max_tiles_m ? tiles_m - t0 : max_tiles_m;
+    const dim3 grid((unsigned)(nt * tiles_k));
 #define HIF4_TILE(tile, r, c)                                                                     \
   hipLaunchKernelGGL((quantize_fp8_tile_kernel<T, tile, r, c, kRows>), grid, block, 0, stream, x,  \
-                     ld, rows, (int)k, tk, codes, scales, lds, codes_t, scales_t, lds_t)
-  if (block_rows == 1) {
-    if (codes) HIF4_TILE(false, true, true);
-    else HIF4_TILE(false, false, true);
-  } else if (codes_t) {
-    if (codes) HIF4_TILE(true, true, true);
-    else HIF4_TILE(true, false, true);
-  } else {
-    HIF4_TILE(true, true, false);
-  }
+                     ld, rows, (int)k, t0, tk, codes, scales, lds, codes_t, scales_t, lds_t)
+    if (block_rows == 1) {
+      if (codes) HIF4_TILE(false, true, true);
+      else HIF4_TILE(false, false, true);
+    } else if (codes_t) {
+      if (codes) HIF4_TILE(true, true, true);
+      else HIF4_TILE(true, false, true);
+    } else {
+      HIF4_TILE(true, true, false);
+    }
 #undef HIF4_TILE
-  return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace hif4

@@ -113,7 +113,7 @@ static void linear_sizes() {
 }
 
 static void linear_backward_sizes() {
-  const auto sizes = around({1, 17, 64, 128, 129, 1024, 2048, 8192, 1 << 18});
+  const auto sizes = around({1, 17, 64, 128, 129, 1024, 2048, 8192, 1 << 18, 1 << 22});
   auto ks = sizes;
   for (int64_t k : around({(int64_t)1 << 30, ((int64_t)1 << 31) - 128, (int64_t)1 << 31})) ks.push_back(k);
   for (int64_t m : sizes)
@@ -128,6 +128,26 @@ static void linear_backward_sizes() {
         if (st == HIF4_ERR_SHAPE && need != 0) fail("bytes for a refused backward", m, n, k);
         if (st == HIF4_OK && m > 0 && n > 0 && k > 0 && need == 0) fail("no bytes for a backward", m, n, k);
       }
+}
+
+static void quantize_sizes() {
+  const auto rows = around({1, 128, 129, 57600, 1 << 22, 1 << 30, ((int64_t)1 << 31) - 127, (int64_t)1 << 31});
+  const auto ks = around({1, 8, 128, 129, 5120, 65536, 1 << 22});
+  const int64_t lds = 1 << 25;
+  for (int64_t r : rows)
+    for (int64_t k : ks)
+      for (int dt = 0; dt < 2; ++dt)
+        for (int64_t br : {1, 128}) {
+          hif4_status st[4] = {
+              hif4_quantize_fp8(A, dt, r, k, k < 1 ? 1 : k, br, 0, U8, U8, lds, nullptr),
+              hif4_quantize_fp8(A, dt, r, k, k < 1 ? 1 : k, br, 1, U8, U8, lds, nullptr),
+              hif4_quantize_fp8_both(A, dt, r, k, k < 1 ? 1 : k, br, U8, U8, lds, U8, U8, lds, nullptr),
+              hif4_dequantize_fp8(U8, A, HIF4_SCALE_E8M0, br, lds, r, k, A, dt, nullptr)};
+          const bool ok = r >= 0 && k >= 0 && r < (int64_t)1 << 31 && k <= 1 << 22;
+          const bool many = ok && (r + 127) / 128 * ((k + 127) / 128) >= (int64_t)1 << 31;
+          for (int i = 0; i < 4; ++i)
+            if (st[i] != (ok && !(many && i < 3) ? HIF4_OK : HIF4_ERR_SHAPE)) fail("status of a quantizer", r, k, i);
+        }
 }
 
 static void norm_sizes() {
@@ -156,6 +176,7 @@ static void norm_sizes() {
 int main() {
   linear_sizes();
   linear_backward_sizes();
+  quantize_sizes();
   norm_sizes();
   printf("%d launches\n", launches);
   if (failures) return 1;

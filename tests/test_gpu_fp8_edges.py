@@ -31,3 +31,25 @@ def test_linear_few_rows_up_to_the_largest_grid(hip, n):
     y = hip.linear_fp8(xc.view(F8), xs.view(E8)[:, :1], wc.view(F8), ws.view(E8)[:, :1], y_dtype=torch.bfloat16)
     want = torch.exp2((torch.arange(n, device="cuda") % 5).float()).to(torch.bfloat16)
     assert torch.equal(y, torch.stack([want, 2 * want, -2 * want]))
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_more_row_tiles_than_a_grid(hip, block_rows):
+    """The most rows there are, of one column: 2^24 row tiles, over several launches."""
+    rows = (1 << 31) - 1
+    x = torch.zeros((rows, 1), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 127, 128, (1 << 30) - 1, 1 << 30, (1 << 30) + 1, rows - 128, rows - 2, rows - 1])
+    vals = torch.tensor([1.0, -2.0, 3.0, 448.0, 0.5, -7.0, 5.0, 1.5, -0.375], dtype=torch.bfloat16)
+    x[at.cuda(), 0] = vals.cuda()
+    codes, scales = hip.quantize_fp8(x, block_rows=block_rows, transposed=True)
+    want = torch.zeros(rows, dtype=torch.bfloat16, device="cuda")
+    want[at.cuda()] = vals.cuda()
+    for t in sorted({int(i) // 128 for i in at}):
+        part = slice(128 * t, min(128 * t + 128, rows))
+        rc, rs = ref64.fp8_quantize(want[part][None].cpu(), block_rows)
+        assert torch.equal(_bytes(codes[:, 128 * t:128 * t + 128]), rc)
+        assert torch.equal(_bytes(scales[:, t:t + 1]), rs)
+    # everything else is zero
+    assert int(torch.count_nonzero(codes.view(torch.uint8).view(torch.int64))) == len(
+        {int(i) // 8 for i in at})
+    assert int(torch.count_nonzero(scales.contiguous().view(torch.uint8))) == len({int(i) // 128 for i in at})
