@@ -53,3 +53,28 @@ def test_quantize_more_row_tiles_than_a_grid(hip, block_rows):
     assert int(torch.count_nonzero(codes.view(torch.uint8).view(torch.int64))) == len(
         {int(i) // 8 for i in at})
     assert int(torch.count_nonzero(scales.contiguous().view(torch.uint8))) == len({int(i) // 128 for i in at})
+
+
+def _nearest_bf16(v):
+    """float64 v at the nearest bf16 value (ties to even), as float64."""
+    step = torch.exp2((torch.frexp(v)[1].clamp(min=-125) - 8).double())
+    return torch.round(v / step) * step
+
+
+@pytest.mark.parametrize("power", [0, -100, -122, -126, -131, -135, 100])
+def test_dequantize_rounds_once(hip, power):
+    """Every code times float32 scales that bring products next to the middle between two
+    bf16 values (also where they are subnormal): the nearest one, of the exact product."""
+    blocks = 512
+    g = torch.Generator().manual_seed(3)
+    middle = (2 * torch.randint(128, 256, (blocks,), generator=g) + 1).double()
+    code = torch.randint(8, 16, (blocks,), generator=g).double()
+    s = (middle / code).float().view(torch.int32) + torch.randint(-2, 3, (blocks,), generator=g, dtype=torch.int32)
+    s = (s.view(torch.float32) * 2.0 ** power)[None]
+    s[0, 0] = (0x815555 / 2 ** 23) * 2.0 ** power  # times 1.125 just above a middle
+    codes = torch.arange(256, dtype=torch.uint8).view(2, 128).repeat(1, blocks)
+    want = ref64.fp8_values(codes, s, 128)
+    for out, rounded in ((torch.bfloat16, _nearest_bf16(want)), (torch.float32, want.float().double())):
+        got = hip.dequantize_fp8(codes.cuda().view(F8), s.cuda(), out_dtype=out).double().cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(rounded)), power
