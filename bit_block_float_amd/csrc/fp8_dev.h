@@ -69,17 +69,17 @@ __device__ __forceinline__ uint32_t pick(uint32_t m, uint32_t a, uint32_t b) {
 }
 
 // 8 consecutive elements of a row of c >= 1, from column col; elements at or past
-// c are zero.
+// c are zero, or with kOther any other elements of the row.
 template <typename T>
 struct Run8;
 template <>
 struct Run8<uint16_t> {
   uint4 w;
-  template <int kRows>
+  template <int kRows, bool kOther = false>
   __device__ __forceinline__ void load(const uint16_t* row, int col, int c) {
     if constexpr (kRows == kAligned) {
       const uint4 v = *reinterpret_cast<const uint4*>(row + (col < c ? col : 0));
-      const uint32_t m = col < c ? 0xFFFFFFFFu : 0u;
+      const uint32_t m = kOther || col < c ? 0xFFFFFFFFu : 0u;
       w = make_uint4(v.x & m, v.y & m, v.z & m, v.w & m);
     } else if constexpr (kRows == kAny) {
       const int start = min(col, c - 8), skip = col - start;
@@ -87,19 +87,22 @@ struct Run8<uint16_t> {
       const any4_t v = *reinterpret_cast<const any4_t*>(row + start);
       const uint32_t s4 = 0u - ((skip >> 2) & 1u), s2 = 0u - ((skip >> 1) & 1u);
       const uint32_t a0 = pick(s4, v[2], v[0]), a1 = pick(s4, v[3], v[1]);
-      const uint32_t a2 = v[2] & ~s4, a3 = v[3] & ~s4;
+      // shifted down by skip, or with kOther turned (what leaves comes in behind)
+      const uint32_t a2 = pick(s4, kOther ? v[0] : 0u, v[2]);
+      const uint32_t a3 = pick(s4, kOther ? v[1] : 0u, v[3]);
       const uint32_t b0 = pick(s2, a1, a0), b1 = pick(s2, a2, a1), b2 = pick(s2, a3, a2);
-      const uint32_t b3 = a3 & ~s2, sh = (skip & 1) * 16, m = skip < 8 ? 0xFFFFFFFFu : 0u;
+      const uint32_t b3 = pick(s2, kOther ? a0 : 0u, a3), sh = (skip & 1) * 16;
+      const uint32_t m = kOther || skip < 8 ? 0xFFFFFFFFu : 0u;
       w = make_uint4(__builtin_amdgcn_alignbit(b1, b0, sh) & m,
                      __builtin_amdgcn_alignbit(b2, b1, sh) & m,
                      __builtin_amdgcn_alignbit(b3, b2, sh) & m,
-                     __builtin_amdgcn_alignbit(0u, b3, sh) & m);
+                     __builtin_amdgcn_alignbit(kOther ? b0 : 0u, b3, sh) & m);
     } else {
       uint32_t h[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[i] = row[min(col + i, c - 1)];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] &= col + i < c ? 0xFFFFu : 0u;
+      for (int i = 0; i < 8; ++i) h[i] &= kOther || col + i < c ? 0xFFFFu : 0u;
       w = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16),
                      h[6] | (h[7] << 16));
     }
@@ -133,7 +136,7 @@ struct Run8<uint16_t> {
 template <>
 struct Run8<float> {
   float v[8];
-  template <int kRows>
+  template <int kRows, bool kOther = false>
   __device__ __forceinline__ void load(const float* row, int col, int c) {
     if constexpr (kRows == kAligned) {
       const float4 a = *reinterpret_cast<const float4*>(row + (col < c ? col : 0));
@@ -141,7 +144,7 @@ struct Run8<float> {
       v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
       v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = col + (i & 4) < c ? v[i] : 0.0f;
+      for (int i = 0; i < 8; ++i) v[i] = kOther || col + (i & 4) < c ? v[i] : 0.0f;
     } else if constexpr (kRows == kAny) {
       typedef uint32_t any4_t __attribute__((ext_vector_type(4), aligned(4)));
       any4_t q[2];
@@ -152,20 +155,21 @@ struct Run8<float> {
       for (int h = 0; h < 2; ++h) {
         const int skip = col + 4 * h - min(col + 4 * h, c - 4);
         const uint32_t s2 = 0u - ((skip >> 1) & 1u), s1 = 0u - (skip & 1u);
-        const uint32_t m = skip < 4 ? 0xFFFFFFFFu : 0u;
+        const uint32_t m = kOther || skip < 4 ? 0xFFFFFFFFu : 0u;
         const uint32_t a0 = pick(s2, q[h][2], q[h][0]), a1 = pick(s2, q[h][3], q[h][1]);
-        const uint32_t a2 = q[h][2] & ~s2, a3 = q[h][3] & ~s2;
+        const uint32_t a2 = pick(s2, kOther ? q[h][0] : 0u, q[h][2]);
+        const uint32_t a3 = pick(s2, kOther ? q[h][1] : 0u, q[h][3]);
         v[4 * h] = __uint_as_float(pick(s1, a1, a0) & m);
         v[4 * h + 1] = __uint_as_float(pick(s1, a2, a1) & m);
         v[4 * h + 2] = __uint_as_float(pick(s1, a3, a2) & m);
-        v[4 * h + 3] = __uint_as_float(a3 & ~s1 & m);
+        v[4 * h + 3] = __uint_as_float(pick(s1, kOther ? a0 : 0u, a3) & m);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = row[min(col + i, c - 1)];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i] = __uint_as_float(__float_as_uint(v[i]) & (col + i < c ? 0xFFFFFFFFu : 0u));
+        v[i] = __uint_as_float(__float_as_uint(v[i]) & (kOther || col + i < c ? 0xFFFFFFFFu : 0u));
     }
   }
   __device__ __forceinline__ void keep_if(bool ok) {

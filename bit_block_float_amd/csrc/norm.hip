@@ -522,7 +522,10 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
 
 // Backward. A workgroup walks rows blockIdx.x, + gridDim.x, ...; a thread owns
 // the same kRuns runs of 8 columns in every row and keeps their weight and its
-// part of dw and db in registers. The parts of all workgroups go to `parts`
+// part of dw and db in registers. Behind a row's last column x and dy are 0, and
+// xhat = -mean rstd may overflow: infinity times 0 would make the whole row's
+// mean(g xhat) a NaN. So the mean is 0 there, or (where a run may be part of a row) x
+// another element of it. The parts of all workgroups go to `parts`
 // ([gridDim.x][2][c]) and are added in a fixed order by the kernel below. Bound: HBM,
 // x and dy read and dx written once: 57600 x 5120 bf16 323 us (5.5 TB/s), 57600 x
 // 13824 907 us (5.3 TB/s), 777 x 1003 fp32 8.2 us.
@@ -547,16 +550,20 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
 #pragma unroll
     for (int n = 0; n < kRuns; ++n) {
       const int col = (n * nt + t) * 8;
-      xr[n].template load<kRows>(xs, col, c);
+      xr[n].template load<kRows, kRows != kAligned>(xs, col, c);
       dr[n].template load<kRows>(ds, col, c);
     }
     const float mean = a.mean[row], rstd = a.rstd[row];
+    float mu[kRuns];  // kAligned: a run is whole or empty, the last one of a thread only
+#pragma unroll
+    for (int n = 0; n < kRuns; ++n)
+      mu[n] = kRows == kAligned && n == kRuns - 1 && (n * nt + t) * 8 >= c ? 0.0f : mean;
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int n = 0; n < kRuns; ++n)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float xhat = (xr[n].get(i) - mean) * rstd, d = dr[n].get(i);
+        const float xhat = (xr[n].get(i) - mu[n]) * rstd, d = dr[n].get(i);
         const float g = d * w[n][i];
         s1 += g;
         s2 = fmaf(g, xhat, s2);
@@ -582,7 +589,7 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs 
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float xhat = (xr[n].get(i) - mean) * rstd;
+        const float xhat = (xr[n].get(i) - mu[n]) * rstd;
         v[i] = (dr[n].get(i) * w[n][i] - s1 - xhat * s2) * rstd;
       }
       store_run8<kRows>(o + col, c - col, v);
@@ -624,7 +631,7 @@ __global__ __launch_bounds__(256) void layer_norm_backward_narrow_kernel(NormBac
     const bool live = row0 + group < a.rows;
     const int64_t row = live ? row0 + group : a.rows - 1;  // read again, not stored or summed
     Run8<T> xr, dr;
-    xr.template load<kRows>(reinterpret_cast<const T*>(a.x) + row * a.ldx, col, c);
+    xr.template load<kRows, true>(reinterpret_cast<const T*>(a.x) + row * a.ldx, col, c);
     dr.template load<kRows>(reinterpret_cast<const T*>(a.dy) + row * a.lddy, col, c);
     const float mean = a.mean[row], rstd = a.rstd[row];
     float s1 = 0.0f, s2 = 0.0f;
