@@ -12,10 +12,11 @@
 //    8 are added; the runs and the accumulator add in full fp32. The loss is at
 //    most 7 * 2^-13 of each run's largest product, on random signs some 1e-5 of
 //    |Y|: far below the 2^-9 rounding of a bf16 result, and half the time.
-//  - fp32: the codes are widened to bf16 (v_cvt_scalef32_pk_bf16_fp8, exact,
-//    with the power-of-two scale applied; below 2^-126 bf16 is subnormal and
-//    may round) and multiplied by the bf16 forms, whose products and sums are
-//    full fp32: a float32 result is asked for where the last bits count.
+//  - fp32: the codes are widened to bf16 (v_cvt_scalef32_pk_bf16_fp8, with the
+//    power-of-two scale applied: exact for scale bytes 3 to 246; below, bf16 has no
+//    bits under 2^-133 and rounds, above, its range ends) and multiplied by the bf16
+//    forms, whose products and sums are full fp32, subnormal operands included: a
+//    float32 result is asked for where the last bits count.
 // A weight whose scales are float32 (one per 128 x 128) keeps sx in the
 // operands and adds each block's partial sum times sw with one FMA per output.
 //

@@ -483,10 +483,17 @@ HIF4_EXPORT size_t hif4_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t
  *          Y = 0.
  *  y       [m][n] contiguous of y_dtype, 16-byte aligned.
  *  workspace >= hif4_linear_fp8_workspace_bytes(m, n, k), 256-byte aligned.
- *  Precision: a float32 Y is a full fp32 sum of exact products. A bf16 Y comes
+ *  Precision: a float32 Y is a full fp32 sum of products of operands code times
+ *  scale (code alone for a weight with float scales). The operands are held in
+ *  bf16: exactly for scale bytes 3 to 246, whatever the other side's scale is.
+ *  Under bytes 0 to 2 one is rounded to a multiple of 2^-133 (half of that off),
+ *  and from 2^128 on it is infinite. Float weight scales multiply a block's sum,
+ *  which has to stay in range before, too. A bf16 Y takes every scale byte and comes
  *  from the fp8 matrix instructions, which cut the products of each run of 8
  *  consecutive K values to 2^-13 of the largest one's power of two: less than
- *  7 * 2^-13 of sum |x||w| at worst, some 1e-5 of |Y| on random signs.
+ *  7 * 2^-13 of sum |x||w| at worst (a run whose large products cancel keeps
+ *  nothing of its small ones), some 1e-5 of |Y| on random signs. Where that
+ *  matters, ask for a float32 Y.
  */
 HIF4_EXPORT hif4_status hif4_linear_fp8(const uint8_t *x_codes, const uint8_t *x_scales,
                               int64_t ldxs, const uint8_t *w_codes, const void *w_scales,

@@ -78,3 +78,50 @@ def test_dequantize_rounds_once(hip, power):
         got = hip.dequantize_fp8(codes.cuda().view(F8), s.cuda(), out_dtype=out).double().cpu()
         assert torch.equal(torch.isnan(got), torch.isnan(want))
         assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(rounded)), power
+
+
+def _extreme(m, n, k, side, byte, codes, seed):
+    """x and w codes and E8M0 bytes: `byte` for one side's every block, the other's such
+    that sums are ordinary numbers; and the 64-bit product. Whole numbers of one unit:
+    every sum of up to 2^24 units is exact in fp32, in any order."""
+    g = torch.Generator().manual_seed(seed)
+    few = torch.tensor(codes, dtype=torch.uint8)[torch.randint(0, len(codes), ((m if side == "x" else n), k), generator=g)]
+    small = torch.tensor([0, 0x38, 0x40, 0xC0], dtype=torch.uint8)  # 0, 1, 2, -2
+    other = small[torch.randint(0, 4, ((n if side == "x" else m), k), generator=g)]
+    kp = (k // 128 + 3) // 4 * 4
+    back = 200 if byte < 127 else 20
+    one = lambda rows, b: torch.full((rows, kp), b, dtype=torch.uint8)
+    if side == "x":
+        return few, one(m, byte), other, one(n, back)
+    return other, one(m, back), few, one(n, byte)
+
+
+TILES = [(3, 40, 256), (20, 70, 384), (300, 96, 4224), (1408, 1536, 128), (2176, 2304, 128), (2048, 5248, 128)]
+
+
+@pytest.mark.parametrize("side", ["x", "w"])
+@pytest.mark.parametrize("byte", [0, 1, 2, 3, 4, 246, 247])
+@pytest.mark.parametrize("m,n,k", TILES)
+def test_linear_extreme_scales(hip, m, n, k, byte, side):
+    """Every kernel, one operand at either end of E8M0: its smallest codes (k 2^-9) under the
+    lowest scales, its largest under the highest (up to 240 under 247: 2^128 - 2^124)."""
+    codes = [0, 1, 2, 3, 7, 0x83] if byte < 127 else [0, 0x70, 0x74, 0x77, 0xF7] + ([0x7C, 0x7E] if byte < 247 else [])
+    xc, xs, wc, ws = _extreme(m, n, k, side, byte, codes, byte)
+    kb = k // 128
+    rows = torch.tensor([0, 1, m // 2, m - 1])
+    xv, wv = ref64.fp8_values(xc[rows], xs[rows, :kb]), ref64.fp8_values(wc, ws[:, :kb])
+    want, size = xv @ wv.T, xv.abs() @ wv.abs().T
+    # bytes 0 to 2: the operand is off by half of 2^-133 at most
+    off = torch.zeros_like(want)
+    if byte < 3:
+        off = 2.0 ** -134 * (wv.abs().sum(1)[None, :] if side == "x" else xv.abs().sum(1)[:, None]).expand_as(want)
+    xd, xsd, wd, wsd = xc.cuda().view(F8), xs.cuda().view(E8)[:, :kb], wc.cuda().view(F8), ws.cuda().view(E8)[:, :kb]
+    kinds = [wsd]
+    if side == "x" and byte < 127:  # float32 scales come after a block's sum, which has to stay in range
+        kinds.append(torch.full(((n + 127) // 128, kb), 2.0 ** (int(ws[0, 0]) - 127), device="cuda"))
+    for w_scales in kinds:
+        y = hip.linear_fp8(xd, xsd, wd, w_scales)[rows.cuda()].double().cpu()
+        assert bool(((y - want).abs() <= off).all()), (byte, side, w_scales.dtype, float(((y - want).abs() / size).max()))
+        y = hip.linear_fp8(xd, xsd, wd, w_scales, y_dtype=torch.bfloat16)[rows.cuda()].double().cpu()
+        tol = 7 * 2.0 ** -13 * size * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+        assert bool(((y - want).abs() <= tol).all()), (byte, side, "bf16")
