@@ -3,12 +3,11 @@ grids, exact sums, extreme scales, rounding next to ties."""
 import pytest
 import torch
 
+import fp8_cases
 import ref64
 
 pytestmark = pytest.mark.gpu
 
-U = 2.0 ** -24           # half a step of fp32
-HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}  # half a step of the output type
 F8, E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
@@ -125,3 +124,38 @@ def test_linear_extreme_scales(hip, m, n, k, byte, side):
         y = hip.linear_fp8(xd, xsd, wd, w_scales, y_dtype=torch.bfloat16)[rows.cuda()].double().cpu()
         tol = 7 * 2.0 ** -13 * size * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
         assert bool(((y - want).abs() <= tol).all()), (byte, side, "bf16")
+
+
+@pytest.mark.parametrize("kind", ["tiles", "rows", "f32"])
+@pytest.mark.parametrize("m,n,k", fp8_cases.KERNELS)
+def test_linear_float32_sums_are_exact(hip, m, n, k, kind):
+    """Every kernel: runs of products that cancel but for small ones. fp32 sums hold them
+    exactly (tests/test_fp8_cases.py: the fp8 instructions would keep none); a bf16 Y is
+    within what those may lose."""
+    x, w = fp8_cases.cancelling(m, n, k)
+    kb, kp, tiles = k // 128, (k // 128 + 3) // 4 * 4, (n + 127) // 128
+    one = lambda rows: torch.full((rows, kp), 127, dtype=torch.uint8, device="cuda").view(E8)[:, :kb]
+    ws = {"tiles": one(tiles), "rows": one(n), "f32": torch.ones((tiles, kb), device="cuda")}[kind]
+    rows = torch.tensor([0, 1, 2, m // 2, m - 2, m - 1])
+    xv, wv = fp8_cases.values(x[rows]), fp8_cases.values(w)
+    want = xv @ wv.T
+    xd, wd = x.cuda().view(F8), w.cuda().view(F8)
+    y = hip.linear_fp8(xd, one(m), wd, ws)[rows.cuda()].double().cpu()
+    assert torch.equal(y, want)
+    y = hip.linear_fp8(xd, one(m), wd, ws, y_dtype=torch.bfloat16)[rows.cuda()].double().cpu()
+    assert bool(((y - want).abs() <= 7 * 2.0 ** -13 * (xv.abs() @ wv.abs().T)).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(70, 300, 513), (1400, 1300, 257), (2176, 2300, 257), (4224, 4096, 257)])
+def test_backward_float32_sums_are_exact(hip, m, n, k):
+    """dX in float32 from a dY whose runs of 8 along n cancel against W^T's."""
+    np_ = (n + 127) // 128 * 128
+    dy, wt = fp8_cases.cancelling(m, k, np_)
+    dy = fp8_cases.values(dy)[:, :n].float()
+    wt[:, n:] = 0
+    unit = torch.full(((k + 127) // 128, (np_ // 128 + 3) // 4 * 4), 127, dtype=torch.uint8, device="cuda")
+    xt = hip.quantize_fp8(torch.ones((m, k), device="cuda"), transposed=True)
+    # 256 is each block's largest: dY's own scales are 1 and its codes exact
+    dx, _ = hip.linear_fp8_backward(dy.cuda(), *xt, wt.cuda().view(F8), unit.view(E8)[:, :np_ // 128])
+    rows = torch.tensor([0, 1, m // 2, m - 1])
+    assert torch.equal(dx[rows.cuda()].double().cpu(), dy[rows].double() @ fp8_cases.values(wt)[:, :n].T)
