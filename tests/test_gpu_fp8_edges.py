@@ -5,6 +5,7 @@ import torch
 
 import fp8_cases
 import ref64
+from test_gpu_fp8 import _check_product, _linear_case
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +160,15 @@ def test_backward_float32_sums_are_exact(hip, m, n, k):
     dx, _ = hip.linear_fp8_backward(dy.cuda(), *xt, wt.cuda().view(F8), unit.view(E8)[:, :np_ // 128])
     rows = torch.tensor([0, 1, m // 2, m - 1])
     assert torch.equal(dx[rows.cuda()].double().cpu(), dy[rows].double() @ fp8_cases.values(wt)[:, :n].T)
+
+
+@pytest.mark.parametrize("kind", ["tiles", "rows", "f32"])
+@pytest.mark.parametrize("m,n,k", [(301, 701, 4224), (17, 3, 8192), (301, 701, 13824), (650, 330, 4224),
+                                   (1408, 1536, 256), (1409, 1535, 384), (2176, 2304, 256), (2177, 2303, 384),
+                                   (2049, 5003, 256)])
+def test_linear_both_types_by_every_kernel(hip, m, n, k, kind):
+    """K split with an odd count of results, and every tile kernel, to both types."""
+    args, xv, wv = _linear_case(hip, m, n, k, kind, seed=3)
+    rows = torch.tensor([0, 1, 2, 15, 16, m // 2, m - 2, m - 1])
+    for out in (torch.float32, torch.bfloat16):
+        _check_product(hip.linear_fp8(*args, y_dtype=out)[rows.cuda()], xv[rows], wv)
