@@ -1,5 +1,6 @@
 // api_norm.hip -- the C ABI of the layer norm, declared and documented in
 // include/hif4.h. Every argument check runs before any HIP call.
+#include <float.h>
 #include <math.h>
 
 #include "api_util.h"
@@ -29,7 +30,7 @@ hif4_status check_forward(const void* x, int x_dtype, int64_t rows, int64_t c, i
   const hif4_status st = check_common(rows, c, x_dtype, w_dtype);
   if (st != HIF4_OK) return st;
   if (ld < c) return HIF4_ERR_SHAPE;
-  if (!(eps >= 0.0) || !isfinite(eps)) return HIF4_ERR_ARG;
+  if (!(eps >= 0.0 && eps <= FLT_MAX)) return HIF4_ERR_ARG;
   if (rows == 0) return HIF4_OK;
   if (!x) return HIF4_ERR_NULL;
   if (!aligned(x, elem(x_dtype)) || !aligned(weight, elem(w_dtype)) ||
@@ -44,7 +45,8 @@ hif4_status check_forward(const void* x, int x_dtype, int64_t rows, int64_t c, i
   a.w = weight;
   a.b = bias;
   a.w_bf16 = w_dtype == HIF4_BF16;
-  a.eps = (float)eps;
+  // a positive eps stays positive: a row of equal values has rstd = eps^(-1/2), not infinity
+  a.eps = eps > 0.0 ? fmaxf((float)eps, FLT_TRUE_MIN) : 0.0f;
   return HIF4_OK;
 }
 

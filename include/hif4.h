@@ -536,7 +536,8 @@ HIF4_EXPORT hif4_status hif4_linear_fp8_backward(const void *dy, int dy_dtype, i
  *         element (16-byte rows are read in whole runs); any rows < 2^31,
  *         1 <= c <= 65536.
  *  weight, bias  [c] of w_dtype, or NULL (1 and 0); element-aligned.
- *  eps    finite and >= 0 (HIF4_ERR_ARG otherwise).
+ *  eps    >= 0 and within float's range (HIF4_ERR_ARG otherwise); taken as the
+ *         nearest float, a positive one as a positive float.
  *  y = (x - mean) rstd weight + bias, rstd = (var + eps)^(-1/2), var the mean
  *  of (x - mean)^2. Statistics in fp32; y rounded once.
  */

@@ -1,4 +1,5 @@
-"""Size queries of the 8-bit linear layer, on the CPU: 0 bytes for what the calls refuse."""
+"""Size queries of the 8-bit linear layer, on the CPU: 0 bytes for what the calls refuse;
+refusals of the norm's eps."""
 import pytest
 
 
@@ -26,3 +27,11 @@ def test_a_split_product_needs_its_planes(L):
     assert parts == int(parts) and 2 <= parts <= 13824 // 128
     assert L.hif4_linear_fp8_workspace_bytes(300, 700, 128) == 0
     assert L.hif4_linear_fp8_workspace_bytes(300, 700, 0) == 0
+
+
+@pytest.mark.parametrize("eps", [3.5e38, 1e39, 1e300])
+def test_norm_refuses_an_eps_beyond_float(L, eps):
+    a = 0x100000  # never dereferenced
+    assert L.hif4_layer_norm(a, 0, 4, 8, 8, a, a, 0, eps, a, 8, a, a, None) == 8
+    assert L.hif4_layer_norm_quantize(a, 0, 4, 64, 64, a, a, 0, eps, None, 0, None, a, a, None) == 8
+    assert L.hif4_layer_norm_quantize_fp8(a, 0, 4, 8, 8, a, a, 0, eps, a, a, 4, None) == 8

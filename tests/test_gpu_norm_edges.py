@@ -28,3 +28,14 @@ def test_backward_of_far_constant_rows(hip, c, dtype):
     assert bool((err <= tol * (1 + half) + half * want.abs()).all())
     assert bool((dw == 0).all())
     assert bool(((db.double().cpu() - d.sum(0)).abs() <= rows * U * d.abs().sum(0)).all())
+
+
+@pytest.mark.parametrize("eps", [1e-46, 1e-60, 1e-45])
+@pytest.mark.parametrize("c", [7, 300, 5120])
+def test_forward_of_constant_rows_under_a_tiny_eps(hip, c, eps):
+    """A positive eps below float's least is not 0: equal values give the bias, not NaN."""
+    x, b = torch.full((3, c), 0.5, device="cuda"), torch.randn(c, device="cuda")
+    y, mean, rstd = hip.layer_norm(x, torch.ones(c, device="cuda"), b, eps=eps)
+    assert torch.equal(y, b.expand(3, c)) and bool((mean == 0.5).all())
+    # the least float, 2^-149: its root is 2^-74.5
+    assert bool(((rstd.double() - 2.0 ** 74.5).abs() <= 4 * U * 2.0 ** 74.5).all())
