@@ -1,13 +1,11 @@
 // fp8_dev.h -- device helpers of the E4M3 block format (the rule is stated in
-// hif4.h): the E8M0 scale of a block from its maximum, the encoding of 16
-// elements, and guarded 16-element loads.
+// hif4.h): the E8M0 scale of a block from its maximum, runs of 8 elements with
+// guarded loads, and their encoding.
 #pragma once
 
 #include "hif4_dev.h"
 
 namespace hif4 {
-
-constexpr int kFp8Block = 128;  // elements that share one scale along a row
 
 // Biased exponent (E8M0 byte) of the smallest power of two s >= 2^-127 with
 // amax <= 448 s; `bits` = |amax| as fp32 bits. 448 = 1.75 * 2^8, so the
@@ -44,14 +42,6 @@ __device__ __forceinline__ uint32_t encode4_bf16(uint32_t lo, uint32_t hi, float
   r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(pair_t, lo), scale, false);
   r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(pair_t, hi), scale, true);
   return __builtin_bit_cast(uint32_t, r);
-}
-
-// Per-half maximum of two words of u16 pairs; with the sign bits cleared, bf16
-// magnitudes order as integers (NaNs above infinity).
-__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
-  typedef unsigned short u16_pair_t __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16_pair_t, a),
-                                                                __builtin_bit_cast(u16_pair_t, b)));
 }
 
 // How rows are read. Loads are unconditional, from clamped addresses (a load
@@ -118,8 +108,9 @@ struct Run8<uint16_t> {
   }
   // the largest magnitude, as fp32 bits
   __device__ __forceinline__ uint32_t abs_max() const {
-    const uint32_t m = pair_max(pair_max(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                pair_max(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+    // with the sign bits cleared, bf16 magnitudes order as integers (NaNs above infinity)
+    const uint32_t m = pkmax_u16(pkmax_u16(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                pkmax_u16(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
     return max(m << 16, m & 0xFFFF0000u);
   }
   // the 8 codes under the scale byte e (all NaN for 255)
@@ -176,7 +167,6 @@ struct Run8<float> {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = ok ? v[i] : 0.0f;
   }
-  __device__ __forceinline__ void opaque() {}
   __device__ __forceinline__ uint32_t abs_max() const {
     uint32_t m = 0;
 #pragma unroll
@@ -198,10 +188,10 @@ __device__ __forceinline__ void column_max(const Run8<uint16_t> (&v)[8], uint32_
   uint32_t p[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    p[0] = pair_max(p[0], v[r].w.x & 0x7FFF7FFFu);
-    p[1] = pair_max(p[1], v[r].w.y & 0x7FFF7FFFu);
-    p[2] = pair_max(p[2], v[r].w.z & 0x7FFF7FFFu);
-    p[3] = pair_max(p[3], v[r].w.w & 0x7FFF7FFFu);
+    p[0] = pkmax_u16(p[0], v[r].w.x & 0x7FFF7FFFu);
+    p[1] = pkmax_u16(p[1], v[r].w.y & 0x7FFF7FFFu);
+    p[2] = pkmax_u16(p[2], v[r].w.z & 0x7FFF7FFFu);
+    p[3] = pkmax_u16(p[3], v[r].w.w & 0x7FFF7FFFu);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) m[i] = (i & 1) ? p[i >> 1] & 0xFFFF0000u : p[i >> 1] << 16;

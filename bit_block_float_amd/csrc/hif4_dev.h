@@ -78,6 +78,14 @@ __device__ __forceinline__ uint32_t fdiv(uint32_t n, const FastDiv& f) {
   return (__umulhi(n, f.m) + n) >> f.s;
 }
 
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+// Per-half maximum of two words of u16 halves.
+__device__ __forceinline__ uint32_t pkmax_u16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
+                                                                __builtin_bit_cast(u16x2_t, b)));
+}
+
 // DPP lane moves within a row of 16 lanes (gfx9 encodings).
 constexpr int kDppQuadXor1 = 0xB1;     // quad_perm [1,0,3,2]
 constexpr int kDppQuadXor2 = 0x4E;     // quad_perm [2,3,0,1]

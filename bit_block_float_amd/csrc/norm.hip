@@ -848,7 +848,10 @@ hipError_t hif4_launch_layer_norm(const NormArgs& a, bool x_bf16, int out, hipSt
     using T = decltype(type);
     constexpr int kOut = decltype(kind)::value;
     if (a.vec) return launch_norm<T, kOut, kAligned>(a, stream);
-    return a.c >= 8 ? launch_norm<T, kOut, kAny>(a, stream) : launch_norm<T, kOut, kTiny>(a, stream);
+    if constexpr (kOut != kOutHif4) {  // (c % 64 == 0 there)
+      if (a.c < 8) return launch_norm<T, kOut, kTiny>(a, stream);
+    }
+    return launch_norm<T, kOut, kAny>(a, stream);
   };
   const auto by_type = [&](auto kind) {
     return x_bf16 ? go(uint16_t{}, kind) : go(float{}, kind);

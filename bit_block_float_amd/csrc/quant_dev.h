@@ -40,7 +40,6 @@ __device__ __forceinline__ uint32_t or4_u32(uint32_t v) {
 // rounds to nearest even; min(., 1031) saturates k at 7 and leaves k in the
 // low byte of each half. (Checked on the CPU for every bf16 y below 14 and
 // every m, and by the element-rounding parity tests.)
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint32_t kpair(uint32_t absw, uint32_t csub, uint32_t hi2,
@@ -62,11 +61,6 @@ __device__ __forceinline__ uint32_t kpair(uint32_t absw, uint32_t csub, uint32_t
 
 // Larger of the two u16 halves.
 __device__ __forceinline__ uint32_t hmax_u16(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
-// Per-half maximum of two words of u16 halves.
-__device__ __forceinline__ uint32_t pkmax_u16(uint32_t a, uint32_t b) {
-  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
-                                                                __builtin_bit_cast(u16x2_t, b)));
-}
 
 // RN16(4/(4+m)) and the fp16 remainder, both halves.
 __device__ __forceinline__ uint32_t kinv_hi2(uint32_t m) {
