@@ -599,7 +599,13 @@ def linear_fp8_workspace_bytes(m, n, k):
 def linear_fp8(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=None, workspace=None,
                stream=None):
     """Y [m][n] = X W^T of E4M3 codes x_codes [m][k] (E8M0 scales per 1 x 128) and
-    w_codes [n][k] (E8M0 scales per 1 x 128 or 128 x 128, or float32 per 128 x 128)."""
+    w_codes [n][k] (E8M0 scales per 1 x 128 or 128 x 128, or float32 per 128 x 128).
+
+    A float32 Y is a full fp32 sum of exact products (for scale bytes 3 to 246; the
+    header states the rest). A bfloat16 Y comes from the fp8 matrix instructions, which
+    cut each product to 2^-13 of the largest of its run of 8 along k: at most
+    7 * 2^-13 of sum |x||w| is lost, on random signs some 1e-5 of |Y|, but all of the
+    small products beside large ones that cancel. Take float32 where those count."""
     _check_codes(x_codes, "x_codes")
     _check_codes(w_codes, "w_codes")
     (m, k), n = x_codes.shape, w_codes.shape[0]
@@ -635,7 +641,10 @@ def linear_fp8_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype=N
     dX [m][k] = Q(dY) W and dW [n][k] = Q(dY^T) X for dy [m][n] (bf16 or fp32),
     with X^T and W^T quantized along m and n (quantize_fp8(..., transposed=True);
     the weight's scales as linear_fp8 takes them). dX is of dy's type unless
-    dx_dtype says otherwise."""
+    dx_dtype says otherwise. Each gradient has linear_fp8's precision for its type: a
+    bfloat16 dX, the default for a bfloat16 dy, is cut as a bfloat16 Y is (to at most
+    7 * 2^-13 of sum |dy||w|); dx_dtype=torch.float32 gives the full fp32 sum, as dw's
+    default does."""
     _check_rows(dy, "dy")
     _check_codes(xt_codes, "xt_codes")
     _check_codes(wt_codes, "wt_codes")

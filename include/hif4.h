@@ -508,7 +508,8 @@ HIF4_EXPORT size_t hif4_linear_fp8_backward_workspace_bytes(int64_t m, int64_t n
  * hif4_linear_fp8_backward -- the two gradients of Y = X W^T through the
  * quantizers (taken as the identity): dX [m][k] = Q(dY) W, dY quantized along
  * n, and dW [n][k] = Q(dY^T) X, dY quantized along m, each from
- * hif4_linear_fp8. dY is read once for both quantizations.
+ * hif4_linear_fp8, with its precision for dx_dtype and dw_dtype. dY is read once
+ * for both quantizations.
  *  dy     [m][lddy] of dy_dtype, element-aligned, lddy >= n.
  *  wt_codes [k][n up to 128s], wt_scales [.][ldwt]: W transposed (quantized
  *         with transposed = 1, or a weight's own codes and scales transposed),
