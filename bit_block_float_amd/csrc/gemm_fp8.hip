@@ -4,7 +4,8 @@
 // Y[i][j] = sum_b sx[i][b] sw[j][b] sum_{t in block b} cx[i][t] cw[j][t].
 // sx is a power of two (E8M0), and so is sw where the library quantized it.
 //
-// Which matrix instruction, by the type of Y:
+// Which matrix instruction, by the type of Y (beyond 16 rows; up to there the bf16
+// forms cost nothing, see gemm_fp8_skinny_kernel):
 //  - bf16: v_mfma_scale_f32_32x32x64_f8f6f4 on the codes as they are, both E8M0
 //    bytes applied by the instruction. Measured on gfx950 (and the same for the
 //    unscaled fp8 forms): within each run of 8 consecutive K values a product
@@ -48,10 +49,6 @@ __device__ __forceinline__ i32x8_t join(gu32x4_t a, gu32x4_t b) {
 
 __device__ __forceinline__ gf32x16_t mfma32(i32x8_t a, i32x8_t b, gf32x16_t c, int sa, int sb) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, kFmtE4M3, kFmtE4M3, 0, sa, 0, sb);
-}
-
-__device__ __forceinline__ gf32x4_t mfma16(i32x8_t a, i32x8_t b, gf32x4_t c, int sa, int sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, kFmtE4M3, kFmtE4M3, 0, sa, 0, sb);
 }
 
 // This wave's loads but the newest n have landed, its LDS reads are done.
@@ -697,6 +694,12 @@ void gemm_fp8_pair_kernel(GemmArgs a, GemmArgs b, uint32_t first) {
 // operand registers, and their sums meet in LDS in a fixed order. Rows past M or
 // the workgroup's columns repeat the last one and are not stored.
 //
+// The codes are widened to bf16 without their scales (exact), so a block's sum is a
+// full fp32 sum of exact products for either type of Y; then its two scales are
+// applied as one exponent, so that only the result has to be in fp32's range. The
+// fp8 instructions, which would cut products, are no faster here: 1 x 13824 x 5120
+// with float32 scales 13.1 us both ways, 16 x 5120 x 5120 10.9 and 11.2.
+//
 // What a CU can have in flight to memory sets the pace, so the columns are cut to
 // give every CU the same share: cols is the least that leaves as many workgroups
 // a CU as 16 would. Measured, one row: n = 5120, k = 13824, 320 workgroups of 16
@@ -743,32 +746,34 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
       x[u][0] = *reinterpret_cast<const gu32x4_t*>(xp + (int64_t)k * 128);
       x[u][1] = *reinterpret_cast<const gu32x4_t*>(xp + (int64_t)k * 128 + 64);
       sx[u] = xsb[k];
-      sw[u] = kF32Scale ? (uint32_t)kUnitScale : wsb[k];
+      sw[u] = kF32Scale ? 0u : wsb[k];
       swf0[u] = kF32Scale ? wsf0[k] : 1.0f;
       swf1[u] = kF32Scale ? wsf1[k] : 1.0f;
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (kb + u * kSkinnyWaves >= KB) break;  // uniform
-      gf32x4_t p = kF32Scale ? gf32x4_t{0, 0, 0, 0} : acc;
-      if constexpr (kBf16) {
-        p = mfma16(join(w[u][0], w[u][1]), join(x[u][0], x[u][1]), p, (int)sw[u], (int)sx[u]);
-      } else {
-        const float fw = e8m0_f32(sw[u]), fx = e8m0_f32(sx[u]);
+      // the block's sum of code products, then its two scales, result by result
+      gf32x4_t p = {0, 0, 0, 0};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[u][h].x, w[u][h].y, fw),
-                                                      widen(x[u][h].x, x[u][h].y, fx), p, 0, 0, 0);
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[u][h].z, w[u][h].w, fw),
-                                                      widen(x[u][h].z, x[u][h].w, fx), p, 0, 0, 0);
-        }
+      for (int h = 0; h < 2; ++h) {
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[u][h].x, w[u][h].y, 1.0f),
+                                                    widen(x[u][h].x, x[u][h].y, 1.0f), p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[u][h].z, w[u][h].w, 1.0f),
+                                                    widen(x[u][h].z, x[u][h].w, 1.0f), p, 0, 0, 0);
       }
-      if constexpr (kF32Scale) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[r] = fmaf(p[r], n0 + kq * 4 + r < border ? swf0[u] : swf1[u], acc[r]);
-      } else {
-        acc = p;
+      for (int r = 0; r < 4; ++r) {
+        const int j = kq * 4 + r;  // the column, whose operand is in lane j
+        if constexpr (kF32Scale) {
+          const float swf = n0 + j < border ? swf0[u] : swf1[u];
+          const float s = sx[u] == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(swf, (int)sx[u] - 127);
+          acc[r] = fmaf(p[r], s, acc[r]);
+        } else {
+          const uint32_t swj = (uint32_t)__shfl((int)sw[u], j, 64);
+          acc[r] += max(sx[u], swj) == 255u ? __uint_as_float(0x7FC00000u)
+                                            : ldexpf(p[r], (int)(sx[u] + swj) - 254);
+        }
       }
     }
   }

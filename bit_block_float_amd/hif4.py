@@ -605,7 +605,8 @@ def linear_fp8(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=No
     header states the rest). A bfloat16 Y comes from the fp8 matrix instructions, which
     cut each product to 2^-13 of the largest of its run of 8 along k: at most
     7 * 2^-13 of sum |x||w| is lost, on random signs some 1e-5 of |Y|, but all of the
-    small products beside large ones that cancel. Take float32 where those count."""
+    small products beside large ones that cancel. Take float32 where those count. Up to
+    16 rows either type is the full sum."""
     _check_codes(x_codes, "x_codes")
     _check_codes(w_codes, "w_codes")
     (m, k), n = x_codes.shape, w_codes.shape[0]

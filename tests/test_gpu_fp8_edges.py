@@ -172,3 +172,47 @@ def test_linear_both_types_by_every_kernel(hip, m, n, k, kind):
     rows = torch.tensor([0, 1, 2, 15, 16, m // 2, m - 2, m - 1])
     for out in (torch.float32, torch.bfloat16):
         _check_product(hip.linear_fp8(*args, y_dtype=out)[rows.cuda()], xv[rows], wv)
+
+
+@pytest.mark.parametrize("x_byte,w_byte", [(0, 127), (1, 200), (2, 120), (127, 0), (0, 254), (254, 0), (254, 1), (1, 254),
+                                           (247, 20), (130, 3), (127, 127)])
+@pytest.mark.parametrize("m,n,k", [(1, 130, 384), (3, 41, 5120), (16, 300, 640)])
+def test_linear_few_rows_are_exact_under_every_scale(hip, m, n, k, x_byte, w_byte):
+    """Up to 16 rows: runs of products that cancel but for small ones, at every end of
+    E8M0. float32: the exact sum; bfloat16: the nearest value to it."""
+    x, w = fp8_cases.cancelling(m, n, k)
+    kb, kp, tiles = k // 128, (k // 128 + 3) // 4 * 4, (n + 127) // 128
+    scales = lambda rows, b: torch.full((rows, kp), b, dtype=torch.uint8, device="cuda").view(E8)[:, :kb]
+    want = (fp8_cases.values(x) @ fp8_cases.values(w).T) * 2.0 ** (x_byte - 127) * 2.0 ** (w_byte - 127)
+    kinds = [scales(tiles, w_byte), scales(n, w_byte)]
+    if 3 <= w_byte <= 253:
+        kinds.append(torch.full((tiles, kb), 2.0 ** (w_byte - 127), device="cuda"))
+    for ws in kinds:
+        for out in (torch.float32, torch.bfloat16):
+            y = hip.linear_fp8(x.cuda().view(F8), scales(m, x_byte), w.cuda().view(F8), ws, y_dtype=out)
+            assert torch.equal(y.double().cpu(), want if out == torch.float32 else _nearest_bf16(want)), (ws.shape, out)
+
+
+@pytest.mark.parametrize("m", [1, 16])
+def test_linear_few_rows_differing_scales(hip, m):
+    """Every column and block under a scale of its own, also beside others that are NaN."""
+    n, k = 37, 1280
+    g = torch.Generator().manual_seed(m)
+    xc = torch.randint(0, 120, (m, k), generator=g, dtype=torch.uint8)
+    wc = torch.randint(0, 120, (n, k), generator=g, dtype=torch.uint8)
+    xs = torch.randint(60, 190, (m, 12), generator=g, dtype=torch.uint8)
+    ws = torch.randint(60, 190, (n, 12), generator=g, dtype=torch.uint8)
+    xv, wv = ref64.fp8_values(xc, xs[:, :10]), ref64.fp8_values(wc, ws[:, :10])
+    args = xc.cuda().view(F8), xs.cuda().view(E8)[:, :10], wc.cuda().view(F8)
+    # scales up to 2^62 each: some columns' sums of up to 2^124 448^2 1280 leave fp32's range
+    inside = (xv.abs() @ wv.abs().T).amax(0) < 2.0 ** 127
+    assert int(inside.sum()) >= n // 2
+    for out in (torch.float32, torch.bfloat16):
+        y = hip.linear_fp8(*args, ws.cuda().view(E8)[:, :10], y_dtype=out).cpu()
+        _check_product(y[:, inside], xv, wv[inside])
+    bad = ws.clone()
+    bad[5, 3] = 255
+    y = hip.linear_fp8(*args, bad.cuda().view(E8)[:, :10]).cpu()
+    assert bool(torch.isnan(y[:, 5]).all())
+    inside[5] = False
+    _check_product(y[:, inside], xv, wv[inside])
