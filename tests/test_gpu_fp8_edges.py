@@ -216,3 +216,32 @@ def test_linear_few_rows_differing_scales(hip, m):
     assert bool(torch.isnan(y[:, 5]).all())
     inside[5] = False
     _check_product(y[:, inside], xv, wv[inside])
+
+
+def test_offsets_beyond_32_bits(hip):
+    """More than 2^31 elements of x, of codes both ways, and of Y."""
+    rows, k = 270001, 8192
+    x = torch.zeros((rows, k), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(6)
+    last = torch.randn((300, k), generator=g).to(torch.bfloat16).cuda()
+    x[-300:] = last
+    codes, scales, codes_t, scales_t = hip.quantize_fp8_both(x)
+    c2, s2 = hip.quantize_fp8(last)
+    assert torch.equal(codes[-300:].view(torch.uint8), c2.view(torch.uint8))
+    assert torch.equal(scales[-300:].view(torch.uint8), s2.view(torch.uint8))
+    tail = rows // 128 * 128  # the last block along the rows, 49 of them
+    t2, u2 = hip.quantize_fp8(x[tail:], transposed=True)
+    assert torch.equal(codes_t[:, tail:].contiguous().view(torch.uint8), t2.view(torch.uint8))
+    assert torch.equal(scales_t[:, -1:].contiguous().view(torch.uint8), u2.contiguous().view(torch.uint8))
+    back = hip.dequantize_fp8(codes, scales, out_dtype=torch.bfloat16)
+    assert torch.equal(back[-300:], hip.dequantize_fp8(c2, s2, out_dtype=torch.bfloat16))
+    del back, codes_t, scales_t, x
+    n = 8000
+    wq = hip.quantize_fp8(torch.randn((n, k), generator=g).cuda(), block_rows=128)
+    for out in (torch.bfloat16, torch.float32):
+        y = hip.linear_fp8(codes, scales, *wq, y_dtype=out)
+        assert y.numel() > 1 << 31 and not bool(y[:-300].any())
+        xv = ref64.fp8_values(_bytes(c2[:3]), _bytes(s2[:3]))
+        _check_product(y[-300:-297], xv, ref64.fp8_values(_bytes(wq[0]), _bytes(wq[1]), 128))
+        assert torch.equal(y[-256:], hip.linear_fp8(codes[-8192:], scales[-8192:], *wq, y_dtype=out)[-256:])
+        del y
