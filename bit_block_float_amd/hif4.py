@@ -481,6 +481,12 @@ def _check_out(t, name, shape, dtype):
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {shape}")
 
 
+def _workspace_bytes(t):
+    if not t.is_contiguous():  # its elements may share memory
+        raise ValueError("workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def _check_scales(t, name, rows, blocks):
     """E8M0 scales [rows][blocks] whose rows are whole 32-bit words in memory."""
     if t.dtype != torch.float8_e8m0fnu or tuple(t.shape) != (rows, blocks):
@@ -624,7 +630,7 @@ def linear_fp8(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=No
         need = linear_fp8_workspace_bytes(m, n, k)
         if workspace is None and need:
             workspace = torch.empty((need,), dtype=torch.uint8, device=x_codes.device)
-        nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        nbytes = _workspace_bytes(workspace) if workspace is not None else 0
         _ok(lib().hif4_linear_fp8(_at(x_codes), _at(x_scales), _scale_ld(x_scales), _at(w_codes),
                                   _at(w_scales), ldws, kind, block_rows, m, n, k, _at(y),
                                   _DTYPE[y_dtype], _at(workspace), nbytes, st), "hif4_linear_fp8")
@@ -669,7 +675,7 @@ def linear_fp8_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype=N
                                            _at(wt_scales), ldwt, kind, block_rows, m, n, k, _at(dx),
                                            _DTYPE[dx_dtype], _at(dw), _DTYPE[dw_dtype],
                                            _at(workspace),
-                                           workspace.numel() * workspace.element_size(), st),
+                                           _workspace_bytes(workspace), st),
             "hif4_linear_fp8_backward")
     return dx, dw
 
@@ -781,6 +787,6 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, workspace=None, stream=N
         _ok(lib().hif4_layer_norm_backward(_at(dy), _ld(dy), _at(x), _ld(x), _DTYPE[x.dtype], rows,
                                            c, _at(mean), _at(rstd), _at(weight), wd, _at(dx), c,
                                            _at(dweight), _at(dbias), _at(workspace),
-                                           workspace.numel() * workspace.element_size(), st),
+                                           _workspace_bytes(workspace), st),
             "hif4_layer_norm_backward")
     return dx, dweight, dbias

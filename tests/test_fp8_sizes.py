@@ -35,3 +35,31 @@ def test_norm_refuses_an_eps_beyond_float(L, eps):
     assert L.hif4_layer_norm(a, 0, 4, 8, 8, a, a, 0, eps, a, 8, a, a, None) == 8
     assert L.hif4_layer_norm_quantize(a, 0, 4, 64, 64, a, a, 0, eps, None, 0, None, a, a, None) == 8
     assert L.hif4_layer_norm_quantize_fp8(a, 0, 4, 8, 8, a, a, 0, eps, a, a, 4, None) == 8
+
+
+def test_binding_refuses_a_workspace_that_is_not_contiguous():
+    """An expanded tensor has the elements, but not the memory."""
+    import torch
+
+    from bit_block_float_amd import hif4
+    assert hif4._workspace_bytes(torch.empty(300)) == 1200
+    for t in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty((8, 8)).T[1:]):
+        with pytest.raises(ValueError):
+            hif4._workspace_bytes(t)
+
+
+@pytest.mark.gpu
+def test_calls_refuse_a_workspace_that_is_not_contiguous(hip):
+    import torch
+    wide = torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 28)
+    x, w = torch.ones((300, 4224), device="cuda"), torch.ones((96, 4224), device="cuda")
+    xq, wq = hip.quantize_fp8(x), hip.quantize_fp8(w, block_rows=128)
+    assert hip.linear_fp8_workspace_bytes(300, 96, 4224) > 0
+    with pytest.raises(ValueError):
+        hip.linear_fp8(*xq, *wq, workspace=wide)
+    xt, wt = hip.quantize_fp8(x, transposed=True), hip.quantize_fp8(w, block_rows=128, transposed=True)
+    with pytest.raises(ValueError):
+        hip.linear_fp8_backward(torch.ones((300, 96), device="cuda"), *xt, *wt, workspace=wide)
+    _, mean, rstd = hip.layer_norm(x)
+    with pytest.raises(ValueError):
+        hip.layer_norm_backward(x, x, mean, rstd, workspace=wide)
