@@ -5,14 +5,16 @@
 // sx is a power of two (E8M0), and so is sw where the library quantized it.
 //
 // Which matrix instruction, by the type of Y (beyond 16 rows; up to there the bf16
-// forms cost nothing, see gemm_fp8_skinny_kernel):
+// forms cost next to nothing, see gemm_fp8_skinny_kernel):
 //  - bf16: v_mfma_scale_f32_32x32x64_f8f6f4 on the codes as they are, both E8M0
 //    bytes applied by the instruction. Measured on gfx950 (and the same for the
 //    unscaled fp8 forms): within each run of 8 consecutive K values a product
 //    is cut to a multiple of 2^-13 of the largest one's power of two before the
 //    8 are added; the runs and the accumulator add in full fp32. The loss is at
 //    most 7 * 2^-13 of each run's largest product, on random signs some 1e-5 of
-//    |Y|: far below the 2^-9 rounding of a bf16 result, and half the time.
+//    |Y|: far below the 2^-8 rounding of a bf16 result, and half the time. (Where a
+//    run's large products cancel, its small ones are lost: hif4.h says so, and that
+//    a float32 Y has them.)
 //  - fp32: the codes are widened to bf16 (v_cvt_scalef32_pk_bf16_fp8, with the
 //    power-of-two scale applied: exact for scale bytes 3 to 246; below, bf16 has no
 //    bits under 2^-133 and rounds, above, its range ends) and multiplied by the bf16
@@ -474,7 +476,7 @@ __global__ __launch_bounds__(256) void gemm_fp8_reduce_kernel(const float* __res
 // be busy as long as the matrix cores.
 //
 // Bound: the matrix cores at the clock that the chip's power allows. Measured on
-// 57600 x 13824 x 5120, bf16 Y: 2.95 to 3.14 ms (2.6 to 2.76 PFLOP/s), the matrix
+// 57600 x 13824 x 5120, bf16 Y: 2.95 to 3.17 ms (2.57 to 2.76 PFLOP/s), the matrix
 // cores busy 73% of the cycles; without any load, LDS read or store it would take
 // 2.1 ms. fp32 Y (bf16 instructions): 5.74 ms, 1.42 PFLOP/s. Workgroups that stay
 // and run on from tile to tile, with the next tile's first blocks loaded ahead,
@@ -697,8 +699,10 @@ void gemm_fp8_pair_kernel(GemmArgs a, GemmArgs b, uint32_t first) {
 // The codes are widened to bf16 without their scales (exact), so a block's sum is a
 // full fp32 sum of exact products for either type of Y; then its two scales are
 // applied as one exponent, so that only the result has to be in fp32's range. The
-// fp8 instructions, which would cut products, are no faster here: 1 x 13824 x 5120
-// with float32 scales 13.1 us both ways, 16 x 5120 x 5120 10.9 and 11.2.
+// fp8 instructions, which would cut products, gain little here, W's bytes being what
+// counts (us, they and this): 1 x 13824 x 5120 with float32 scales 13.1 and 13.1, 1 x
+// 5120 x 13824 15.5 and 15.4, 16 x 5120 x 5120 10.9 and 11.2, 16 x 13824 x 5120 with
+// six weights in turn 24.8 and 25.8.
 //
 // What a CU can have in flight to memory sets the pace, so the columns are cut to
 // give every CU the same share: cols is the least that leaves as many workgroups
@@ -762,17 +766,19 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
         p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[u][h].z, w[u][h].w, 1.0f),
                                                     widen(x[u][h].z, x[u][h].w, 1.0f), p, 0, 0, 0);
       }
+      if constexpr (kF32Scale) {
+        const float nan = __uint_as_float(0x7FC00000u);
+        const float s0 = sx[u] == 255u ? nan : __builtin_amdgcn_ldexpf(swf0[u], (int)sx[u] - 127);
+        const float s1 = sx[u] == 255u ? nan : __builtin_amdgcn_ldexpf(swf1[u], (int)sx[u] - 127);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int j = kq * 4 + r;  // the column, whose operand is in lane j
-        if constexpr (kF32Scale) {
-          const float swf = n0 + j < border ? swf0[u] : swf1[u];
-          const float s = sx[u] == 255u ? __uint_as_float(0x7FC00000u) : ldexpf(swf, (int)sx[u] - 127);
-          acc[r] = fmaf(p[r], s, acc[r]);
-        } else {
-          const uint32_t swj = (uint32_t)__shfl((int)sw[u], j, 64);
+        for (int r = 0; r < 4; ++r) acc[r] = fmaf(p[r], n0 + kq * 4 + r < border ? s0 : s1, acc[r]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          // the column's operand is in lane kq * 4 + r
+          const uint32_t swj = (uint32_t)__shfl((int)sw[u], kq * 4 + r, 64);
           acc[r] += max(sx[u], swj) == 255u ? __uint_as_float(0x7FC00000u)
-                                            : ldexpf(p[r], (int)(sx[u] + swj) - 254);
+                                            : __builtin_amdgcn_ldexpf(p[r], (int)(sx[u] + swj) - 254);
         }
       }
     }

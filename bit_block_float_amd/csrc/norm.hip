@@ -3,8 +3,9 @@
 // weight's and bias' gradients. HBM-streaming kernels for gfx950.
 //
 // Forward: y = (x - mean) rstd w + b with rstd = (var + eps)^(-1/2). A row is
-// held in registers from its one read, so the variance is the mean of
-// (x - mean)^2 over the same registers, not a difference of two large sums.
+// held in registers from its one read (part of one of more than 16384 columns in
+// scratch memory), so the variance is the mean of (x - mean)^2 over what was read,
+// not a difference of two large sums.
 // Backward, with xhat = (x - mean) rstd and g = dy w:
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)),
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy.
@@ -301,9 +302,15 @@ __global__ __launch_bounds__(512) void layer_norm_wave_kernel(NormArgs a) {
 // Forward of the widest rows (over 16384 columns): 1024 threads share a row, a
 // lane owns items (16 consecutive elements) t, t + 1024, ..., the quantizers' own
 // mapping, so 4 aligned lanes hold a HiF4 unit and 8 an E4M3 block when the row
-// leaves through one of them. The value
-// quantized is the one kOutY would store (rounded to bf16 for HiF4, to x's type
-// for E4M3), so the codes are those of the two calls in turn.
+// leaves through one of them. The value quantized is the one kOutY would store
+// (rounded to bf16 for HiF4, to x's type for E4M3), so the codes are those of the
+// two calls in turn.
+//
+// Bound: not by HBM. 64 columns a lane do not fit the 128 registers that 1024
+// threads leave (380 to 932 bytes of scratch a lane), and weight and bias are read
+// again for each row. Measured, 4096 rows of bf16: 20480 columns 480 us (0.7 TB/s),
+// to HiF4 615, to E4M3 503; 65536 columns 778, 900 and 800 us; of 16384 columns, by
+// the kernel below, 64 us.
 template <typename T, int kItems, int kOut, int kRows>
 __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(NormArgs a) {
   constexpr int P = 1024;
@@ -522,13 +529,15 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
 
 // Backward. A workgroup walks rows blockIdx.x, + gridDim.x, ...; a thread owns
 // the same kRuns runs of 8 columns in every row and keeps their weight and its
-// part of dw and db in registers. Behind a row's last column x and dy are 0, and
-// xhat = -mean rstd may overflow: infinity times 0 would make the whole row's
-// mean(g xhat) a NaN. So the mean is 0 there, or (where a run may be part of a row) x
-// another element of it. The parts of all workgroups go to `parts`
-// ([gridDim.x][2][c]) and are added in a fixed order by the kernel below. Bound: HBM,
-// x and dy read and dx written once: 57600 x 5120 bf16 323 us (5.5 TB/s), 57600 x
-// 13824 907 us (5.3 TB/s), 777 x 1003 fp32 8.2 us.
+// part of dw and db in registers (with 4 or 8 runs, beyond 16384 columns, mostly in
+// scratch memory). The parts of all workgroups go to `parts` ([gridDim.x][2][c]) and
+// are added in a fixed order by the kernel below.
+// Behind a row's last column x and dy are 0, and xhat = -mean rstd may overflow:
+// infinity times 0 would make the whole row's mean(g xhat) a NaN. So the mean is 0
+// there, or (where a run may be part of a row) x another element of the row.
+// Bound: HBM, x and dy read and dx written once: 57600 x 5120 bf16 325 us (5.4 TB/s),
+// 57600 x 13824 925 us (5.2 TB/s), 777 x 1003 fp32 8.2 us; but 4096 x 20480 504 us
+// (1.0 TB/s) and 4096 x 65536 3.5 ms, by their scratch memory.
 template <typename T, int kRuns, bool kSums, int kRows>
 __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(NormBackArgs a) {
   __shared__ float sums[2][2][16];
@@ -727,8 +736,11 @@ __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(const float* __r
 // A wave per row against it, into a quantizer: HiF4 57600 x 5120 215 and 315,
 // 57600 x 6144 295 and 349, 2048 x 5120 12.5 and 17.8, 1024 x 5120 11.5 and 10.2;
 // but 57600 x 4096 185 and 163, 57600 x 8192 486 and 323 (E4M3 the same way: 176 and
-// 213, 226 and 258, 144 and 139, 329 and 286): workgroups of 5 and 6 waves leave the
-// SIMDs of a CU unevenly filled, 4 and 8 do not.
+// 213, 226 and 258, 144 and 139, 329 and 286). At 57600 x 7168 the two outputs differ:
+// HiF4 421 and 361, E4M3 253 and 272; so 5 and 6 waves for both. Workgroups of 5, 6
+// and 7 waves leave the SIMDs of a CU unevenly filled, 4 and 8 do not; and a wave's own
+// row needs more registers with every 1024 columns. More than 8 waves were not tried
+// (weight and bias would leave 64 KB of LDS).
 template <typename T, int kOut, int kRows>
 static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
   const int items = kOut == kOutFp8 ? a.kp / 16 : (a.c + 15) / 16;
