@@ -698,11 +698,12 @@ void gemm_fp8_pair_kernel(GemmArgs a, GemmArgs b, uint32_t first) {
 //
 // The codes are widened to bf16 without their scales (exact), so a block's sum is a
 // full fp32 sum of exact products for either type of Y; then its two scales are
-// applied as one exponent, so that only the result has to be in fp32's range. The
-// fp8 instructions, which would cut products, gain little here, W's bytes being what
-// counts (us, they and this): 1 x 13824 x 5120 with float32 scales 13.1 and 13.1, 1 x
-// 5120 x 13824 15.5 and 15.4, 16 x 5120 x 5120 10.9 and 11.2, 16 x 13824 x 5120 with
-// six weights in turn 24.8 and 25.8.
+// applied as one exponent (a float scale's significand by the FMA that adds the
+// block), so that only the result has to be in fp32's range. The fp8 instructions,
+// which would cut products, gain little, W's bytes being what counts. With six
+// weights in turn, they and this, us: float32 scales 1 x 13824 x 5120 14.4 and 14.9, 16
+// x 13824 x 5120 24.5 and 24.6; E8M0 tiles 1 x 5120 x 13824 18.3 and 17.2, 16 x 13824 x
+// 5120 25.0 and 24.9; E8M0 rows 25.8 and 26.9.
 //
 // What a CU can have in flight to memory sets the pace, so the columns are cut to
 // give every CU the same share: cols is the least that leaves as many workgroups
@@ -712,11 +713,13 @@ void gemm_fp8_pair_kernel(GemmArgs a, GemmArgs b, uint32_t first) {
 // the other way about, 14.3 and 12.0 us.)
 constexpr int kSkinnyRows = 16;
 constexpr int kSkinnyWaves = 16;
-template <bool kF32Scale, bool kBf16>
+// kTiles: W's scales are one per 128 x 128, float32 or E8M0; else E8M0 bytes per row.
+template <bool kTiles, bool kF32Scale, bool kBf16>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
     const uint8_t* __restrict__ X, const uint8_t* __restrict__ XS, int64_t ldxs,
-    const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int w_shift, int M,
-    int64_t N, int K, int cols, void* __restrict__ Y) {
+    const uint8_t* __restrict__ W, const void* __restrict__ WS, int64_t ldws, int M, int64_t N,
+    int K, int cols, void* __restrict__ Y) {
+  static_assert(kTiles || !kF32Scale, "float32 scales are per 128 x 128");
   __shared__ gf32x4_t part[kSkinnyWaves][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -727,11 +730,24 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
   // of each block lane group kq takes bytes 16 kq and 64 + 16 kq on, of both operands
   const uint8_t* wp = W + wr * K + kq * 16;
   const uint8_t* xp = X + (int64_t)xr * K + kq * 16;
-  const uint8_t* wsb = (const uint8_t*)WS + (wr >> w_shift) * ldws;
+  const uint8_t* wsb = (const uint8_t*)WS + wr * ldws;
   const uint8_t* xsb = XS + (int64_t)xr * ldxs;
-  // float32 scales: the columns lie in one block row, or two
-  const float* wsf0 = (const float*)WS + (n0 >> 7) * ldws;
-  const float* wsf1 = (const float*)WS + ((n1 - 1) >> 7) * ldws;
+  // kTiles: the columns lie in one block row, or two
+  const int64_t ws0 = (n0 >> 7) * ldws, ws1 = ((n1 - 1) >> 7) * ldws;
+  auto scale_of = [&](int64_t row, int k) {  // as f 2^q: 1 <= |f| < 2 (a power of two: f = 1)
+    struct { float f; int q; } r;
+    if constexpr (kF32Scale) {
+      const float s = reinterpret_cast<const float*>(WS)[row + k];
+      r.f = 2.0f * __builtin_amdgcn_frexp_mantf(s);
+      r.q = __builtin_amdgcn_frexp_expf(s) - 1;
+    } else {
+      const uint32_t b =
+          reinterpret_cast<const uint32_t*>((const uint8_t*)WS + row)[k >> 2] >> (8 * (k & 3)) & 255u;
+      r.f = b == 255u ? __uint_as_float(0x7FC00000u) : 1.0f;
+      r.q = (int)b - 127;
+    }
+    return r;
+  };
   const int64_t border = ((n1 - 1) >> 7) << 7;  // first column of the second
   gf32x4_t acc = {0, 0, 0, 0};
   const int KB = K / 128;
@@ -741,7 +757,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
   for (int kb = wave; kb < KB; kb += kU * kSkinnyWaves) {
     gu32x4_t w[kU][2], x[kU][2];
     uint32_t sw[kU], sx[kU];
-    float swf0[kU], swf1[kU];
+    decltype(scale_of(0, 0)) t0[kU], t1[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int k = min(kb + u * kSkinnyWaves, KB - 1);
@@ -750,9 +766,12 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
       x[u][0] = *reinterpret_cast<const gu32x4_t*>(xp + (int64_t)k * 128);
       x[u][1] = *reinterpret_cast<const gu32x4_t*>(xp + (int64_t)k * 128 + 64);
       sx[u] = xsb[k];
-      sw[u] = kF32Scale ? 0u : wsb[k];
-      swf0[u] = kF32Scale ? wsf0[k] : 1.0f;
-      swf1[u] = kF32Scale ? wsf1[k] : 1.0f;
+      if constexpr (kTiles) {
+        t0[u] = scale_of(ws0, k);
+        t1[u] = scale_of(ws1, k);
+      } else {
+        sw[u] = wsb[k];
+      }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -766,12 +785,15 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void gemm_fp8_skinny_kernel(
         p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(w[u][h].z, w[u][h].w, 1.0f),
                                                     widen(x[u][h].z, x[u][h].w, 1.0f), p, 0, 0, 0);
       }
-      if constexpr (kF32Scale) {
+      if constexpr (kTiles) {
         const float nan = __uint_as_float(0x7FC00000u);
-        const float s0 = sx[u] == 255u ? nan : __builtin_amdgcn_ldexpf(swf0[u], (int)sx[u] - 127);
-        const float s1 = sx[u] == 255u ? nan : __builtin_amdgcn_ldexpf(swf1[u], (int)sx[u] - 127);
+        const float f0 = sx[u] == 255u ? nan : t0[u].f, f1 = sx[u] == 255u ? nan : t1[u].f;
+        const int e0 = (int)sx[u] - 127 + t0[u].q, e1 = (int)sx[u] - 127 + t1[u].q;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] = fmaf(p[r], n0 + kq * 4 + r < border ? s0 : s1, acc[r]);
+        for (int r = 0; r < 4; ++r) {
+          const bool first = n0 + kq * 4 + r < border;
+          acc[r] = fmaf(__builtin_amdgcn_ldexpf(p[r], first ? e0 : e1), first ? f0 : f1, acc[r]);
+        }
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -855,10 +877,19 @@ static hipError_t launch_gemm(const Fp8Product& p, void* workspace, hipStream_t 
     case kSkinny: {
       const int64_t per_cu = (p.n + 16 * kCus - 1) / (16 * kCus);
       const int cols = (int)((p.n + kCus * per_cu - 1) / (kCus * per_cu));  // 1 .. 16
-      hipLaunchKernelGGL((gemm_fp8_skinny_kernel<kF32Scale, kBf16>),
-                         dim3((unsigned)((p.n + cols - 1) / cols)), dim3(kSkinnyWaves * 64), 0,
-                         stream, p.x, p.xs, p.ldxs, p.w, p.ws, p.ldws, p.w_block == 128 ? 7 : 0,
-                         (int)p.m, p.n, (int)p.k, cols, p.y);
+      const auto launch = [&](auto tiles) {
+        hipLaunchKernelGGL((gemm_fp8_skinny_kernel<decltype(tiles)::value, kF32Scale, kBf16>),
+                           dim3((unsigned)((p.n + cols - 1) / cols)), dim3(kSkinnyWaves * 64), 0,
+                           stream, p.x, p.xs, p.ldxs, p.w, p.ws, p.ldws, (int)p.m, p.n, (int)p.k,
+                           cols, p.y);
+      };
+      if constexpr (!kF32Scale) {
+        if (p.w_block == 1) {
+          launch(std::false_type{});
+          break;
+        }
+      }
+      launch(std::true_type{});
       break;
     }
     case kLarge:

@@ -9,6 +9,7 @@ from test_gpu_fp8 import _check_product, _linear_case
 
 pytestmark = pytest.mark.gpu
 
+U = 2.0 ** -24  # half a step of fp32
 F8, E8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 
@@ -245,3 +246,29 @@ def test_offsets_beyond_32_bits(hip):
         _check_product(y[-300:-297], xv, ref64.fp8_values(_bytes(wq[0]), _bytes(wq[1]), 128))
         assert torch.equal(y[-256:], hip.linear_fp8(codes[-8192:], scales[-8192:], *wq, y_dtype=out)[-256:])
         del y
+
+
+@pytest.mark.parametrize("power,x_byte", [(-90, 82), (-95, 79), (-126, 247), (-140, 200), (120, 27), (126, 1), (-60, 60), (0, 127)])
+@pytest.mark.parametrize("m", [1, 16])
+def test_linear_few_rows_float_scales_of_any_size(hip, m, power, x_byte):
+    """Float32 weight scales whose product with X's leaves the normal numbers, while the
+    results do not: only the results have to be in range."""
+    n, k = 300, 640
+    g = torch.Generator().manual_seed(m)
+    xc = torch.randint(0, 120, (m, k), generator=g, dtype=torch.uint8)
+    wc = torch.randint(0, 120, (n, k), generator=g, dtype=torch.uint8)
+    xs = torch.full((m, 8), x_byte, dtype=torch.uint8)
+    s32 = ((1 + torch.rand((3, 5), generator=g)).double() * 2.0 ** power).float()
+    xv, wv = ref64.fp8_values(xc, xs[:, :5]), ref64.fp8_values(wc, s32, 128)
+    size = xv.abs() @ wv.abs().T
+    # (additions below 2^-126 are exact: U times a size above it counts every rounding)
+    assert 2.0 ** -126 < float(size.min()) and float(size.max()) < 2.0 ** 127
+    args = xc.cuda().view(F8), xs.cuda().view(E8)[:, :5], wc.cuda().view(F8), s32.cuda()
+    for out in (torch.float32, torch.bfloat16):
+        y = hip.linear_fp8(*args, y_dtype=out)
+        want = xv @ wv.T
+        # k additions, a rounding a block, one of the result: nothing is cut for either type
+        tol = (k + k // 128 + 1) * U * size
+        if out == torch.bfloat16:
+            tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+        assert bool(((y.double().cpu() - want).abs() <= tol).all()), out
