@@ -493,7 +493,7 @@ HIF4_EXPORT size_t hif4_linear_fp8_workspace_bytes(int64_t m, int64_t n, int64_t
  *  consecutive K values to 2^-13 of the largest one's power of two: less than
  *  7 * 2^-13 of sum |x||w| at worst (a run whose large products cancel keeps
  *  nothing of its small ones), some 1e-5 of |Y| on random signs. Where that
- *  matters, ask for a float32 Y. For m <= 16 both types are full fp32 sums of
+ *  matters, ask for a float32 Y. For m <= 16 (n <= 2^26 - 16) both are full sums of
  *  exact products under every scale byte.
  */
 HIF4_EXPORT hif4_status hif4_linear_fp8(const uint8_t *x_codes, const uint8_t *x_scales,
