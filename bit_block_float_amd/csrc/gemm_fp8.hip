@@ -476,7 +476,7 @@ __global__ __launch_bounds__(256) void gemm_fp8_reduce_kernel(const float* __res
 // be busy as long as the matrix cores.
 //
 // Bound: the matrix cores at the clock that the chip's power allows. Measured on
-// 57600 x 13824 x 5120, bf16 Y: 2.95 to 3.17 ms (2.57 to 2.76 PFLOP/s), the matrix
+// 57600 x 13824 x 5120, bf16 Y: 2.95 to 3.21 ms (2.54 to 2.76 PFLOP/s), the matrix
 // cores busy 73% of the cycles; without any load, LDS read or store it would take
 // 2.1 ms. fp32 Y (bf16 instructions): 5.74 ms, 1.42 PFLOP/s. Workgroups that stay
 // and run on from tile to tile, with the next tile's first blocks loaded ahead,
