@@ -116,6 +116,24 @@ hif4_status hif4_layer_norm_quantize_fp8(const void* x, int x_dtype, int64_t row
   return launched(hif4_launch_layer_norm(a, x_dtype == HIF4_BF16, 2, stream));
 }
 
+hif4_status hif4_layer_norm_quantize_mxfp4(const void* x, int x_dtype, int64_t rows, int64_t c,
+                                           int64_t ld, const void* weight, const void* bias, int w_dtype,
+                                           double eps, uint8_t* codes, uint8_t* scales,
+                                           hipStream_t stream) {
+  hif4::NormArgs a;
+  hif4_status st = check_forward(x, x_dtype, rows, c, ld, weight, bias, w_dtype, eps, a);
+  if (st != HIF4_OK) return st;
+  if (rows == 0) return HIF4_OK;
+  if (!codes || !scales) return HIF4_ERR_NULL;
+  if (!aligned(codes, 16) || !aligned(scales, 4)) return HIF4_ERR_ALIGN;
+  a.codes = codes;
+  a.scales = scales;
+  a.kp = (int)((c + 127) / 128 * 128);
+  st = check_device();
+  if (st != HIF4_OK) return st;
+  return launched(hif4_launch_layer_norm(a, x_dtype == HIF4_BF16, 3, stream));
+}
+
 size_t hif4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t c) {
   if (rows < 0 || rows >= (int64_t(1) << 31) || c < 1 || c > kMaxC) return 0;
   return align256((size_t)hif4_layer_norm_backward_parts(rows, c) * 2 * (size_t)c * sizeof(float));

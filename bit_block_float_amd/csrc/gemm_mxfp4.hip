@@ -1,0 +1,490 @@
+// gemm_mxfp4.hip -- Y = X W^T on E2M1 codes with a power-of-two (E8M0) scale per 32
+// along K, on gfx950's scaled matrix cores; one W, one W for each group of rows, or
+// one Y for each group along K.
+//
+// Y[i][j] = sum_b sx[i][b] sw[j][b] sum_{t in block b} cx[i][t] cw[j][t].
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4 (16x16x128 up to 16 rows) on the codes as they
+// are. A lane's operand is 32 consecutive values of a row, one block, and the scale
+// byte that it gives is that block's. Measured on gfx950: the 4-bit products are
+// exact (unlike the 8-bit forms nothing is cut, also where large products of a run
+// cancel), and the sums over a block, over the instruction's blocks and onto the
+// accumulator are those of fp32: from 64 to 128 products at a time the error stayed
+// within 2^-23 of the sum of magnitudes, scale bytes 0 to 254 on either side. So
+// results of either type come from the same sums, rounded once for bf16.
+//
+// The MFMA's first operand is W, so a lane of the result holds one row of Y
+// (its column index) and runs of 4 consecutive columns.
+#include <algorithm>
+#include <type_traits>
+
+#include "gemm_tile_dev.h"
+#include "mxfp4_dev.h"
+
+namespace hif4 {
+
+constexpr int kFmtE2M1 = 4;  // cbsz / blgp of the f8f6f4 forms
+
+__device__ __forceinline__ i32x8_t operand(gu32x4_t v) {
+  return i32x8_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+}
+// 64 values along K; the scale bytes are byte kByte of sa and sb.
+template <int kByte>
+__device__ __forceinline__ gf32x16_t mfma64(gu32x4_t a, gu32x4_t b, gf32x16_t c, uint32_t sa, uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), c, kFmtE2M1, kFmtE2M1,
+                                                         kByte, (int)sa, kByte, (int)sb);
+}
+__device__ __forceinline__ gf32x4_t mfma128(gu32x4_t a, gu32x4_t b, gf32x4_t c, uint32_t sa, uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), operand(b), c, kFmtE2M1, kFmtE2M1,
+                                                          0, (int)sa, 0, (int)sb);
+}
+
+// This wave's loads but the newest n have landed, its LDS reads are done.
+template <int n>
+__device__ __forceinline__ void wait_mx4() {
+  static_assert(n == 0 || n == 5 || n == 10, "one asm a count");
+  if constexpr (n == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  if constexpr (n == 5) asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)" ::: "memory");
+  if constexpr (n == 10) asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)" ::: "memory");
+}
+
+struct Mx4Args {
+  const uint8_t *x, *xs;
+  const uint8_t *w, *ws;
+  uint32_t ldx, ldw;  // bytes of a row of codes (a multiple of 64); of scales a 16th
+  int64_t m, n;
+  int runs;  // of 128 along K (kMx4Depth: of a whole row)
+  void* y;
+  bool y_bf16;
+  int mode;
+  uint32_t tiles_m, tiles_n;  // kMx4Rows: tiles_m is the most that the groups can have
+  Groups groups;
+};
+
+// One tile of Y: its operands from their first row and first run on.
+struct Mx4Tile {
+  const uint8_t *x, *xs, *w, *ws;
+  int mrows, nrows, runs;
+  int64_t row0, col0, m;  // in Y, whose rows end at m
+  char* y;
+};
+
+// Tile t of the product; false: there is none (groups have fewer than their most).
+template <int BM, int BN>
+__device__ __forceinline__ bool mx4_locate(const Mx4Args& a, uint32_t t, Mx4Tile& tile) {
+  constexpr int kShift = BM == 16 ? 4 : BM == 64 ? 6 : BM == 128 ? 7 : 8;
+  static_assert(1 << kShift == BM, "a tile's rows");
+  int64_t tm, tn, group = 0, k0 = 0;
+  int64_t rows_begin = 0, rows_end = a.m;
+  tile.runs = a.runs;
+  if (a.mode == kMx4Plain) {
+    tile_of(t, a.tiles_m, a.tiles_n, tm, tn);
+  } else if (a.mode == kMx4Rows) {
+    const uint32_t total = group_units(a.groups, kShift) * a.tiles_n;
+    if (t >= total) return false;
+    t = xcd_order(t, total);
+    int e;
+    uint32_t before;
+    if (!group_unit(a.groups, kShift, t / a.tiles_n, e, before)) return false;
+    group_range(a.groups, e, rows_begin, rows_end);
+    const uint32_t own = (uint32_t)((rows_end - rows_begin + BM - 1) >> kShift);
+    tile_in(t - before * a.tiles_n, own, a.tiles_n, tm, tn);
+    group = e;
+  } else {
+    const uint32_t per = a.tiles_m * a.tiles_n;
+    t = xcd_order(t, per * (uint32_t)a.groups.count);
+    const uint32_t e = t / per;
+    tile_in(t - e * per, a.tiles_m, a.tiles_n, tm, tn);
+    int64_t begin, end;
+    group_range(a.groups, (int)e, begin, end);
+    // within the row, whatever the offsets say
+    k0 = min((int64_t)units_before(a.groups, 7, (int)e), (int64_t)a.runs);
+    tile.runs = (int)min((end - begin + 127) >> 7, a.runs - k0);
+    group = e;
+  }
+  tile.row0 = rows_begin + tm * BM;
+  tile.col0 = tn * BN;
+  tile.m = rows_end;
+  if (tile.row0 >= rows_end || tile.col0 >= a.n) return false;
+  tile.mrows = (int)min((int64_t)BM, rows_end - tile.row0);
+  tile.nrows = (int)min((int64_t)BN, a.n - tile.col0);
+  const int64_t wrow = tile.col0 + (a.mode == kMx4Rows ? group * a.n : 0);
+  tile.x = a.x + tile.row0 * a.ldx + k0 * 64;
+  tile.xs = a.xs + tile.row0 * (a.ldx / 16) + k0 * 4;
+  tile.w = a.w + wrow * a.ldw + k0 * 64;
+  tile.ws = a.ws + wrow * (a.ldw / 16) + k0 * 4;
+  tile.y = reinterpret_cast<char*>(a.y) + (a.mode == kMx4Depth ? group * a.m * a.n * (a.y_bf16 ? 2 : 4) : 0);
+  return true;
+}
+
+// A tile's operands as buffers: what lies past their last row, or past the last
+// row's end, reads as zero.
+struct Mx4Buffers {
+  __amdgpu_buffer_rsrc_t x, xs, w, ws;
+  __device__ __forceinline__ Mx4Buffers(const Mx4Tile& t, uint32_t ldx, uint32_t ldw)
+      : x(__builtin_amdgcn_make_buffer_rsrc((void*)t.x, (short)0, (t.mrows - 1) * ldx + t.runs * 64, kRsrc3)),
+        xs(__builtin_amdgcn_make_buffer_rsrc((void*)t.xs, (short)0, (t.mrows - 1) * (ldx / 16) + t.runs * 4,
+                                             kRsrc3)),
+        w(__builtin_amdgcn_make_buffer_rsrc((void*)t.w, (short)0, (t.nrows - 1) * ldw + t.runs * 64, kRsrc3)),
+        ws(__builtin_amdgcn_make_buffer_rsrc((void*)t.ws, (short)0, (t.nrows - 1) * (ldw / 16) + t.runs * 4,
+                                             kRsrc3)) {}
+};
+
+// BM x BN of Y a workgroup, kWM x kWN waves. A stage is 256 values along K (two runs
+// of 128): rows of 128 bytes = 8 chunks of 16, chunk c of row r in slot c ^ ((r >> 1)
+// & 7), so that the fragment reads of 16 consecutive rows land in distinct bank
+// groups, and behind them 16 bytes of scales a row (the stage's 8, and 8 more). kStages
+// of them are in LDS, brought by direct-to-LDS buffer loads, 8 rows of codes or 64 of
+// scales an instruction, the swizzle applied to the global address. Loads past the last
+// stage repeat it, into stages that no one reads; a last stage of one run only has
+// bytes in its second half that are not used.
+//
+// Part `split`: stages [split per_split, (split + 1) per_split) only, the sums to that
+// plane of Y as float32 (few tiles and a long K: the parts are added by
+// mx4_reduce_kernel in order).
+template <int BM, int BN, int kStages>
+constexpr int kMx4Lds = kStages * (BM + BN) * (128 + 16) + 1024;  // stages, a sink for idle scale loads
+template <int BM, int BN, int kWM, int kWN, int kStages>
+__device__ __forceinline__ void mx4_tile(const Mx4Args& a, uint32_t t, int split, int per_split,
+                                         char* const lds) {
+  constexpr int kWaves = kWM * kWN;
+  constexpr int kTM = BM / kWM / 32, kTN = BN / kWN / 32;  // 32 x 32 blocks of a wave
+  constexpr int kCodes = (BM + BN) * 128, kStage = kCodes + (BM + BN) * 16;
+  constexpr int kGroups = (BM + BN) / 64;  // of 64 rows' scales
+  static_assert(kGroups <= kWaves, "one group a wave");
+
+  Mx4Tile tile;
+  if (!mx4_locate<BM, BN>(a, t, tile)) return;
+  const Mx4Buffers buf(tile, a.ldx, a.ldw);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / kWN, wn = wave % kWN;
+  const int stages = (tile.runs + 1) / 2;
+  const int kb0 = split * per_split, kb1 = min(kb0 + per_split, stages);
+
+  // this wave's scale rows: X's (groups 0 ..), then W's; waves without a group read
+  // X's first row into the sink
+  const bool has = wave < kGroups, of_x = wave < BM / 64 || !has;
+  const __amdgpu_buffer_rsrc_t rs = of_x ? buf.xs : buf.ws;
+  const uint32_t soff = !has ? 0u : of_x ? (uint32_t)(wave * 64 + lane) * (a.ldx / 16)
+                                         : (uint32_t)((wave - BM / 64) * 64 + lane) * (a.ldw / 16);
+
+  constexpr int kLoads = (BM + BN) / 8 / kWaves;  // of codes, per wave and stage
+  constexpr int kXLoads = BM / 8 / kWaves;
+  static_assert((BM + BN) % (8 * kWaves) == 0 && BM % (8 * kWaves) == 0, "whole loads a wave");
+  uint32_t voff[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const bool x = i < kXLoads;
+    const int row = (x ? wave * kXLoads + i : wave * (kLoads - kXLoads) + i - kXLoads) * 8 + (lane >> 3);
+    voff[i] = (uint32_t)row * (x ? a.ldx : a.ldw) + (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
+  }
+  auto load_stage = [&](int kb, int slot) {
+    char* base = lds + slot * kStage;
+    const int blk = min(kb, kb1 - 1);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (i < kXLoads)
+        load_lds16(buf.x, base + (wave * kXLoads + i) * 1024, voff[i], blk * 128);
+      else
+        load_lds16(buf.w, base + BM * 128 + (wave * (kLoads - kXLoads) + i - kXLoads) * 1024, voff[i],
+                   blk * 128);
+    }
+    load_lds16(rs, has ? base + kCodes + wave * 1024 : lds + kStages * kStage, soff, blk * 8);
+  };
+
+  gf32x16_t acc[kTN][kTM];
+#pragma unroll
+  for (int i = 0; i < kTN; ++i)
+#pragma unroll
+    for (int j = 0; j < kTM; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  const int frow = lane & 31, fhalf = lane >> 5, fsw = (frow >> 1) & 7;
+  const int xrow = wm * (BM / kWM) + frow, wrow = wn * (BN / kWN) + frow;
+  if (kb0 < kb1) {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) load_stage(kb0 + s, s);
+  }
+  int slot = 0;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    // stage kb has landed for this wave (the loads of the kStages - 2 after it may
+    // be in flight); after the barrier for all, and every wave has read the stage
+    // that is loaded next
+    wait_mx4<(kStages - 2) * (kLoads + 1)>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    load_stage(kb + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+    const char* const stage = lds + slot * kStage;
+    slot = slot == kStages - 1 ? 0 : slot + 1;
+    gu32x2_t sx[kTM], sw[kTN];  // scale words of the two runs
+#pragma unroll
+    for (int j = 0; j < kTM; ++j)
+      sx[j] = *reinterpret_cast<const gu32x2_t*>(stage + kCodes + (xrow + j * 32) * 16);
+#pragma unroll
+    for (int i = 0; i < kTN; ++i)
+      sw[i] = *reinterpret_cast<const gu32x2_t*>(stage + kCodes + (BM + wrow + i * 32) * 16);
+    const char* xs = stage + xrow * 128;
+    const char* ws = stage + (BM + wrow) * 128;
+    // Run h: lanes 0..31 chunks 4h, 4h + 2, lanes 32..63 the ones behind those; a
+    // chunk is a block, its scale the byte of the same number.
+    auto run = [&](int h) {
+      auto chunk = [&](const char* row, int s) {
+        return *reinterpret_cast<const gu32x4_t*>(row + (((4 * h + 2 * s + fhalf) ^ fsw) * 16));
+      };
+      gu32x4_t fx[kTM][2];
+#pragma unroll
+      for (int j = 0; j < kTM; ++j)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) fx[j][s] = chunk(xs + j * 4096, s);
+#pragma unroll
+      for (int i = 0; i < kTN; ++i) {
+        const gu32x4_t w0 = chunk(ws + i * 4096, 0), w1 = chunk(ws + i * 4096, 1);
+#pragma unroll
+        for (int j = 0; j < kTM; ++j)
+          acc[i][j] = mfma64<0>(w0, fx[j][0], acc[i][j], sw[i][h] >> (8 * fhalf), sx[j][h] >> (8 * fhalf));
+#pragma unroll
+        for (int j = 0; j < kTM; ++j)
+          acc[i][j] = mfma64<2>(w1, fx[j][1], acc[i][j], sw[i][h] >> (8 * fhalf), sx[j][h] >> (8 * fhalf));
+      }
+    };
+    run(0);
+    if (2 * kb + 1 < tile.runs) run(1);
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  static_assert(kWaves * kStageBytes<false, kTN> <= kMx4Lds<BM, BN, kStages>, "epilogue stage");
+  const int64_t row0 = tile.row0 + wm * (BM / kWM), col0 = tile.col0 + wn * (BN / kWN);
+  if (a.y_bf16)
+    store_tile<true, kTN, kTM>(acc, lds + wave * kStageBytes<true, kTN>, tile.y, row0, col0, tile.m, a.n, lane);
+  else
+    store_tile<false, kTN, kTM>(acc, lds + wave * kStageBytes<false, kTN>, tile.y + split * a.m * a.n * 4,
+                                row0, col0, tile.m, a.n, lane);
+}
+
+// One product, or two in one launch, the first with `first` workgroups: few tiles
+// leave CUs idle that the second's can have.
+template <int BM, int BN, int kWM, int kWN, int kStages>
+__global__ __launch_bounds__(kWM* kWN * 64) void mx4_tile_kernel(Mx4Args a, Mx4Args b, uint32_t first,
+                                                                 int per_split) {
+  __shared__ __attribute__((aligned(1024))) char lds[kMx4Lds<BM, BN, kStages>];
+  const bool second = blockIdx.x >= first;
+  mx4_tile<BM, BN, kWM, kWN, kStages>(second ? b : a, blockIdx.x - (second ? first : 0u), (int)blockIdx.y,
+                                      per_split, lds);
+}
+
+// Y = sum of `splits` float32 planes, in order; 4 elements a thread.
+template <bool kBf16>
+__global__ __launch_bounds__(256) void mx4_reduce_kernel(const float* __restrict__ parts, int splits,
+                                                         int64_t total, void* __restrict__ Y) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= total) return;
+  const bool vec = (total & 3) == 0;  // whole runs in every plane
+  float s[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s[e] = 0.0f;
+  for (int p = 0; p < splits; ++p) {
+    const float* src = parts + p * total + i;
+    if (vec) {
+      const gf32x4_t v = *reinterpret_cast<const gf32x4_t*>(src);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += src[min((int64_t)e, total - 1 - i)];
+    }
+  }
+  store4<kBf16>(Y, i, 0, (int)min((int64_t)4, total - i), vec, s[0], s[1], s[2], s[3]);
+}
+
+// Up to 16 rows (of a group): bound by reading W once. A workgroup owns `cols` <= 16
+// columns of Y; its waves take the stages (256 values along K) in turn, W straight
+// from memory into the MFMA's operand registers, and their sums meet in LDS in a fixed
+// order. Rows past the last or columns past the workgroup's repeat the last one and
+// are not stored.
+constexpr int kMx4SkinnyWaves = 8;
+__global__ __launch_bounds__(kMx4SkinnyWaves * 64) void mx4_skinny_kernel(Mx4Args a, int cols) {
+  __shared__ gf32x4_t part[kMx4SkinnyWaves][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, kq = lane >> 4;
+  int64_t row0 = 0, row1 = a.m, wbase = 0;
+  const uint32_t unit = blockIdx.x / a.tiles_n;
+  if (a.mode == kMx4Rows) {
+    int e;
+    uint32_t before;
+    if (!group_unit(a.groups, 4, unit, e, before)) return;
+    group_range(a.groups, e, row0, row1);
+    row0 += (int64_t)(unit - before) * 16;
+    row1 = min(row0 + 16, row1);
+    if (row0 >= row1) return;
+    wbase = e * a.n;
+  }
+  const int64_t n0 = (int64_t)(blockIdx.x - unit * a.tiles_n) * cols, n1 = min(n0 + cols, a.n);
+  const int64_t wr = wbase + min(n0 + r16, n1 - 1), xr = min(row0 + r16, row1 - 1);
+  const uint8_t *wp = a.w + wr * a.ldw + kq * 16, *xp = a.x + xr * a.ldx + kq * 16;
+  const uint32_t* wsp = reinterpret_cast<const uint32_t*>(a.ws + wr * (a.ldw / 16));
+  const uint32_t* xsp = reinterpret_cast<const uint32_t*>(a.xs + xr * (a.ldx / 16));
+  gf32x4_t acc = {0, 0, 0, 0};
+  // kU stages at a time, their loads all in flight before the first product (past the
+  // end the last run again, not used)
+  constexpr int kU = 4;
+  const int stages = (a.runs + 1) / 2;
+  for (int s0 = wave; s0 < stages; s0 += kU * kMx4SkinnyWaves) {
+    gu32x4_t w[kU][2], x[kU][2];
+    uint32_t sw[kU][2], sx[kU][2];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = min(2 * (s0 + u * kMx4SkinnyWaves) + h, a.runs - 1);
+        w[u][h] = *reinterpret_cast<const gu32x4_t*>(wp + (int64_t)r * 64);
+        x[u][h] = *reinterpret_cast<const gu32x4_t*>(xp + (int64_t)r * 64);
+        sw[u][h] = wsp[r];
+        sx[u][h] = xsp[r];
+      }
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (2 * (s0 + u * kMx4SkinnyWaves) + h < a.runs)  // uniform
+          acc = mfma128(w[u][h], x[u][h], acc, sw[u][h] >> (8 * kq), sx[u][h] >> (8 * kq));
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (wave == 0) {
+    gf32x4_t s = part[0][lane];
+#pragma unroll
+    for (int v = 1; v < kMx4SkinnyWaves; ++v) s += part[v][lane];
+    const bool vec = (a.n & 3) == 0 && (cols & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+    const int64_t col = n0 + kq * 4, row = row0 + r16;
+    if (row < row1 && col < n1) {
+      if (a.y_bf16) store4<true>(a.y, row * a.n + col, (int)col, (int)n1, vec, s[0], s[1], s[2], s[3]);
+      else store4<false>(a.y, row * a.n + col, (int)col, (int)n1, vec, s[0], s[1], s[2], s[3]);
+    }
+  }
+}
+
+enum Mx4Kind { kMx4Skinny, kMx4Small, kMx4OneRound, kMx4Middle };
+struct Mx4Plan {
+  Mx4Kind kind;
+  int splits, per_split;  // of K's stages
+};
+constexpr int64_t kMx4Cus = 256;
+static int64_t tiles_in(int64_t v, int64_t tile) { return (v + tile - 1) / tile; }
+
+// Which kernel, from the sizes alone.
+static Mx4Plan plan_mx4(int64_t m, int64_t n, int64_t k) {
+  const int64_t stages = tiles_in(k, 256);
+  const auto tiles = [&](int64_t t) { return tiles_in(m, t) * tiles_in(n, t); };
+  // (a grid has fewer than 2^32 threads: 512 for 16 columns, so 2^23 - 1 workgroups)
+  if (m <= 16 && n <= (int64_t(1) << 26)) return {kMx4Skinny, 1, (int)stages};
+  const int64_t t128 = tiles(128);
+  if (t128 > kMx4Cus) return {kMx4Middle, 1, (int)stages};
+  if (t128 >= kMx4Cus / 2) return {kMx4OneRound, 1, (int)stages};
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kMx4Cus / tiles(64), stages / 8));
+  const int64_t per = tiles_in(stages, splits);
+  return {kMx4Small, (int)tiles_in(stages, per), (int)per};
+}
+static Mx4Plan plan_of(const Mx4Product& p) {
+  const int all = (int)tiles_in(p.k, 256);
+  if (p.mode == kMx4Plain) return plan_mx4(p.m, p.n, p.k);
+  if (p.mode == kMx4Rows) {
+    const int64_t mean = tiles_in(p.groups.rows, p.groups.count);
+    if (mean <= 16 && most_units(p.groups.rows, p.groups.count, 4) * tiles_in(p.n, 16) < (1 << 23))
+      return {kMx4Skinny, 1, all};
+    return {mean <= 64 ? kMx4Small : kMx4Middle, 1, all};
+  }
+  return {p.groups.count * tiles_in(p.m, 128) * tiles_in(p.n, 128) >= kMx4Cus ? kMx4Middle : kMx4Small, 1, all};
+}
+
+static Mx4Args mx4_args(const Mx4Product& p, int64_t tile) {
+  const int shift = tile == 16 ? 4 : tile == 64 ? 6 : 7;
+  const int64_t tiles_m = p.mode == kMx4Rows ? most_units(p.groups.rows, p.groups.count, shift) : tiles_in(p.m, tile);
+  return Mx4Args{p.x, p.xs, p.w, p.ws, (uint32_t)p.ldx, (uint32_t)p.ldw, p.m, p.n, (int)(p.k / 128), p.y,
+                 p.y_bf16, p.mode, (uint32_t)tiles_m, (uint32_t)tiles_in(p.n, tile), p.groups};
+}
+static uint64_t mx4_tiles(const Mx4Args& a) {
+  return (uint64_t)a.tiles_m * a.tiles_n * (a.mode == kMx4Depth ? a.groups.count : 1);
+}
+
+// The tile kernels by kind: tile rows and columns, waves both ways, stages.
+#define HIF4_MX4_SMALL 64, 64, 2, 2, 4
+#define HIF4_MX4_ONE_ROUND 128, 128, 2, 4, 3
+#define HIF4_MX4_MIDDLE 128, 128, 2, 2, 2
+
+// `b` may be NULL. false: not launched (too many tiles).
+static bool launch_mx4_tiles(const Mx4Args& a, const Mx4Args* b, const Mx4Plan& plan, hipStream_t stream) {
+  const uint64_t first = mx4_tiles(a), all = first + (b ? mx4_tiles(*b) : 0);
+  if (all >= (1ull << 24)) return false;  // a grid has fewer than 2^32 threads
+  const dim3 grid((unsigned)all, plan.splits);
+#define HIF4_MX4(config, threads)                                                                 \
+  hipLaunchKernelGGL((mx4_tile_kernel<config>), grid, dim3(threads), 0, stream, a, b ? *b : a,    \
+                     (uint32_t)first, plan.per_split)
+  switch (plan.kind) {
+    case kMx4Middle: HIF4_MX4(HIF4_MX4_MIDDLE, 256); break;
+    case kMx4OneRound: HIF4_MX4(HIF4_MX4_ONE_ROUND, 512); break;
+    case kMx4Small: HIF4_MX4(HIF4_MX4_SMALL, 256); break;
+    case kMx4Skinny: return false;
+  }
+#undef HIF4_MX4
+  return true;
+}
+static int64_t mx4_tile_rows(Mx4Kind kind) { return kind == kMx4Small ? 64 : 128; }
+
+}  // namespace hif4
+
+using namespace hif4;
+
+hipError_t hif4_launch_gemm_mxfp4(const Mx4Product& p, void* workspace, hipStream_t stream) {
+  const Mx4Plan plan = plan_of(p);
+  if (plan.kind == kMx4Skinny) {
+    // columns: the least that leaves as many workgroups a CU as 16 would, so that
+    // every CU has the same share (with groups, whose number is known on the device
+    // only, 16)
+    const int64_t per_cu = tiles_in(p.n, 16 * kMx4Cus);
+    const int cols = p.mode == kMx4Rows ? 16 : (int)tiles_in(p.n, kMx4Cus * per_cu);  // 1 .. 16
+    Mx4Args a = mx4_args(p, 16);
+    a.tiles_n = (uint32_t)tiles_in(p.n, cols);
+    hipLaunchKernelGGL(mx4_skinny_kernel, dim3(a.tiles_m * a.tiles_n), dim3(kMx4SkinnyWaves * 64), 0,
+                       stream, a, cols);
+    return hipGetLastError();
+  }
+  Mx4Args a = mx4_args(p, mx4_tile_rows(plan.kind));
+  if (plan.splits == 1)
+    return launch_mx4_tiles(a, nullptr, plan, stream) ? hipGetLastError() : hipErrorInvalidValue;
+  a.y = workspace;
+  a.y_bf16 = false;
+  if (!launch_mx4_tiles(a, nullptr, plan, stream)) return hipErrorInvalidValue;
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)tiles_in(p.m * p.n, 1024));
+  if (p.y_bf16)
+    hipLaunchKernelGGL(mx4_reduce_kernel<true>, grid, dim3(256), 0, stream, (const float*)workspace,
+                       plan.splits, p.m * p.n, p.y);
+  else
+    hipLaunchKernelGGL(mx4_reduce_kernel<false>, grid, dim3(256), 0, stream, (const float*)workspace,
+                       plan.splits, p.m * p.n, p.y);
+  return hipGetLastError();
+}
+
+// Two independent products, in one launch where both take the same tile kernel whole.
+hipError_t hif4_launch_gemm_mxfp4_two(const Mx4Product& a, const Mx4Product& b, void* workspace,
+                                      hipStream_t stream) {
+  const Mx4Plan pa = plan_of(a), pb = plan_of(b);
+  if (pa.kind == pb.kind && pa.kind != kMx4Skinny && pa.splits == 1 && pb.splits == 1) {
+    const Mx4Args ga = mx4_args(a, mx4_tile_rows(pa.kind)), gb = mx4_args(b, mx4_tile_rows(pb.kind));
+    const int most = pa.per_split > pb.per_split ? pa.per_split : pb.per_split;
+    if (launch_mx4_tiles(ga, &gb, Mx4Plan{pa.kind, 1, most}, stream)) return hipGetLastError();
+  }
+  const hipError_t e = hif4_launch_gemm_mxfp4(a, workspace, stream);
+  return e != hipSuccess ? e : hif4_launch_gemm_mxfp4(b, workspace, stream);
+}
+
+size_t hif4_gemm_mxfp4_ws_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m == 0 || n == 0 || k == 0) return 0;
+  const Mx4Plan p = plan_mx4(m, n, k);
+  return p.splits == 1 ? 0 : (size_t)p.splits * (size_t)m * (size_t)n * sizeof(float);
+}

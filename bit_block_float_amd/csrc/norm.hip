@@ -1,5 +1,5 @@
 // norm.hip -- layer norm over the rows of a matrix: forward, forward that ends
-// in a quantizer (HiF4 or E4M3 blocks), and backward with the reduction of the
+// in a quantizer (HiF4, E4M3 or MXFP4 blocks), and backward with the reduction of the
 // weight's and bias' gradients. HBM-streaming kernels for gfx950.
 //
 // Forward: y = (x - mean) rstd w + b with rstd = (var + eps)^(-1/2). A row is
@@ -13,13 +13,19 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "fp8_dev.h"
+#include "mxfp4_dev.h"
 #include "norm_dev.h"
 #include "quant_dev.h"
 
 namespace hif4 {
 
-enum NormOut { kOutY = 0, kOutHif4 = 1, kOutFp8 = 2 };
+enum NormOut { kOutY = 0, kOutHif4 = 1, kOutFp8 = 2, kOutMx4 = 3 };
+
+// Items of 16 columns a row: E4M3 and MXFP4 rows have their padding's, too.
+template <int kOut>
+__device__ __host__ __forceinline__ int row_items(const NormArgs& a) {
+  return kOut == kOutFp8 || kOut == kOutMx4 ? a.kp / 16 : (a.c + 15) / 16;
+}
 
 // Sum over the lanes of a wave, the same bits in every lane: DPP moves inside
 // each row of 16 lanes, then the rows by permlane swaps (which leave the two
@@ -125,7 +131,7 @@ __device__ __forceinline__ void store_run8(float* p, int valid, const float (&v)
   }
 }
 
-// Item j (16 columns) of a row of results: as they are, to HiF4, or to E4M3.
+// Item j (16 columns) of a row of results: as they are, to HiF4, to E4M3 or to MXFP4.
 template <typename T, int kOut, int kRows>
 __device__ __forceinline__ void store_item(const NormArgs& a, float (&y)[2][8], int64_t row, int j,
                                            int c, uint32_t info) {
@@ -165,10 +171,19 @@ __device__ __forceinline__ void store_item(const NormArgs& a, float (&y)[2][8], 
       }
       if constexpr (kRows == kAligned) r[h].keep_if(col + 8 * h < c);
     }
-    const uint32_t e = e8m0_of(max8_u32(max(r[0].abs_max(), r[1].abs_max())));
-    const uint2 c0 = r[0].encode(e), c1 = r[1].encode(e);
-    *reinterpret_cast<uint4*>(a.codes + row * a.kp + col) = make_uint4(c0.x, c0.y, c1.x, c1.y);
-    if ((j & 7) == 0) a.scales[row * a.lds + (j >> 3)] = (uint8_t)e;
+    const uint32_t m = max(r[0].abs_max(), r[1].abs_max());
+    if constexpr (kOut == kOutFp8) {
+      const uint32_t e = e8m0_of(max8_u32(m));
+      const uint2 c0 = r[0].encode(e), c1 = r[1].encode(e);
+      *reinterpret_cast<uint4*>(a.codes + row * a.kp + col) = make_uint4(c0.x, c0.y, c1.x, c1.y);
+      if ((j & 7) == 0) a.scales[row * a.lds + (j >> 3)] = (uint8_t)e;
+    } else {  // two lanes a block, eight a word of four scales
+      const uint32_t e = mx4_scale_of(max(m, dpp<kDppQuadXor1>(m)));
+      *reinterpret_cast<uint2*>(a.codes + row * (a.kp / 2) + col / 2) =
+          make_uint2(mx4_encode(r[0], e), mx4_encode(r[1], e));
+      const uint32_t word = or8_u32(e << (8 * ((j >> 1) & 3)));
+      if ((j & 7) == 0) *reinterpret_cast<uint32_t*>(a.scales + row * (a.kp / 32) + (j >> 1)) = word;
+    }
   }
 }
 
@@ -214,7 +229,7 @@ __global__ __launch_bounds__(512) void layer_norm_wave_kernel(NormArgs a) {
   extern __shared__ float4 affine[];
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int c = a.c;
-  const int items = kOut == kOutFp8 ? a.kp / 16 : (c + 15) / 16;
+  const int items = row_items<kOut>(a);
   for (int j = threadIdx.x; j < items; j += blockDim.x) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -317,7 +332,7 @@ __global__ __launch_bounds__(1024) void layer_norm_wide_kernel(NormArgs a) {
   __shared__ float slots[2][P / 64];
   const int t = threadIdx.x;
   const int c = a.c;
-  const int items = kOut == kOutFp8 ? a.kp / 16 : (c + 15) / 16;
+  const int items = row_items<kOut>(a);
   const T* x = reinterpret_cast<const T*>(a.x);
 
   // protected channels (HiF4): the item's mask bits and the rank of its first
@@ -421,7 +436,7 @@ __global__ __launch_bounds__(1024) void layer_norm_rows_kernel(NormArgs a) {
   const int waves = kMulti ? (int)(blockDim.x >> 6) : 1;
   const int groups = kMulti ? 1 : (int)blockDim.x / kLanes, group = kMulti ? 0 : (int)threadIdx.x / kLanes;
   const int c = a.c, col = t * 16;
-  const int items = kOut == kOutFp8 ? a.kp / 16 : (c + 15) / 16;
+  const int items = row_items<kOut>(a);
   const bool live = t < items;
 
   uint32_t info = 0;
@@ -743,7 +758,7 @@ __global__ __launch_bounds__(1024) void layer_norm_parts_kernel(const float* __r
 // (weight and bias would leave 64 KB of LDS).
 template <typename T, int kOut, int kRows>
 static hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
-  const int items = kOut == kOutFp8 ? a.kp / 16 : (a.c + 15) / 16;
+  const int items = row_items<kOut>(a);
   const int waves = (items + 63) / 64;
 #define HIF4_NORM(rr, multi, grid, waves, lanes)                                             \
   hipLaunchKernelGGL((layer_norm_rows_kernel<T, rr, kOut, multi, kRows, lanes>), dim3(grid), \
@@ -871,7 +886,8 @@ hipError_t hif4_launch_layer_norm(const NormArgs& a, bool x_bf16, int out, hipSt
   switch (out) {
     case kOutY: return by_type(std::integral_constant<int, kOutY>{});
     case kOutHif4: return by_type(std::integral_constant<int, kOutHif4>{});
-    default: return by_type(std::integral_constant<int, kOutFp8>{});
+    case kOutFp8: return by_type(std::integral_constant<int, kOutFp8>{});
+    default: return by_type(std::integral_constant<int, kOutMx4>{});
   }
 }
 

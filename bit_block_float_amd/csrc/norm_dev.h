@@ -18,13 +18,13 @@ struct NormArgs {
   void* y;  // plain output, of x's type
   int64_t ldy;
   float *mean, *rstd;  // either may be NULL
-  uint8_t* codes;      // HiF4 [rows][c/2] or E4M3 [rows][kp]
+  uint8_t* codes;      // HiF4 [rows][c/2], E4M3 [rows][kp] or MXFP4 [rows][kp/2]
   uint32_t* meta;      // HiF4
   const uint8_t* mask;
   uint16_t* kept;
   int n_mask;
-  int kp;           // E4M3: c rounded up to 128
-  uint8_t* scales;  // E4M3 [rows][lds]
+  int kp;           // E4M3, MXFP4: c rounded up to 128
+  uint8_t* scales;  // E4M3 [rows][lds], MXFP4 [rows][kp/32]
   int64_t lds;
 };
 

@@ -87,12 +87,37 @@ def lib():
         L.hif4_linear_fp8_backward.argtypes = [p, i, i64, p, p, i64, p, p, i64, i, i64, i64, i64, i64,
                                                p, i, p, i, p, sz, p]
         L.hif4_linear_fp8_backward.restype = i
+        L.hif4_mxfp4_columns.argtypes = [i64, i64]
+        L.hif4_mxfp4_columns.restype = i64
+        L.hif4_quantize_mxfp4.argtypes = [p, i, i64, i64, i64, i64, i, p, i64, p, p, p]
+        L.hif4_quantize_mxfp4.restype = i
+        L.hif4_quantize_mxfp4_both.argtypes = [p, i, i64, i64, i64, i64, p, i64, p, p, p, p, p]
+        L.hif4_quantize_mxfp4_both.restype = i
+        L.hif4_dequantize_mxfp4.argtypes = [p, p, i64, i64, p, i, p]
+        L.hif4_dequantize_mxfp4.restype = i
+        L.hif4_linear_mxfp4_workspace_bytes.argtypes = [i64, i64, i64]
+        L.hif4_linear_mxfp4_workspace_bytes.restype = sz
+        L.hif4_linear_mxfp4.argtypes = [p, p, p, p, i64, i64, i64, p, i, p, sz, p]
+        L.hif4_linear_mxfp4.restype = i
+        L.hif4_linear_mxfp4_grouped.argtypes = [p, p, p, p, p, i64, i64, i64, i64, p, i, p]
+        L.hif4_linear_mxfp4_grouped.restype = i
+        L.hif4_linear_mxfp4_backward_workspace_bytes.argtypes = [i64, i64, i64]
+        L.hif4_linear_mxfp4_backward_workspace_bytes.restype = sz
+        L.hif4_linear_mxfp4_backward.argtypes = [p, i, i64, p, p, p, p, i64, i64, i64, p, i, p, i, p, sz, p]
+        L.hif4_linear_mxfp4_backward.restype = i
+        L.hif4_linear_mxfp4_grouped_backward_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        L.hif4_linear_mxfp4_grouped_backward_workspace_bytes.restype = sz
+        L.hif4_linear_mxfp4_grouped_backward.argtypes = [p, i, i64, p, p, p, p, p, i64, i64, i64, i64, p, i, p,
+                                                         i, p, sz, p]
+        L.hif4_linear_mxfp4_grouped_backward.restype = i
         L.hif4_layer_norm.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, i64, p, p, p]
         L.hif4_layer_norm.restype = i
         L.hif4_layer_norm_quantize.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, i64, p, p, p, p]
         L.hif4_layer_norm_quantize.restype = i
         L.hif4_layer_norm_quantize_fp8.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, p, i64, p]
         L.hif4_layer_norm_quantize_fp8.restype = i
+        L.hif4_layer_norm_quantize_mxfp4.argtypes = [p, i, i64, i64, i64, p, p, i, d, p, p, p]
+        L.hif4_layer_norm_quantize_mxfp4.restype = i
         L.hif4_layer_norm_backward_workspace_bytes.argtypes = [i64, i64]
         L.hif4_layer_norm_backward_workspace_bytes.restype = sz
         L.hif4_layer_norm_backward.argtypes = [p, i64, p, i64, i, i64, i64, p, p, p, i, p, i64, p, p,
@@ -680,6 +705,250 @@ def linear_fp8_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype=N
     return dx, dw
 
 
+# ---------------------------------------------------------------- 4-bit microscaled linear layers
+#
+# A matrix [rows][k] is codes uint8 [rows][kp/2] and scales torch.float8_e8m0fnu
+# [rows][kp/32], kp = k up to 128s, both contiguous; experts' weights have one more
+# dimension in front. Groups of rows are an int64 tensor of offsets on the GPU: group e
+# is rows offsets[e] .. offsets[e + 1] - 1.
+
+MXFP4_BLOCK = 32
+
+
+def mxfp4_columns(rows, groups=0):
+    """Columns of a transpose quantized along its source's rows (in `groups` groups)."""
+    return int(lib().hif4_mxfp4_columns(rows, groups))
+
+
+def _check_offsets(offsets):
+    """Number of groups of an offsets tensor."""
+    if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int64 tensor [groups + 1]")
+    return offsets.numel() - 1
+
+
+def _mx4_out(lead, rows, length, codes, scales, dev):
+    """Codes [*lead, rows, length up to 128s / 2] and their scales, given or new."""
+    kp = _up128(length)
+    if codes is None:
+        codes = torch.empty((*lead, rows, kp // 2), dtype=torch.uint8, device=dev)
+    else:
+        _check_out(codes, "codes", (*lead, rows, kp // 2), torch.uint8)
+    if scales is None:
+        scales = torch.empty((*lead, rows, kp // MXFP4_BLOCK), dtype=torch.float8_e8m0fnu, device=dev)
+    else:
+        _check_out(scales, "scales", (*lead, rows, kp // MXFP4_BLOCK), torch.float8_e8m0fnu)
+    return codes, scales
+
+
+def _mx4_x(x, offsets, transposed):
+    """(batch, rows, k, ld, leading dimensions, groups) of what is quantized."""
+    if x.dim() == 3:
+        if x.dtype not in _DTYPE or not x.is_contiguous():
+            raise ValueError("x must be a contiguous fp32 or bf16 tensor where it has three dimensions")
+        batch, rows, k = x.shape
+        ld, lead = k, (batch,)
+    else:
+        _check_rows(x, "x")
+        (rows, k), batch, ld, lead = x.shape, 1, _ld(x), ()
+    if offsets is None:
+        return batch, rows, k, ld, lead, 0
+    groups = _check_offsets(offsets)
+    if not transposed or lead or groups == 0:
+        raise ValueError("offsets (of one group at least) go with a 2-D x quantized along its rows")
+    return batch, rows, k, ld, lead, groups
+
+
+def quantize_mxfp4(x, transposed=False, offsets=None, codes=None, scales=None, stream=None):
+    """MXFP4-quantize x [rows][k] (bf16 or fp32; or [experts][rows][k]) in blocks of 32
+    along k, or with transposed=True x^T in blocks along the rows of x, with `offsets`
+    each group's rows by themselves. Returns (codes [rows][k up to 128s / 2], scales
+    [rows][k up to 128s / 32]), or those of x^T, whose columns are
+    mxfp4_columns(rows, groups)."""
+    batch, rows, k, ld, lead, groups = _mx4_x(x, offsets, transposed)
+    with _On(x, stream, offsets, codes, scales) as st:
+        out = (k, mxfp4_columns(rows, groups)) if transposed else (rows, k)
+        codes, scales = _mx4_out(lead, *out, codes, scales, x.device)
+        _ok(lib().hif4_quantize_mxfp4(_at(x), _DTYPE[x.dtype], batch, rows, k, ld, int(bool(transposed)),
+                                      _at(offsets), groups, _at(codes), _at(scales), st),
+            "hif4_quantize_mxfp4")
+    return codes, scales
+
+
+def quantize_mxfp4_both(x, offsets=None, stream=None):
+    """quantize_mxfp4 of x and of x^T (in groups of its rows) from one read: (codes,
+    scales, codes_t, scales_t). Codes and scales of rows outside every group are not
+    written."""
+    batch, rows, k, ld, lead, groups = _mx4_x(x, offsets, True)
+    with _On(x, stream, offsets) as st:
+        codes, scales = _mx4_out(lead, rows, k, None, None, x.device)
+        codes_t, scales_t = _mx4_out(lead, k, mxfp4_columns(rows, groups), None, None, x.device)
+        _ok(lib().hif4_quantize_mxfp4_both(_at(x), _DTYPE[x.dtype], batch, rows, k, ld, _at(offsets), groups,
+                                           _at(codes), _at(scales), _at(codes_t), _at(scales_t), st),
+            "hif4_quantize_mxfp4_both")
+    return codes, scales, codes_t, scales_t
+
+
+def _check_mx4(codes, scales, name, dims=2):
+    """Codes [..., rows, kp/2] with scales [..., rows, kp/32]: their leading sizes and kp."""
+    if (codes.dtype != torch.uint8 or codes.dim() != dims or not codes.is_contiguous()
+            or codes.shape[-1] % (FP8_BLOCK // 2)):
+        raise ValueError(f"{name}_codes must be a contiguous {dims}-D uint8 tensor, its rows a multiple of 64 "
+                         "bytes (128 codes) long")
+    kp = codes.shape[-1] * 2
+    want = (*codes.shape[:-1], kp // MXFP4_BLOCK)
+    if scales.dtype != torch.float8_e8m0fnu or tuple(scales.shape) != want or not scales.is_contiguous():
+        raise ValueError(f"{name}_scales must be a contiguous float8_e8m0fnu tensor of shape {want}")
+    return *codes.shape[:-1], kp
+
+
+def dequantize_mxfp4(codes, scales, k=None, out_dtype=torch.float32, out=None, stream=None):
+    """Values [rows][k] (fp32 or bf16; [experts][rows][k] of such codes) of codes and
+    scales; k: the columns before the padding."""
+    *lead, kp = _check_mx4(codes, scales, "the", codes.dim() if codes.dim() in (2, 3) else 2)
+    k = kp if k is None else int(k)
+    if _up128(k) != kp or k < 0:
+        raise ValueError(f"k = {k} does not fit codes of {kp} columns")
+    if out_dtype not in _DTYPE:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    with _On(codes, stream, scales, out) as st:
+        if out is None:
+            out = torch.empty((*lead, k), dtype=out_dtype, device=codes.device)
+        else:
+            _check_out(out, "out", (*lead, k), out_dtype)
+        rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+        _ok(lib().hif4_dequantize_mxfp4(_at(codes), _at(scales), rows, k, _at(out), _DTYPE[out_dtype], st),
+            "hif4_dequantize_mxfp4")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
+def linear_mxfp4_workspace_bytes(m, n, k):
+    return int(lib().hif4_linear_mxfp4_workspace_bytes(m, n, k))
+
+
+def _y_out(y, m, n, y_dtype, dev):
+    if y_dtype not in _DTYPE:
+        raise ValueError("y_dtype must be float32 or bfloat16")
+    if y is None:
+        return torch.empty((m, n), dtype=y_dtype, device=dev)
+    _check_out(y, "y", (m, n), y_dtype)
+    return y
+
+
+def linear_mxfp4(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=None, workspace=None,
+                 stream=None):
+    """Y [m][n] = X W^T of MXFP4 X [m][k] and W [n][k]: exact products, fp32 sums,
+    rounded once."""
+    m, k = _check_mx4(x_codes, x_scales, "x")
+    n, kw = _check_mx4(w_codes, w_scales, "w")
+    if kw != k:
+        raise ValueError(f"x has {k} columns, w {kw}")
+    with _On(x_codes, stream, x_scales, w_codes, w_scales, y, workspace) as st:
+        y = _y_out(y, m, n, y_dtype, x_codes.device)
+        need = linear_mxfp4_workspace_bytes(m, n, k)
+        if workspace is None and need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=x_codes.device)
+        nbytes = _workspace_bytes(workspace) if workspace is not None else 0
+        _ok(lib().hif4_linear_mxfp4(_at(x_codes), _at(x_scales), _at(w_codes), _at(w_scales), m, n, k,
+                                    _at(y), _DTYPE[y_dtype], _at(workspace), nbytes, st),
+            "hif4_linear_mxfp4")
+    return y
+
+
+def linear_mxfp4_grouped(x_codes, x_scales, w_codes, w_scales, offsets, y_dtype=torch.float32, y=None,
+                         stream=None):
+    """Y [m][n]: Y[i] = X[i] W[e]^T for the rows i of each group e (rows offsets[e] ..
+    offsets[e + 1] - 1), MXFP4 X [m][k] and W [experts][n][k]. Rows outside every group
+    are not written."""
+    m, k = _check_mx4(x_codes, x_scales, "x")
+    experts, n, kw = _check_mx4(w_codes, w_scales, "w", 3)
+    groups = _check_offsets(offsets)
+    if kw != k or experts != groups:
+        raise ValueError(f"x has {k} columns and offsets {groups} groups, w {kw} columns and {experts} experts")
+    with _On(x_codes, stream, x_scales, w_codes, w_scales, offsets, y) as st:
+        y = _y_out(y, m, n, y_dtype, x_codes.device)
+        _ok(lib().hif4_linear_mxfp4_grouped(_at(x_codes), _at(x_scales), _at(w_codes), _at(w_scales),
+                                            _at(offsets), groups, m, n, k, _at(y), _DTYPE[y_dtype], st),
+            "hif4_linear_mxfp4_grouped")
+    return y
+
+
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
+def linear_mxfp4_backward_workspace_bytes(m, n, k):
+    return int(lib().hif4_linear_mxfp4_backward_workspace_bytes(m, n, k))
+
+
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
+def linear_mxfp4_grouped_backward_workspace_bytes(groups, m, n, k):
+    return int(lib().hif4_linear_mxfp4_grouped_backward_workspace_bytes(groups, m, n, k))
+
+
+def _mx4_gradient_types(dy, dx_dtype, dw_dtype):
+    dx_dtype = dy.dtype if dx_dtype is None else dx_dtype
+    if dx_dtype not in _DTYPE or dw_dtype not in _DTYPE:
+        raise ValueError("dx_dtype and dw_dtype must be float32 or bfloat16")
+    return dx_dtype
+
+
+def linear_mxfp4_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype=None,
+                          dw_dtype=torch.float32, workspace=None, stream=None):
+    """Gradients of Y = X W^T through the quantizers (taken as the identity): dX [m][k] =
+    Q(dY) W and dW [n][k] = Q(dY^T) X for dy [m][n] (bf16 or fp32), with X^T and W^T
+    quantized along m and n (quantize_mxfp4(..., transposed=True)). dX is of dy's type
+    unless dx_dtype says otherwise."""
+    _check_rows(dy, "dy")
+    (m, n), (k, mp) = dy.shape, _check_mx4(xt_codes, xt_scales, "xt")
+    kw, np_ = _check_mx4(wt_codes, wt_scales, "wt")
+    if kw != k or mp != _up128(m) or np_ != _up128(n):
+        raise ValueError(f"dy is {m} x {n}: xt must be [k][{_up128(m)}], wt [k][{_up128(n)}]")
+    dx_dtype = _mx4_gradient_types(dy, dx_dtype, dw_dtype)
+    with _On(dy, stream, xt_codes, xt_scales, wt_codes, wt_scales, workspace) as st:
+        dx = torch.empty((m, k), dtype=dx_dtype, device=dy.device)
+        dw = torch.empty((n, k), dtype=dw_dtype, device=dy.device)
+        if workspace is None:
+            workspace = torch.empty((linear_mxfp4_backward_workspace_bytes(m, n, k),), dtype=torch.uint8,
+                                    device=dy.device)
+        _ok(lib().hif4_linear_mxfp4_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt_codes),
+                                             _at(xt_scales), _at(wt_codes), _at(wt_scales), m, n, k,
+                                             _at(dx), _DTYPE[dx_dtype], _at(dw), _DTYPE[dw_dtype],
+                                             _at(workspace), _workspace_bytes(workspace), st),
+            "hif4_linear_mxfp4_backward")
+    return dx, dw
+
+
+def linear_mxfp4_grouped_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, offsets, dx_dtype=None,
+                                  dw_dtype=torch.float32, workspace=None, stream=None):
+    """Gradients of linear_mxfp4_grouped: dX [m][k], dX[i] = Q(dY)[i] W[e] for the rows i
+    of each group e, and dW [experts][n][k], dW[e] = Q(dY_e^T) X_e (0 for a group without
+    rows), for dy [m][n], with X^T quantized along each group's rows
+    (quantize_mxfp4(x, transposed=True, offsets=offsets)) and the experts' W^T along n
+    (quantize_mxfp4(w, transposed=True)). Rows of dX outside every group are not
+    written."""
+    _check_rows(dy, "dy")
+    (m, n), (k, mp) = dy.shape, _check_mx4(xt_codes, xt_scales, "xt")
+    experts, kw, np_ = _check_mx4(wt_codes, wt_scales, "wt", 3)
+    groups = _check_offsets(offsets)
+    want = mxfp4_columns(m, groups) if groups else 0
+    if kw != k or experts != groups or mp != want or np_ != _up128(n):
+        raise ValueError(f"dy is {m} x {n} in {groups} groups: xt must be [k][{want}], wt [{groups}][k]"
+                         f"[{_up128(n)}]")
+    dx_dtype = _mx4_gradient_types(dy, dx_dtype, dw_dtype)
+    with _On(dy, stream, xt_codes, xt_scales, wt_codes, wt_scales, offsets, workspace) as st:
+        dx = torch.empty((m, k), dtype=dx_dtype, device=dy.device)
+        dw = torch.empty((groups, n, k), dtype=dw_dtype, device=dy.device)
+        if workspace is None:
+            need = linear_mxfp4_grouped_backward_workspace_bytes(groups, m, n, k)
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dy.device)
+        _ok(lib().hif4_linear_mxfp4_grouped_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt_codes),
+                                                     _at(xt_scales), _at(wt_codes), _at(wt_scales),
+                                                     _at(offsets), groups, m, n, k, _at(dx),
+                                                     _DTYPE[dx_dtype], _at(dw), _DTYPE[dw_dtype],
+                                                     _at(workspace), _workspace_bytes(workspace), st),
+            "hif4_linear_mxfp4_grouped_backward")
+    return dx, dw
+
+
 # ---------------------------------------------------------------- layer norm
 
 
@@ -757,6 +1026,20 @@ def layer_norm_quantize_fp8(x, weight=None, bias=None, eps=1e-6, codes=None, sca
                                                _at(weight), _at(bias), wd, float(eps),
                                                _at(codes), _at(scales), _scale_ld(scales), st),
             "hif4_layer_norm_quantize_fp8")
+    return codes, scales
+
+
+def layer_norm_quantize_mxfp4(x, weight=None, bias=None, eps=1e-6, codes=None, scales=None, stream=None):
+    """layer_norm and quantize_mxfp4 in one pass: (codes, scales), what linear_mxfp4 takes
+    as x_codes and x_scales."""
+    _check_rows(x, "x")
+    rows, c = x.shape
+    wd = _check_affine(weight, bias, c)
+    with _On(x, stream, weight, bias, codes, scales) as st:
+        codes, scales = _mx4_out((), rows, c, codes, scales, x.device)
+        _ok(lib().hif4_layer_norm_quantize_mxfp4(_at(x), _DTYPE[x.dtype], rows, c, _ld(x), _at(weight),
+                                                 _at(bias), wd, float(eps), _at(codes), _at(scales), st),
+            "hif4_layer_norm_quantize_mxfp4")
     return codes, scales
 
 

@@ -532,6 +532,146 @@ HIF4_EXPORT hif4_status hif4_linear_fp8_backward(const void *dy, int dy_dtype, i
                               void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * 4-bit microscaled (MXFP4) linear layers: E2M1 codes with a scale per block of 32,
+ * the 4-bit format that gfx950 multiplies as it is; with one weight, or one for each
+ * group of rows (experts).
+ *
+ * FORMAT (OCP Microscaling Formats 1.0, MXFP4)
+ *  - A code is 4 bits: sign, 2 exponent bits, 1 fraction bit: 0, 0.5, 1, 1.5, 2, 3,
+ *    4, 6. Element 2i of a row is the low half of byte i, element 2i + 1 the high one.
+ *  - A block is 32 consecutive elements of a row. Its scale is an E8M0 byte b for
+ *    2^(b - 127). The quantizer takes the smallest power of two s >= 2^-127 with
+ *    max|x| <= 6 s, so nothing is clipped; codes are round-to-nearest-even(x / s),
+ *    a zero keeps its sign. A block that holds a NaN or an infinity gets scale byte
+ *    255 (E8M0's NaN) and decodes to NaN throughout. Codes and scales made by another
+ *    rule are decoded and multiplied as the format says.
+ *  - Rows are padded to a multiple of 128 elements with zero codes (the padding's
+ *    scale is the one its block has, byte 0 for a block of padding alone). A matrix
+ *    [rows][k] has codes u8 [rows][kp/2] and scales u8 [rows][kp/32], kp = k up to
+ *    128s, both contiguous; codes 16-byte, scales 4-byte aligned.
+ *
+ * GROUPS
+ *  - offsets int64 [groups + 1], on the device: group e is rows offsets[e] ..
+ *    offsets[e + 1] - 1, which may be none; 0 <= groups <= 65536. Offsets have to
+ *    ascend and to lie within the rows (where they do not, results are unspecified;
+ *    nothing outside the arguments is read or written).
+ *  - Along the rows (a transpose's k) each group is a run of whole 128s: group e's
+ *    columns begin behind those of the groups before it, its last 128 is padded with
+ *    zeros, and behind the last group's columns there are zeros up to
+ *    hif4_mxfp4_columns(rows, groups), what any groups of as many rows can take.
+ */
+
+/* Columns of a transpose quantized along its source's rows: rows up to 128s (groups 0),
+ * or 128 floor((rows + 127 groups) / 128). 0 for sizes that the calls refuse. */
+HIF4_EXPORT int64_t hif4_mxfp4_columns(int64_t rows, int64_t groups);
+
+/*
+ * hif4_quantize_mxfp4 -- quantize x along k, or (transposed) x^T along the rows of x,
+ * all of them or (offsets given) each group's by themselves.
+ *
+ *  x      `batch` matrices [rows][ld] of x_dtype (HIF4_F32 or HIF4_BF16), one after the
+ *         other (the experts' weights), ld >= k, aligned to its element; batch * rows <
+ *         2^31, k <= 2^22.
+ *  transposed 0 or 1.
+ *  offsets, groups: NULL and 0, or groups of x's rows, with transposed = 1 and
+ *         batch = 1 (HIF4_ERR_ARG otherwise).
+ *  codes, scales  of [batch][rows][k], or transposed of [batch][k][rows]; with groups
+ *         of [k][hif4_mxfp4_columns(rows, groups)].
+ */
+HIF4_EXPORT hif4_status hif4_quantize_mxfp4(const void *x, int x_dtype, int64_t batch, int64_t rows,
+                              int64_t k, int64_t ld, int transposed, const int64_t *offsets,
+                              int64_t groups, uint8_t *codes, uint8_t *scales, hipStream_t stream);
+
+/*
+ * hif4_quantize_mxfp4_both -- both of the above from one read of x. With groups, rows
+ * outside every group leave codes and scales as they were.
+ */
+HIF4_EXPORT hif4_status hif4_quantize_mxfp4_both(const void *x, int x_dtype, int64_t batch, int64_t rows,
+                              int64_t k, int64_t ld, const int64_t *offsets, int64_t groups,
+                              uint8_t *codes, uint8_t *scales, uint8_t *codes_t, uint8_t *scales_t,
+                              hipStream_t stream);
+
+/* hif4_dequantize_mxfp4 -- codes and scales of [rows][k] to values of out_dtype, contiguous,
+ * element-aligned: exact in either type (beyond its range infinite). */
+HIF4_EXPORT hif4_status hif4_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t rows,
+                              int64_t k, void *out, int out_dtype, hipStream_t stream);
+
+/* Workspace of hif4_linear_mxfp4; 0 for sizes it refuses, and where it needs none
+ * (then workspace may be NULL). */
+HIF4_EXPORT size_t hif4_linear_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
+ * hif4_linear_mxfp4 -- Y = X W^T, X [m][k], W [n][k] as codes and scales; the products
+ * are exact, accumulated in fp32 in a fixed order, and rounded once to y_dtype. Every
+ * scale byte counts as it is (255: NaN); a sum beyond fp32's range is infinite.
+ *  m, n   >= 0, below 2^31, ceil(m/128) ceil(n/128) < 2^24.
+ *  k      >= 0, k % 128 == 0, at most 2^22; k = 0 gives Y = 0.
+ *  y      [m][n] contiguous of y_dtype, 16-byte aligned.
+ *  workspace >= hif4_linear_mxfp4_workspace_bytes(m, n, k), 256-byte aligned.
+ */
+HIF4_EXPORT hif4_status hif4_linear_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales,
+                              const uint8_t *w_codes, const uint8_t *w_scales, int64_t m, int64_t n,
+                              int64_t k, void *y, int y_dtype, void *workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+
+/*
+ * hif4_linear_mxfp4_grouped -- Y[i] = X[i] W_e^T for the rows i of each group e, with W
+ * [groups][n][k]. Rows outside every group are left as they were. Types, precision
+ * and limits as for hif4_linear_mxfp4, with groups * n < 2^31 and
+ * floor((m + 63 groups) / 64) ceil(n/64) < 2^24. Needs no workspace.
+ */
+HIF4_EXPORT hif4_status hif4_linear_mxfp4_grouped(const uint8_t *x_codes, const uint8_t *x_scales,
+                              const uint8_t *w_codes, const uint8_t *w_scales, const int64_t *offsets,
+                              int64_t groups, int64_t m, int64_t n, int64_t k, void *y, int y_dtype,
+                              hipStream_t stream);
+
+/* Workspace of hif4_linear_mxfp4_backward; 0 for sizes it refuses. */
+HIF4_EXPORT size_t hif4_linear_mxfp4_backward_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
+/*
+ * hif4_linear_mxfp4_backward -- the two gradients of Y = X W^T through the quantizers
+ * (taken as the identity): dX [m][k] = Q(dY) W, dY quantized along n, and dW [n][k] =
+ * Q(dY^T) X, dY quantized along m. dY is read once for both quantizations.
+ *  dy     [m][lddy] of dy_dtype, element-aligned, lddy >= n.
+ *  wt_*   W^T [k][n] (quantized with transposed = 1), xt_* X^T [k][m] alike.
+ *  dx     [m][k] of dx_dtype or NULL (wt_* unused); dw [n][k] of dw_dtype or NULL
+ *         (xt_* unused); contiguous, 16-byte aligned. m and n at most 2^22, and
+ *         hif4_linear_mxfp4's limits for both products; m = 0 gives dW = 0, n = 0
+ *         dX = 0.
+ *  workspace >= hif4_linear_mxfp4_backward_workspace_bytes(m, n, k), 256-byte aligned.
+ */
+HIF4_EXPORT hif4_status hif4_linear_mxfp4_backward(const void *dy, int dy_dtype, int64_t lddy,
+                              const uint8_t *xt_codes, const uint8_t *xt_scales,
+                              const uint8_t *wt_codes, const uint8_t *wt_scales, int64_t m, int64_t n,
+                              int64_t k, void *dx, int dx_dtype, void *dw, int dw_dtype,
+                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace of hif4_linear_mxfp4_grouped_backward; 0 for sizes it refuses. */
+HIF4_EXPORT size_t hif4_linear_mxfp4_grouped_backward_workspace_bytes(int64_t groups, int64_t m,
+                              int64_t n, int64_t k);
+
+/*
+ * hif4_linear_mxfp4_grouped_backward -- the gradients of hif4_linear_mxfp4_grouped: dX[i] =
+ * Q(dY)[i] W_e for the rows i of each group e (rows outside every group are left as
+ * they were) and dW_e [n][k] = Q(dY_e^T) X_e, dY and X quantized along the rows of
+ * each group by themselves; 0 for a group without rows.
+ *  wt_*   [groups][k][n] (the weights quantized with transposed = 1 and batch =
+ *         groups); xt_* [k][hif4_mxfp4_columns(m, groups)] (X quantized with
+ *         transposed = 1 and the offsets).
+ *  dx     [m][k], dw [groups][n][k], either may be NULL, as above. n and
+ *         hif4_mxfp4_columns(m, groups) at most 2^22, and the products' limits;
+ *         groups ceil(n/128) ceil(k/128) < 2^24.
+ *  workspace >= hif4_linear_mxfp4_grouped_backward_workspace_bytes(groups, m, n, k),
+ *         256-byte aligned.
+ */
+HIF4_EXPORT hif4_status hif4_linear_mxfp4_grouped_backward(const void *dy, int dy_dtype, int64_t lddy,
+                              const uint8_t *xt_codes, const uint8_t *xt_scales,
+                              const uint8_t *wt_codes, const uint8_t *wt_scales,
+                              const int64_t *offsets, int64_t groups, int64_t m, int64_t n, int64_t k,
+                              void *dx, int dx_dtype, void *dw, int dw_dtype, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * Layer norm, the producer of a linear layer's input.
  *
  *  x      [rows][ld] of x_dtype (HIF4_F32 or HIF4_BF16), aligned to its
@@ -568,6 +708,14 @@ HIF4_EXPORT hif4_status hif4_layer_norm_quantize_fp8(const void *x, int x_dtype,
                               int64_t c, int64_t ld, const void *weight, const void *bias,
                               int w_dtype, double eps, uint8_t *codes, uint8_t *scales,
                               int64_t lds, hipStream_t stream);
+
+/* hif4_layer_norm_quantize_mxfp4 -- the norm and hif4_quantize_mxfp4 along the rows in
+ * one pass: codes [rows][c up to 128s / 2] and scales [rows][c up to 128s / 32] of y
+ * rounded to x's type. */
+HIF4_EXPORT hif4_status hif4_layer_norm_quantize_mxfp4(const void *x, int x_dtype, int64_t rows,
+                              int64_t c, int64_t ld, const void *weight, const void *bias,
+                              int w_dtype, double eps, uint8_t *codes, uint8_t *scales,
+                              hipStream_t stream);
 
 /* Workspace of hif4_layer_norm_backward (0 for sizes it refuses). */
 HIF4_EXPORT size_t hif4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t c);
