@@ -275,6 +275,171 @@ __global__ __launch_bounds__(kWM* kWN * 64) void mx4_tile_kernel(Mx4Args a, Mx4A
                                       per_split, lds);
 }
 
+// Large products. 256 x 256 of Y a workgroup, 4 waves of 128 x 128 (256 fp32
+// accumulators a lane), one workgroup a CU.
+//
+// A stage is 256 values along K: rows of 128 bytes, whole cache lines, chunk c of 16
+// bytes in slot c ^ ((row >> 1) & 7) as above. Two stages are in LDS, each multiplied a
+// run (128 values) at a time: while run 0 of stage kb multiplies from registers, run 1
+// is read into the other register set; then one barrier, after which no wave needs the
+// stage, and stage kb + 2 goes out into it by direct-to-LDS loads while run 1 multiplies
+// and run 0 of stage kb + 1 is read. Stages past the end load the last one again, into
+// one that no one reads. Where the last stage has one run only, the other's codes are
+// loaded as zeros (from beyond the buffers) and its scales taken as 1: an exit between
+// the runs, or a copy of run 0 behind the loop, made the compiler spill. Scales come 16 bytes a row (two stages) at a time, into a ring
+// of two: X's for stages 2g and 2g + 1 in stage 2g - 3, W's in stage 2g - 2 (one load a
+// stage, whose target is chosen without a branch).
+constexpr int kMx4BigSlot = 2 * 256 * 128;
+constexpr int kMx4BigRing = 2 * 256 * 16;
+constexpr int kMx4BigLds = 2 * kMx4BigSlot + 2 * kMx4BigRing;
+
+__device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* const lds) {
+  Mx4Tile tile;
+  if (!mx4_locate<256, 256>(a, t, tile)) return;
+  const Mx4Buffers buf(tile, a.ldx, a.ldw);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int stages = (tile.runs + 1) / 2;
+
+  // Loads: instruction i of a wave brings rows 64 wave + 8 (i & 7) .. + 7 of X (i < 8) or
+  // W. The swizzle is the same for every other i; 8 i rows go into the scalar offset.
+  uint32_t xoff[2], woff[2];
+  bool second[2];  // the lane's chunk is of the stage's second run
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t c = (uint32_t)((lane & 7) ^ ((4 * i + (lane >> 4)) & 7));
+    xoff[i] = (uint32_t)(wave * 64 + (lane >> 3)) * a.ldx + c * 16;
+    woff[i] = (uint32_t)(wave * 64 + (lane >> 3)) * a.ldw + c * 16;
+    second[i] = c >= 4;
+  }
+  auto load_part = [&](int kb, int i) {
+    char* dst = lds + (kb & 1) * kMx4BigSlot + (i >> 3) * 32768 + wave * 8192 + (i & 7) * 1024;
+    const int off = min(kb, stages - 1) * 128;
+    const bool half = (tile.runs & 1) && kb >= stages - 1;
+    const uint32_t at = half && second[i & 1] ? 0x7FFFFFFFu : (i < 8 ? xoff : woff)[i & 1];
+    if (i < 8) load_lds16(buf.x, dst, at, off + (i & 7) * 8 * (int)a.ldx);
+    else load_lds16(buf.w, dst, at, off + (i & 7) * 8 * (int)a.ldw);
+  };
+  const uint32_t xs_off = (uint32_t)(wave * 64 + lane) * (a.ldx / 16);
+  const uint32_t ws_off = (uint32_t)(wave * 64 + lane) * (a.ldw / 16);
+  char* const ring = lds + 2 * kMx4BigSlot;
+  auto load_scale = [&](int kb) {  // kb >= -3
+    const bool is_w = (kb & 1) == 0;
+    const int g = (kb + 3) >> 1, at = min(g, (stages - 1) >> 1) * 16;
+    load_lds16(is_w ? buf.ws : buf.xs, ring + (g & 1) * kMx4BigRing + (is_w ? 4096 : 0) + wave * 1024,
+               is_w ? ws_off : xs_off, at);
+  };
+
+  const int frow = lane & 31, fhalf = lane >> 5, fsw = (frow >> 1) & 7;
+  const char* const xbase = lds + (wm * 128 + frow) * 128;
+  const char* const wbase = lds + 32768 + (wn * 128 + frow) * 128;
+  // fragments of a run: blocks of 32 rows 0..3 of X, 4..7 of W, two chunks each
+  struct Frags {
+    gu32x4_t v[8][2];
+  };
+  int slot[2][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) slot[h][e] = ((4 * h + 2 * e + fhalf) ^ fsw) * 16;
+  auto read_part = [&](Frags& f, int kb, int h, int p) {  // p = 0..15: block p >> 1, chunk p & 1
+    const char* base = ((p >> 1) < 4 ? xbase : wbase) + (kb & 1) * kMx4BigSlot + ((p >> 1) & 3) * 4096;
+    f.v[p >> 1][p & 1] = *reinterpret_cast<const gu32x4_t*>(base + slot[h][p & 1]);
+  };
+  gu32x2_t snext[8];  // the next stage's scale words, a run each
+  uint32_t sc[2][8];  // this stage's, the lane's block in bytes 0 (chunk 0) and 2
+  auto read_scale = [&](int kb, int b) {
+    const char* base = ring + ((kb >> 1) & 1) * kMx4BigRing + (b < 4 ? 0 : 4096);
+    snext[b] = *reinterpret_cast<const gu32x2_t*>(
+        base + ((b < 4 ? wm : wn) * 128 + (b & 3) * 32 + frow) * 16 + (kb & 1) * 8);
+  };
+
+  gf32x16_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  // one run (h of stage kb): the products of `cur`, the other run's fragments into
+  // `nxt`, and in run 1 the loads of stage kb + 2
+  auto run = [&](const Frags& cur, Frags& nxt, int kb, auto h) {
+    constexpr int kH = decltype(h)::value;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      if (c < 16) read_part(nxt, kb + kH, 1 - kH, c);
+      if constexpr (kH == 1) {
+        if ((c & 1) == 1) load_part(kb + 2, c >> 1);
+      }
+      const int q = c >> 4, i = (c >> 2) & 3, j = c & 3;
+      if (q == 0)
+        acc[i][j] = mfma64<0>(cur.v[4 + i][0], cur.v[j][0], acc[i][j], sc[kH][4 + i], sc[kH][j]);
+      else
+        acc[i][j] = mfma64<2>(cur.v[4 + i][1], cur.v[j][1], acc[i][j], sc[kH][4 + i], sc[kH][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  auto take_scales = [&](int kb) {
+    const bool whole = 2 * kb + 1 < tile.runs;
+    const uint32_t keep = whole ? ~0u : 0u, one = whole ? 0u : 0x7F7F7F7Fu;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      sc[0][b] = snext[b].x >> (8 * fhalf);
+      sc[1][b] = ((snext[b].y & keep) | one) >> (8 * fhalf);
+    }
+  };
+  if (stages > 0) {  // (a group may have no rows, a contraction no depth)
+    load_scale(-3);
+    load_scale(-2);
+    load_scale(-1);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) load_part(kb, i);
+    asm volatile("s_waitcnt vmcnt(16)" ::: "memory");  // scales and stage 0
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    Frags f0, f1;
+#pragma unroll
+    for (int p = 0; p < 16; ++p) read_part(f0, 0, 0, p);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) read_scale(0, b);
+    for (int kb = 0; kb < stages; ++kb) {
+      take_scales(kb);
+      run(f0, f1, kb, I0{});
+      // stage kb is in registers everywhere, stage kb + 1 has landed
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      load_scale(kb);
+#pragma unroll
+      for (int b = 0; b < 8; ++b) read_scale(kb + 1, b);
+      run(f1, f0, kb, I1{});
+    }
+  }
+  // every load has landed and every wave has read what it will: the stages are free
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  static_assert(4 * kStageBytes<false, 4> <= kMx4BigLds, "epilogue stage");
+  const int64_t row0 = tile.row0 + wm * 128, col0 = tile.col0 + wn * 128;
+  if (a.y_bf16)
+    store_tile<true, 4, 4>(acc, lds + wave * kStageBytes<true, 4>, tile.y, row0, col0, tile.m, a.n, lane);
+  else
+    store_tile<false, 4, 4>(acc, lds + wave * kStageBytes<false, 4>, tile.y, row0, col0, tile.m, a.n, lane);
+}
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void mx4_big_kernel(Mx4Args a, Mx4Args b, uint32_t first) {
+  __shared__ __attribute__((aligned(1024))) char lds[kMx4BigLds];
+  const bool second = blockIdx.x >= first;
+  mx4_big(second ? b : a, blockIdx.x - (second ? first : 0u), lds);
+}
+
 // Y = sum of `splits` float32 planes, in order; 4 elements a thread.
 template <bool kBf16>
 __global__ __launch_bounds__(256) void mx4_reduce_kernel(const float* __restrict__ parts, int splits,
@@ -299,75 +464,114 @@ __global__ __launch_bounds__(256) void mx4_reduce_kernel(const float* __restrict
   store4<kBf16>(Y, i, 0, (int)min((int64_t)4, total - i), vec, s[0], s[1], s[2], s[3]);
 }
 
-// Up to 16 rows (of a group): bound by reading W once. A workgroup owns `cols` <= 16
-// columns of Y; its waves take the stages (256 values along K) in turn, W straight
-// from memory into the MFMA's operand registers, and their sums meet in LDS in a fixed
-// order. Rows past the last or columns past the workgroup's repeat the last one and
-// are not stored.
-constexpr int kMx4SkinnyWaves = 8;
-__global__ __launch_bounds__(kMx4SkinnyWaves * 64) void mx4_skinny_kernel(Mx4Args a, int cols) {
-  __shared__ gf32x4_t part[kMx4SkinnyWaves][64];
+// Up to 16 kR rows (of a group): bound by reading W once. A wave multiplies 16 columns
+// of Y; `parts` waves share them and take K's quads (four runs, 512 values) in turn, and
+// their sums meet in LDS in a fixed order; a workgroup has as many sets of such waves as
+// its size gives. W goes straight from memory into the MFMA's operand registers: of a
+// quad a lane loads four runs' 16 bytes (256 consecutive bytes a row) and the 16 bytes
+// of the row's scales for all of them at once, kQuads quads before the first product.
+// (A scale word a run, the first way, was as many cache lines again as W itself: one
+// row of 13824 x 5120 17.0 us.) Rows past the last or columns past the workgroup's
+// repeat the last one and are not stored.
+template <int kR, int kQuads>
+__global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4Args a, int cols, int parts) {
+  __shared__ gf32x4_t sums[8][kR][64];
+  constexpr int kShift = kR == 1 ? 4 : kR == 2 ? 5 : 6;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kq = lane >> 4;
+  const int set = wave / parts, part = wave - set * parts, sets = (int)(blockDim.x >> 6) / parts;
   int64_t row0 = 0, row1 = a.m, wbase = 0;
   const uint32_t unit = blockIdx.x / a.tiles_n;
   if (a.mode == kMx4Rows) {
     int e;
     uint32_t before;
-    if (!group_unit(a.groups, 4, unit, e, before)) return;
+    if (!group_unit(a.groups, kShift, unit, e, before)) return;
     group_range(a.groups, e, row0, row1);
-    row0 += (int64_t)(unit - before) * 16;
-    row1 = min(row0 + 16, row1);
+    row0 += (int64_t)(unit - before) << kShift;
+    row1 = min(row0 + 16 * kR, row1);
     if (row0 >= row1) return;
     wbase = e * a.n;
   }
-  const int64_t n0 = (int64_t)(blockIdx.x - unit * a.tiles_n) * cols, n1 = min(n0 + cols, a.n);
-  const int64_t wr = wbase + min(n0 + r16, n1 - 1), xr = min(row0 + r16, row1 - 1);
-  const uint8_t *wp = a.w + wr * a.ldw + kq * 16, *xp = a.x + xr * a.ldx + kq * 16;
-  const uint32_t* wsp = reinterpret_cast<const uint32_t*>(a.ws + wr * (a.ldw / 16));
-  const uint32_t* xsp = reinterpret_cast<const uint32_t*>(a.xs + xr * (a.ldx / 16));
-  gf32x4_t acc = {0, 0, 0, 0};
-  // kU stages at a time, their loads all in flight before the first product (past the
-  // end the last run again, not used)
-  constexpr int kU = 4;
-  const int stages = (a.runs + 1) / 2;
-  for (int s0 = wave; s0 < stages; s0 += kU * kMx4SkinnyWaves) {
-    gu32x4_t w[kU][2], x[kU][2];
-    uint32_t sw[kU][2], sx[kU][2];
+  const int64_t n0 = ((int64_t)(blockIdx.x - unit * a.tiles_n) * sets + set) * cols;
+  const int64_t n1 = min(n0 + cols, a.n);
+  const int rows = (int)(row1 - row0);
+  gf32x4_t acc[kR];
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+  for (int j = 0; j < kR; ++j) acc[j] = gf32x4_t{0, 0, 0, 0};
+  if (n0 < n1) {  // (else the wave only waits for the others)
+    const Mx4Tile tile{a.x + row0 * a.ldx, a.xs + row0 * (a.ldx / 16), a.w + (wbase + n0) * a.ldw,
+                       a.ws + (wbase + n0) * (a.ldw / 16), rows, (int)(n1 - n0), a.runs, 0, 0, 0, nullptr};
+    const Mx4Buffers buf(tile, a.ldx, a.ldw);
+    const int wr = min(r16, tile.nrows - 1);
+    const uint32_t wo = wr * a.ldw + kq * 16, wso = wr * (a.ldw / 16);
+    uint32_t xo[kR], xso[kR];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = min(2 * (s0 + u * kMx4SkinnyWaves) + h, a.runs - 1);
-        w[u][h] = *reinterpret_cast<const gu32x4_t*>(wp + (int64_t)r * 64);
-        x[u][h] = *reinterpret_cast<const gu32x4_t*>(xp + (int64_t)r * 64);
-        sw[u][h] = wsp[r];
-        sx[u][h] = xsp[r];
+    for (int j = 0; j < kR; ++j) {
+      const int r = min(16 * j + r16, rows - 1);
+      xo[j] = r * a.ldx + kq * 16;
+      xso[j] = r * (a.ldx / 16);
+    }
+    auto load = [](__amdgpu_buffer_rsrc_t r, uint32_t lane_off, int off) {
+      return __builtin_bit_cast(gu32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
+    };
+    const int quads = (a.runs + 3) / 4;
+    for (int q0 = part; q0 < quads; q0 += kQuads * parts) {
+      gu32x4_t w[kQuads][4], sw[kQuads], x[kQuads][kR][4], sx[kQuads][kR];
+#pragma unroll
+      for (int u = 0; u < kQuads; ++u) {
+        const int q = q0 + u * parts;  // past the end: zeros, or scales that are not used
+        if (u > 0 && q >= quads) break;  // uniform
+        sw[u] = load(buf.ws, wso, q * 16);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[u][r] = load(buf.w, wo, (4 * q + r) * 64);
+#pragma unroll
+        for (int j = 0; j < kR; ++j) {
+          if (j > 0 && 16 * j >= rows) break;  // uniform
+          sx[u][j] = load(buf.xs, xso[j], q * 16);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[u][j][r] = load(buf.x, xo[j], (4 * q + r) * 64);
+        }
       }
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+      for (int u = 0; u < kQuads; ++u)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (2 * (s0 + u * kMx4SkinnyWaves) + h < a.runs)  // uniform
-          acc = mfma128(w[u][h], x[u][h], acc, sw[u][h] >> (8 * kq), sx[u][h] >> (8 * kq));
+        for (int j = 0; j < kR; ++j) {
+          if (j > 0 && 16 * j >= rows) break;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * (q0 + u * parts) + r < a.runs)
+              acc[j] = mfma128(w[u][r], x[u][j][r], acc[j], sw[u][r] >> (8 * kq), sx[u][j][r] >> (8 * kq));
+        }
+    }
   }
-  part[wave][lane] = acc;
-  __syncthreads();
-  if (wave == 0) {
-    gf32x4_t s = part[0][lane];
+  if (parts > 1) {
+    if (part > 0) {
 #pragma unroll
-    for (int v = 1; v < kMx4SkinnyWaves; ++v) s += part[v][lane];
-    const bool vec = (a.n & 3) == 0 && (cols & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
-    const int64_t col = n0 + kq * 4, row = row0 + r16;
+      for (int j = 0; j < kR; ++j) sums[wave][j][lane] = acc[j];
+    }
+    __syncthreads();
+    if (part > 0) return;
+    for (int v = 1; v < parts; ++v) {
+#pragma unroll
+      for (int j = 0; j < kR; ++j) acc[j] += sums[wave + v][j][lane];
+    }
+  }
+  const bool vec = (a.n & 3) == 0 && (cols & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+  const int64_t col = n0 + kq * 4;
+#pragma unroll
+  for (int j = 0; j < kR; ++j) {
+    const int64_t row = row0 + 16 * j + r16;
     if (row < row1 && col < n1) {
-      if (a.y_bf16) store4<true>(a.y, row * a.n + col, (int)col, (int)n1, vec, s[0], s[1], s[2], s[3]);
-      else store4<false>(a.y, row * a.n + col, (int)col, (int)n1, vec, s[0], s[1], s[2], s[3]);
+      if (a.y_bf16)
+        store4<true>(a.y, row * a.n + col, (int)col, (int)n1, vec, acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+      else
+        store4<false>(a.y, row * a.n + col, (int)col, (int)n1, vec, acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
     }
   }
 }
 
-enum Mx4Kind { kMx4Skinny, kMx4Small, kMx4OneRound, kMx4Middle };
+enum Mx4Kind { kMx4Skinny, kMx4Skinny2, kMx4Skinny4, kMx4Small, kMx4OneRound, kMx4Middle, kMx4Large };
 struct Mx4Plan {
   Mx4Kind kind;
   int splits, per_split;  // of K's stages
@@ -380,8 +584,10 @@ static Mx4Plan plan_mx4(int64_t m, int64_t n, int64_t k) {
   const int64_t stages = tiles_in(k, 256);
   const auto tiles = [&](int64_t t) { return tiles_in(m, t) * tiles_in(n, t); };
   // (a grid has fewer than 2^32 threads: 512 for 16 columns, so 2^23 - 1 workgroups)
-  if (m <= 16 && n <= (int64_t(1) << 26)) return {kMx4Skinny, 1, (int)stages};
+  if (m <= 64 && n <= (int64_t(1) << 26))
+    return {m <= 16 ? kMx4Skinny : m <= 32 ? kMx4Skinny2 : kMx4Skinny4, 1, (int)stages};
   const int64_t t128 = tiles(128);
+  if (4 * tiles_in(tiles(256), kMx4Cus) < 3 * tiles_in(t128, 2 * kMx4Cus)) return {kMx4Large, 1, (int)stages};
   if (t128 > kMx4Cus) return {kMx4Middle, 1, (int)stages};
   if (t128 >= kMx4Cus / 2) return {kMx4OneRound, 1, (int)stages};
   const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kMx4Cus / tiles(64), stages / 8));
@@ -393,15 +599,17 @@ static Mx4Plan plan_of(const Mx4Product& p) {
   if (p.mode == kMx4Plain) return plan_mx4(p.m, p.n, p.k);
   if (p.mode == kMx4Rows) {
     const int64_t mean = tiles_in(p.groups.rows, p.groups.count);
-    if (mean <= 16 && most_units(p.groups.rows, p.groups.count, 4) * tiles_in(p.n, 16) < (1 << 23))
-      return {kMx4Skinny, 1, all};
-    return {mean <= 64 ? kMx4Small : kMx4Middle, 1, all};
+    if (mean <= 64 && most_units(p.groups.rows, p.groups.count, 4) * tiles_in(p.n, 16) < (1 << 23))
+      return {mean <= 8 ? kMx4Skinny : mean <= 16 ? kMx4Skinny2 : kMx4Skinny4, 1, all};
+    return {mean <= 64 ? kMx4Small : mean <= 512 ? kMx4Middle : kMx4Large, 1, all};
   }
+  const int64_t t256 = p.groups.count * tiles_in(p.m, 256) * tiles_in(p.n, 256);
+  if (t256 >= kMx4Cus) return {kMx4Large, 1, all};
   return {p.groups.count * tiles_in(p.m, 128) * tiles_in(p.n, 128) >= kMx4Cus ? kMx4Middle : kMx4Small, 1, all};
 }
 
 static Mx4Args mx4_args(const Mx4Product& p, int64_t tile) {
-  const int shift = tile == 16 ? 4 : tile == 64 ? 6 : 7;
+  const int shift = tile == 16 ? 4 : tile == 32 ? 5 : tile == 64 ? 6 : tile == 128 ? 7 : 8;
   const int64_t tiles_m = p.mode == kMx4Rows ? most_units(p.groups.rows, p.groups.count, shift) : tiles_in(p.m, tile);
   return Mx4Args{p.x, p.xs, p.w, p.ws, (uint32_t)p.ldx, (uint32_t)p.ldw, p.m, p.n, (int)(p.k / 128), p.y,
                  p.y_bf16, p.mode, (uint32_t)tiles_m, (uint32_t)tiles_in(p.n, tile), p.groups};
@@ -424,15 +632,41 @@ static bool launch_mx4_tiles(const Mx4Args& a, const Mx4Args* b, const Mx4Plan& 
   hipLaunchKernelGGL((mx4_tile_kernel<config>), grid, dim3(threads), 0, stream, a, b ? *b : a,    \
                      (uint32_t)first, plan.per_split)
   switch (plan.kind) {
+    case kMx4Large:
+      hipLaunchKernelGGL(mx4_big_kernel, grid, dim3(256), 0, stream, a, b ? *b : a, (uint32_t)first);
+      break;
     case kMx4Middle: HIF4_MX4(HIF4_MX4_MIDDLE, 256); break;
     case kMx4OneRound: HIF4_MX4(HIF4_MX4_ONE_ROUND, 512); break;
     case kMx4Small: HIF4_MX4(HIF4_MX4_SMALL, 256); break;
-    case kMx4Skinny: return false;
+    default: return false;
   }
 #undef HIF4_MX4
   return true;
 }
-static int64_t mx4_tile_rows(Mx4Kind kind) { return kind == kMx4Small ? 64 : 128; }
+
+static hipError_t launch_mx4_skinny(const Mx4Product& p, Mx4Kind kind, hipStream_t stream) {
+  // Columns of a set of waves: the least that leaves as many sets a CU as 16 would, so
+  // that every CU has the same share (of a group, whose number is known on the device
+  // only, 16). A wave takes two quads of K at a time where it can, and small workgroups
+  // of a group are joined, since each has to find its group first.
+  const bool grouped = p.mode == kMx4Rows;
+  const int64_t per_cu = tiles_in(p.n, 16 * kMx4Cus), quads = tiles_in(p.k, 512);
+  const int cols = grouped ? 16 : (int)tiles_in(p.n, kMx4Cus * per_cu);  // 1 .. 16
+  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles_in(quads, 2)));
+  const int sets = grouped ? 8 / parts : 1;
+  Mx4Args a = mx4_args(p, kind == kMx4Skinny ? 16 : kind == kMx4Skinny2 ? 32 : 64);
+  if (!grouped) a.tiles_m = 1;
+  a.tiles_n = (uint32_t)tiles_in(p.n, cols * sets);
+  const dim3 grid(a.tiles_m * a.tiles_n), block(64 * parts * sets);
+  if (kind == kMx4Skinny)
+    hipLaunchKernelGGL((mx4_skinny_kernel<1, 2>), grid, block, 0, stream, a, cols, parts);
+  else if (kind == kMx4Skinny2)
+    hipLaunchKernelGGL((mx4_skinny_kernel<2, 1>), grid, block, 0, stream, a, cols, parts);
+  else
+    hipLaunchKernelGGL((mx4_skinny_kernel<4, 1>), grid, block, 0, stream, a, cols, parts);
+  return hipGetLastError();
+}
+static int64_t mx4_tile_rows(Mx4Kind kind) { return kind == kMx4Small ? 64 : kind == kMx4Large ? 256 : 128; }
 
 }  // namespace hif4
 
@@ -440,18 +674,7 @@ using namespace hif4;
 
 hipError_t hif4_launch_gemm_mxfp4(const Mx4Product& p, void* workspace, hipStream_t stream) {
   const Mx4Plan plan = plan_of(p);
-  if (plan.kind == kMx4Skinny) {
-    // columns: the least that leaves as many workgroups a CU as 16 would, so that
-    // every CU has the same share (with groups, whose number is known on the device
-    // only, 16)
-    const int64_t per_cu = tiles_in(p.n, 16 * kMx4Cus);
-    const int cols = p.mode == kMx4Rows ? 16 : (int)tiles_in(p.n, kMx4Cus * per_cu);  // 1 .. 16
-    Mx4Args a = mx4_args(p, 16);
-    a.tiles_n = (uint32_t)tiles_in(p.n, cols);
-    hipLaunchKernelGGL(mx4_skinny_kernel, dim3(a.tiles_m * a.tiles_n), dim3(kMx4SkinnyWaves * 64), 0,
-                       stream, a, cols);
-    return hipGetLastError();
-  }
+  if (plan.kind <= kMx4Skinny4) return launch_mx4_skinny(p, plan.kind, stream);
   Mx4Args a = mx4_args(p, mx4_tile_rows(plan.kind));
   if (plan.splits == 1)
     return launch_mx4_tiles(a, nullptr, plan, stream) ? hipGetLastError() : hipErrorInvalidValue;
@@ -474,7 +697,7 @@ hipError_t hif4_launch_gemm_mxfp4(const Mx4Product& p, void* workspace, hipStrea
 hipError_t hif4_launch_gemm_mxfp4_two(const Mx4Product& a, const Mx4Product& b, void* workspace,
                                       hipStream_t stream) {
   const Mx4Plan pa = plan_of(a), pb = plan_of(b);
-  if (pa.kind == pb.kind && pa.kind != kMx4Skinny && pa.splits == 1 && pb.splits == 1) {
+  if (pa.kind == pb.kind && pa.kind > kMx4Skinny4 && pa.splits == 1 && pb.splits == 1) {
     const Mx4Args ga = mx4_args(a, mx4_tile_rows(pa.kind)), gb = mx4_args(b, mx4_tile_rows(pb.kind));
     const int most = pa.per_split > pb.per_split ? pa.per_split : pb.per_split;
     if (launch_mx4_tiles(ga, &gb, Mx4Plan{pa.kind, 1, most}, stream)) return hipGetLastError();

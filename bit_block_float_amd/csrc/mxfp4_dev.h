@@ -88,12 +88,15 @@ __device__ __forceinline__ void group_range(const Groups& g, int e, int64_t& beg
 // group_units: how many there are in all; group_unit: the group of unit t, and the
 // units before that group (false: there is no unit t); units_before: the units before
 // group e. Every lane of the wave takes part, and each has the same result.
-__device__ __forceinline__ uint32_t lanes_inclusive(uint32_t v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_up((int)v, d, 64);
-    if (lane >= d) v += o;
-  }
+__device__ __forceinline__ uint32_t lanes_inclusive(uint32_t v) {
+  // DPP moves: within rows of 16 lanes, then row 0's sum to row 1 and 2's to 3, then
+  // the lower half's to the upper one
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);  // row_shr 1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);  // row_shr 2
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);  // row_shr 4
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);  // row_shr 8
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);  // row_bcast 15
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);  // row_bcast 31
   return v;
 }
 __device__ __forceinline__ uint32_t units_of(const Groups& g, int e, int shift) {
@@ -106,14 +109,14 @@ __device__ __forceinline__ uint32_t group_units(const Groups& g, int shift) {
   const int lane = threadIdx.x & 63;
   uint32_t sum = 0;
   for (int e = lane; e < g.count; e += 64) sum += units_of(g, e, shift);
-  return (uint32_t)__builtin_amdgcn_readlane((int)lanes_inclusive(sum, lane), 63);
+  return (uint32_t)__builtin_amdgcn_readlane((int)lanes_inclusive(sum), 63);
 }
 __device__ __forceinline__ bool group_unit(const Groups& g, int shift, uint32_t t, int& group,
                                            uint32_t& before) {
   const int lane = threadIdx.x & 63;
   uint32_t sum = 0;
   for (int e0 = 0; e0 < g.count; e0 += 64) {
-    const uint32_t n = units_of(g, e0 + lane, shift), incl = sum + lanes_inclusive(n, lane);
+    const uint32_t n = units_of(g, e0 + lane, shift), incl = sum + lanes_inclusive(n);
     const uint64_t past = __ballot(incl > t);
     if (past != 0) {
       const int first = __ffsll((unsigned long long)past) - 1;
@@ -129,7 +132,7 @@ __device__ __forceinline__ uint32_t units_before(const Groups& g, int shift, int
   const int lane = threadIdx.x & 63;
   uint32_t sum = 0;
   for (int e = lane; e < group; e += 64) sum += units_of(g, e, shift);
-  return (uint32_t)__builtin_amdgcn_readlane((int)lanes_inclusive(sum, lane), 63);
+  return (uint32_t)__builtin_amdgcn_readlane((int)lanes_inclusive(sum), 63);
 }
 
 // Units of 2^shift rows that groups of as many rows can have at most.
