@@ -42,10 +42,8 @@ __device__ __forceinline__ gf32x4_t mfma128(gu32x4_t a, gu32x4_t b, gf32x4_t c, 
 // This wave's loads but the newest n have landed, its LDS reads are done.
 template <int n>
 __device__ __forceinline__ void wait_mx4() {
-  static_assert(n == 0 || n == 5 || n == 10, "one asm a count");
-  if constexpr (n == 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  if constexpr (n == 5) asm volatile("s_waitcnt vmcnt(5) lgkmcnt(0)" ::: "memory");
-  if constexpr (n == 10) asm volatile("s_waitcnt vmcnt(10) lgkmcnt(0)" ::: "memory");
+  static_assert(n >= 0 && n < 64, "what the counter holds");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(n) : "memory");
 }
 
 struct Mx4Args {
@@ -91,9 +89,8 @@ __device__ __forceinline__ bool mx4_locate(const Mx4Args& a, uint32_t t, Mx4Tile
     tile_in(t - before * a.tiles_n, own, a.tiles_n, tm, tn);
     group = e;
   } else {
-    const uint32_t per = a.tiles_m * a.tiles_n;
-    t = xcd_order(t, per * (uint32_t)a.groups.count);
-    const uint32_t e = t / per;
+    // each group's tiles over all XCDs: their depth differs from group to group
+    const uint32_t per = a.tiles_m * a.tiles_n, e = t / per;
     tile_in(t - e * per, a.tiles_m, a.tiles_n, tm, tn);
     int64_t begin, end;
     group_range(a.groups, (int)e, begin, end);
@@ -286,17 +283,30 @@ __global__ __launch_bounds__(kWM* kWN * 64) void mx4_tile_kernel(Mx4Args a, Mx4A
 // and run 0 of stage kb + 1 is read. Stages past the end load the last one again, into
 // one that no one reads. Where the last stage has one run only, the other's codes are
 // loaded as zeros (from beyond the buffers) and its scales taken as 1: an exit between
-// the runs, or a copy of run 0 behind the loop, made the compiler spill. Scales come 16 bytes a row (two stages) at a time, into a ring
-// of two: X's for stages 2g and 2g + 1 in stage 2g - 3, W's in stage 2g - 2 (one load a
-// stage, whose target is chosen without a branch).
+// the runs, or a copy of run 0 behind the loop, made the compiler spill.
+//
+// Scales come 32 bytes a row, four stages' worth, into a ring of two, one load a stage,
+// whose target is chosen without a branch (a branch in the loop lets the compiler move
+// products across the step's barrier). Each row's are in a line of their own, and a load
+// fetches all 128 bytes of it: 16 bytes a row at a time are half as many bytes from L2 as
+// the codes and cost 5%, these half of that.
+//
+// Bound: the matrix cores at the clock that power allows, and a tile's ends. Measured on
+// 57600 x 13824 x 5120, bf16 Y: 2.02 ms (4.0 PFLOP/s); the products alone, from registers,
+// 1.40 ms (5.8, at 1.55 GHz), without stores 1.80, without loads 1.76, without LDS reads
+// 1.88. Loads spread over a whole stage, fragments of half a run, rows of 64 bytes in four
+// slots with twice the time to land, and one barrier more a stage for earlier loads gave
+// nothing or less.
 constexpr int kMx4BigSlot = 2 * 256 * 128;
-constexpr int kMx4BigRing = 2 * 256 * 16;
+constexpr int kMx4BigRing = 2 * 256 * 32;
 constexpr int kMx4BigLds = 2 * kMx4BigSlot + 2 * kMx4BigRing;
 
 __device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* const lds) {
   Mx4Tile tile;
   if (!mx4_locate<256, 256>(a, t, tile)) return;
   const Mx4Buffers buf(tile, a.ldx, a.ldw);
+  // (uniform for the compiler, too: it would fetch them from a copy of the arguments lane by lane)
+  const uint32_t ldx = __builtin_amdgcn_readfirstlane(a.ldx), ldw = __builtin_amdgcn_readfirstlane(a.ldw);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -309,8 +319,8 @@ __device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* cons
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t c = (uint32_t)((lane & 7) ^ ((4 * i + (lane >> 4)) & 7));
-    xoff[i] = (uint32_t)(wave * 64 + (lane >> 3)) * a.ldx + c * 16;
-    woff[i] = (uint32_t)(wave * 64 + (lane >> 3)) * a.ldw + c * 16;
+    xoff[i] = (uint32_t)(wave * 64 + (lane >> 3)) * ldx + c * 16;
+    woff[i] = (uint32_t)(wave * 64 + (lane >> 3)) * ldw + c * 16;
     second[i] = c >= 4;
   }
   auto load_part = [&](int kb, int i) {
@@ -318,17 +328,23 @@ __device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* cons
     const int off = min(kb, stages - 1) * 128;
     const bool half = (tile.runs & 1) && kb >= stages - 1;
     const uint32_t at = half && second[i & 1] ? 0x7FFFFFFFu : (i < 8 ? xoff : woff)[i & 1];
-    if (i < 8) load_lds16(buf.x, dst, at, off + (i & 7) * 8 * (int)a.ldx);
-    else load_lds16(buf.w, dst, at, off + (i & 7) * 8 * (int)a.ldw);
+    if (i < 8) load_lds16(buf.x, dst, at, off + (i & 7) * 8 * (int)ldx);
+    else load_lds16(buf.w, dst, at, off + (i & 7) * 8 * (int)ldw);
   };
-  const uint32_t xs_off = (uint32_t)(wave * 64 + lane) * (a.ldx / 16);
-  const uint32_t ws_off = (uint32_t)(wave * 64 + lane) * (a.ldw / 16);
+  // A load of scales brings 32 bytes (four stages') of 32 rows, piece p of 16 bytes of row
+  // r in slot p ^ ((r >> 3) & 1)
+  const uint32_t piece = (uint32_t)((lane & 1) ^ ((lane >> 4) & 1)) * 16;
+  const uint32_t xs_off = (uint32_t)(wave * 64 + (lane >> 1)) * (ldx / 16) + piece;
+  const uint32_t ws_off = (uint32_t)(wave * 64 + (lane >> 1)) * (ldw / 16) + piece;
   char* const ring = lds + 2 * kMx4BigSlot;
-  auto load_scale = [&](int kb) {  // kb >= -3
-    const bool is_w = (kb & 1) == 0;
-    const int g = (kb + 3) >> 1, at = min(g, (stages - 1) >> 1) * 16;
-    load_lds16(is_w ? buf.ws : buf.xs, ring + (g & 1) * kMx4BigRing + (is_w ? 4096 : 0) + wave * 1024,
-               is_w ? ws_off : xs_off, at);
+  const int last_group = (stages - 1) >> 2;
+  auto load_scale = [&](int kb) {  // kb >= -5
+    const int g = ((kb + 1) >> 2) + 1, part = (kb + 1) & 3;
+    const bool is_w = part >= 2;
+    load_lds16(is_w ? buf.ws : buf.xs,
+               ring + (g & 1) * kMx4BigRing + (is_w ? 8192 : 0) + wave * 2048 + (part & 1) * 1024,
+               is_w ? ws_off : xs_off,
+               min(g, last_group) * 32 + (part & 1) * 2 * (int)(is_w ? ldw : ldx));
   };
 
   const int frow = lane & 31, fhalf = lane >> 5, fsw = (frow >> 1) & 7;
@@ -347,12 +363,15 @@ __device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* cons
     const char* base = ((p >> 1) < 4 ? xbase : wbase) + (kb & 1) * kMx4BigSlot + ((p >> 1) & 3) * 4096;
     f.v[p >> 1][p & 1] = *reinterpret_cast<const gu32x4_t*>(base + slot[h][p & 1]);
   };
-  gu32x2_t snext[8];  // the next stage's scale words, a run each
-  uint32_t sc[2][8];  // this stage's, the lane's block in bytes 0 (chunk 0) and 2
-  auto read_scale = [&](int kb, int b) {
-    const char* base = ring + ((kb >> 1) & 1) * kMx4BigRing + (b < 4 ? 0 : 4096);
-    snext[b] = *reinterpret_cast<const gu32x2_t*>(
-        base + ((b < 4 ? wm : wn) * 128 + (b & 3) * 32 + frow) * 16 + (kb & 1) * 8);
+  // Scale words, a run each: of the next stage as read, lanes 0..31 a block of 32 rows and
+  // lanes 32..63 the one behind it; of this stage, every lane its own row's of each block,
+  // its chunks' bytes in bytes 0 and 2.
+  gu32x2_t snext[4];
+  uint32_t sc[2][8];
+  auto read_scale = [&](int kb, int q) {  // blocks 2q and 2q + 1
+    const int at = (((kb >> 1) & 1) ^ ((lane >> 3) & 1)) * 16 + (kb & 1) * 8;
+    const char* base = ring + ((kb >> 2) & 1) * kMx4BigRing + (q < 2 ? 0 : 8192);
+    snext[q] = *reinterpret_cast<const gu32x2_t*>(base + ((q < 2 ? wm : wn) * 128 + (q & 1) * 64 + lane) * 32 + at);
   };
 
   gf32x16_t acc[4][4];
@@ -371,7 +390,9 @@ __device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* cons
     for (int c = 0; c < 32; ++c) {
       if (c < 16) read_part(nxt, kb + kH, 1 - kH, c);
       if constexpr (kH == 1) {
+        if (c == 0) load_scale(kb);
         if ((c & 1) == 1) load_part(kb + 2, c >> 1);
+        if (c >= 17 && c < 29 && (c - 17) % 3 == 0) read_scale(kb + 1, (c - 17) / 3);
       }
       const int q = c >> 4, i = (c >> 2) & 3, j = c & 3;
       if (q == 0)
@@ -387,15 +408,19 @@ __device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* cons
     const bool whole = 2 * kb + 1 < tile.runs;
     const uint32_t keep = whole ? ~0u : 0u, one = whole ? 0u : 0x7F7F7F7Fu;
 #pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      sc[0][b] = snext[b].x >> (8 * fhalf);
-      sc[1][b] = ((snext[b].y & keep) | one) >> (8 * fhalf);
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t w0 = snext[q].x, w1 = (snext[q].y & keep) | one;
+      const auto p0 = __builtin_amdgcn_permlane32_swap(w0, w0, false, false);
+      const auto p1 = __builtin_amdgcn_permlane32_swap(w1, w1, false, false);
+      sc[0][2 * q] = p0[0] >> (8 * fhalf);
+      sc[0][2 * q + 1] = p0[1] >> (8 * fhalf);
+      sc[1][2 * q] = p1[0] >> (8 * fhalf);
+      sc[1][2 * q + 1] = p1[1] >> (8 * fhalf);
     }
   };
   if (stages > 0) {  // (a group may have no rows, a contraction no depth)
-    load_scale(-3);
-    load_scale(-2);
-    load_scale(-1);
+#pragma unroll
+    for (int kb = -5; kb < 0; ++kb) load_scale(kb);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
@@ -407,7 +432,7 @@ __device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* cons
 #pragma unroll
     for (int p = 0; p < 16; ++p) read_part(f0, 0, 0, p);
 #pragma unroll
-    for (int b = 0; b < 8; ++b) read_scale(0, b);
+    for (int q = 0; q < 4; ++q) read_scale(0, q);
     for (int kb = 0; kb < stages; ++kb) {
       take_scales(kb);
       run(f0, f1, kb, I0{});
@@ -415,9 +440,6 @@ __device__ __forceinline__ void mx4_big(const Mx4Args& a, uint32_t t, char* cons
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      load_scale(kb);
-#pragma unroll
-      for (int b = 0; b < 8; ++b) read_scale(kb + 1, b);
       run(f1, f0, kb, I1{});
     }
   }
@@ -571,7 +593,7 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4Args a, int cols, in
   }
 }
 
-enum Mx4Kind { kMx4Skinny, kMx4Skinny2, kMx4Skinny4, kMx4Small, kMx4OneRound, kMx4Middle, kMx4Large };
+enum Mx4Kind { kMx4Skinny, kMx4Skinny2, kMx4Skinny4, kMx4Small, kMx4Middle, kMx4Large };
 struct Mx4Plan {
   Mx4Kind kind;
   int splits, per_split;  // of K's stages
@@ -588,8 +610,7 @@ static Mx4Plan plan_mx4(int64_t m, int64_t n, int64_t k) {
     return {m <= 16 ? kMx4Skinny : m <= 32 ? kMx4Skinny2 : kMx4Skinny4, 1, (int)stages};
   const int64_t t128 = tiles(128);
   if (4 * tiles_in(tiles(256), kMx4Cus) < 3 * tiles_in(t128, 2 * kMx4Cus)) return {kMx4Large, 1, (int)stages};
-  if (t128 > kMx4Cus) return {kMx4Middle, 1, (int)stages};
-  if (t128 >= kMx4Cus / 2) return {kMx4OneRound, 1, (int)stages};
+  if (t128 >= kMx4Cus / 2) return {kMx4Middle, 1, (int)stages};
   const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kMx4Cus / tiles(64), stages / 8));
   const int64_t per = tiles_in(stages, splits);
   return {kMx4Small, (int)tiles_in(stages, per), (int)per};
@@ -620,7 +641,6 @@ static uint64_t mx4_tiles(const Mx4Args& a) {
 
 // The tile kernels by kind: tile rows and columns, waves both ways, stages.
 #define HIF4_MX4_SMALL 64, 64, 2, 2, 4
-#define HIF4_MX4_ONE_ROUND 128, 128, 2, 4, 3
 #define HIF4_MX4_MIDDLE 128, 128, 2, 2, 2
 
 // `b` may be NULL. false: not launched (too many tiles).
@@ -636,7 +656,6 @@ static bool launch_mx4_tiles(const Mx4Args& a, const Mx4Args* b, const Mx4Plan& 
       hipLaunchKernelGGL(mx4_big_kernel, grid, dim3(256), 0, stream, a, b ? *b : a, (uint32_t)first);
       break;
     case kMx4Middle: HIF4_MX4(HIF4_MX4_MIDDLE, 256); break;
-    case kMx4OneRound: HIF4_MX4(HIF4_MX4_ONE_ROUND, 512); break;
     case kMx4Small: HIF4_MX4(HIF4_MX4_SMALL, 256); break;
     default: return false;
   }
