@@ -498,7 +498,8 @@ __global__ __launch_bounds__(256) void mx4_reduce_kernel(const float* __restrict
 template <int kR, int kQuads>
 __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4Args a, int cols, int parts) {
   __shared__ gf32x4_t sums[8][kR][64];
-  constexpr int kShift = kR == 1 ? 4 : kR == 2 ? 5 : 6;
+  static_assert(kR == 1 || kR == 2, "units of 16 or 32 rows");
+  constexpr int kShift = kR == 1 ? 4 : 5;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kq = lane >> 4;
@@ -593,7 +594,7 @@ __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4Args a, int cols, in
   }
 }
 
-enum Mx4Kind { kMx4Skinny, kMx4Skinny2, kMx4Skinny4, kMx4Small, kMx4Middle, kMx4Large };
+enum Mx4Kind { kMx4Skinny, kMx4Skinny2, kMx4Small, kMx4Middle, kMx4Large };
 struct Mx4Plan {
   Mx4Kind kind;
   int splits, per_split;  // of K's stages
@@ -601,32 +602,73 @@ struct Mx4Plan {
 constexpr int64_t kMx4Cus = 256;
 static int64_t tiles_in(int64_t v, int64_t tile) { return (v + tile - 1) / tile; }
 
-// Which kernel, from the sizes alone.
+// Which kernel, from the sizes alone. Measured, bf16 Y, us:
+//   m x n x k             16 or 32 rows   64 x 64   128 x 128   256 x 256
+//   17 x 5120 x 5120           7.8           8.5       15
+//   32 x 2048 x 2048           4.1           5.3        8.2
+//   32 x 5120 x 5120           9.5           8.5       15
+//   128 x 13824 x 5120                      17         19.6
+//   256 x 13824 x 5120                      27         21
+//   512 x 5120 x 5120                       21         16         31
+//   512 x 13824 x 5120                      49         30         33
+//   1024 x 5120 x 5120                      37         27         33
+//   1024 x 13824 x 5120                     94         57         43
+//   2048 x 5120 x 5120                      69         45         35
+//   4096 x 4096 x 512                       24         12.2       13.4
+//   4096 x 4096 x 2048                      44         25.4       24.8
+//   8192 x 8192 x 256                                  34         43
+//   8192 x 8192 x 1024                     112         66         62
+// A round of 256 tiles of 256 x 256 costs 4/3 of one of 512 tiles of 128 x 128, from
+// some four stages on (below, its ends count, which nothing else on the CU hides).
+// Splitting K pays for its second kernel from some 16 stages a part: 64 x 5120 x 5120
+// 8.5 us whole, 10.7 in 2; 64 x 5120 x 13824 21 whole, 16.6 in 6, 17 in 3.
 static Mx4Plan plan_mx4(int64_t m, int64_t n, int64_t k) {
   const int64_t stages = tiles_in(k, 256);
   const auto tiles = [&](int64_t t) { return tiles_in(m, t) * tiles_in(n, t); };
   // (a grid has fewer than 2^32 threads: 512 for 16 columns, so 2^23 - 1 workgroups)
-  if (m <= 64 && n <= (int64_t(1) << 26))
-    return {m <= 16 ? kMx4Skinny : m <= 32 ? kMx4Skinny2 : kMx4Skinny4, 1, (int)stages};
+  if (m <= 16 && n <= (int64_t(1) << 26)) return {kMx4Skinny, 1, (int)stages};
+  if (m <= 32 && n <= 4096) return {kMx4Skinny2, 1, (int)stages};
   const int64_t t128 = tiles(128);
-  if (4 * tiles_in(tiles(256), kMx4Cus) < 3 * tiles_in(t128, 2 * kMx4Cus)) return {kMx4Large, 1, (int)stages};
+  if (stages >= 4 && 4 * tiles_in(tiles(256), kMx4Cus) < 3 * tiles_in(t128, 2 * kMx4Cus))
+    return {kMx4Large, 1, (int)stages};
   if (t128 >= kMx4Cus / 2) return {kMx4Middle, 1, (int)stages};
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kMx4Cus / tiles(64), stages / 8));
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kMx4Cus / tiles(64), stages / 16));
   const int64_t per = tiles_in(stages, splits);
   return {kMx4Small, (int)tiles_in(stages, per), (int)per};
 }
+// The same for rows in groups, by the mean of a group (what is on the host). Measured with
+// a skewed choice of groups, bf16 Y, us:
+//   groups x mean x n x k     32 rows   64 x 64   128 x 128   256 x 256
+//   32 x 3 x 5120 x 2048        32         39         41
+//   128 x 4 x 2048 x 1024       30         40         36
+//   32 x 8 x 5120 x 2048        45         43         43
+//   8 x 16 x 5120 x 5120        38         34         38
+//   32 x 16 x 5120 x 2048       58         49         45
+//   32 x 64 x 5120 x 2048      142         67         51          71
+//   128 x 256 x 2048 x 1024               201        102         118
+//   32 x 256 x 5120 x 2048                174         98          99
+//   8 x 512 x 5120 x 5120                 199        109          86
+//   32 x 1024 x 5120 x 2048               570        302         280
+// (units of 16 rows instead of 32, 32 x 3 x 5120 x 2048: 35.5: W is read again for the
+// second half of a group of more.)
 static Mx4Plan plan_of(const Mx4Product& p) {
   const int all = (int)tiles_in(p.k, 256);
   if (p.mode == kMx4Plain) return plan_mx4(p.m, p.n, p.k);
   if (p.mode == kMx4Rows) {
     const int64_t mean = tiles_in(p.groups.rows, p.groups.count);
-    if (mean <= 64 && most_units(p.groups.rows, p.groups.count, 4) * tiles_in(p.n, 16) < (1 << 23))
-      return {mean <= 8 ? kMx4Skinny : mean <= 16 ? kMx4Skinny2 : kMx4Skinny4, 1, all};
-    return {mean <= 64 ? kMx4Small : mean <= 512 ? kMx4Middle : kMx4Large, 1, all};
+    // (workgroups below 2^23, as above)
+    if (mean <= 6 && most_units(p.groups.rows, p.groups.count, 5) * tiles_in(p.n, 16) < (1 << 23))
+      return {kMx4Skinny2, 1, all};
+    if (mean <= 16) return {kMx4Small, 1, all};
+    return {mean >= 256 && mean * p.k >= (1 << 19) ? kMx4Large : kMx4Middle, 1, all};
   }
+  // K in groups, groups x mean x m x n, fp32 Y, 128 x 128 and 256 x 256: 32 x 64 x 2048 x
+  // 2048 104 and 114 (Y's bytes 103), 16 x 256 x 2048 x 5120 135 and 145 (129), 16 x 1024 x
+  // 2048 x 5120 233 and 195, 8 x 2048 x 2048 x 5120 190 and 149, 4 x 512 x 1024 x 1024 7 and
+  // 13 (64 x 64: 10).
   const int64_t t256 = p.groups.count * tiles_in(p.m, 256) * tiles_in(p.n, 256);
-  if (t256 >= kMx4Cus) return {kMx4Large, 1, all};
-  return {p.groups.count * tiles_in(p.m, 128) * tiles_in(p.n, 128) >= kMx4Cus ? kMx4Middle : kMx4Small, 1, all};
+  if (t256 >= kMx4Cus && p.groups.rows / p.groups.count >= 512) return {kMx4Large, 1, all};
+  return {p.groups.count * tiles_in(p.m, 128) * tiles_in(p.n, 128) >= kMx4Cus / 2 ? kMx4Middle : kMx4Small, 1, all};
 }
 
 static Mx4Args mx4_args(const Mx4Product& p, int64_t tile) {
@@ -673,16 +715,14 @@ static hipError_t launch_mx4_skinny(const Mx4Product& p, Mx4Kind kind, hipStream
   const int cols = grouped ? 16 : (int)tiles_in(p.n, kMx4Cus * per_cu);  // 1 .. 16
   const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(8, tiles_in(quads, 2)));
   const int sets = grouped ? 8 / parts : 1;
-  Mx4Args a = mx4_args(p, kind == kMx4Skinny ? 16 : kind == kMx4Skinny2 ? 32 : 64);
+  Mx4Args a = mx4_args(p, kind == kMx4Skinny ? 16 : 32);
   if (!grouped) a.tiles_m = 1;
   a.tiles_n = (uint32_t)tiles_in(p.n, cols * sets);
   const dim3 grid(a.tiles_m * a.tiles_n), block(64 * parts * sets);
   if (kind == kMx4Skinny)
     hipLaunchKernelGGL((mx4_skinny_kernel<1, 2>), grid, block, 0, stream, a, cols, parts);
-  else if (kind == kMx4Skinny2)
-    hipLaunchKernelGGL((mx4_skinny_kernel<2, 1>), grid, block, 0, stream, a, cols, parts);
   else
-    hipLaunchKernelGGL((mx4_skinny_kernel<4, 1>), grid, block, 0, stream, a, cols, parts);
+    hipLaunchKernelGGL((mx4_skinny_kernel<2, 1>), grid, block, 0, stream, a, cols, parts);
   return hipGetLastError();
 }
 static int64_t mx4_tile_rows(Mx4Kind kind) { return kind == kMx4Small ? 64 : kind == kMx4Large ? 256 : 128; }
@@ -693,7 +733,7 @@ using namespace hif4;
 
 hipError_t hif4_launch_gemm_mxfp4(const Mx4Product& p, void* workspace, hipStream_t stream) {
   const Mx4Plan plan = plan_of(p);
-  if (plan.kind <= kMx4Skinny4) return launch_mx4_skinny(p, plan.kind, stream);
+  if (plan.kind <= kMx4Skinny2) return launch_mx4_skinny(p, plan.kind, stream);
   Mx4Args a = mx4_args(p, mx4_tile_rows(plan.kind));
   if (plan.splits == 1)
     return launch_mx4_tiles(a, nullptr, plan, stream) ? hipGetLastError() : hipErrorInvalidValue;
@@ -716,7 +756,7 @@ hipError_t hif4_launch_gemm_mxfp4(const Mx4Product& p, void* workspace, hipStrea
 hipError_t hif4_launch_gemm_mxfp4_two(const Mx4Product& a, const Mx4Product& b, void* workspace,
                                       hipStream_t stream) {
   const Mx4Plan pa = plan_of(a), pb = plan_of(b);
-  if (pa.kind == pb.kind && pa.kind > kMx4Skinny4 && pa.splits == 1 && pb.splits == 1) {
+  if (pa.kind == pb.kind && pa.kind > kMx4Skinny2 && pa.splits == 1 && pb.splits == 1) {
     const Mx4Args ga = mx4_args(a, mx4_tile_rows(pa.kind)), gb = mx4_args(b, mx4_tile_rows(pb.kind));
     const int most = pa.per_split > pb.per_split ? pa.per_split : pb.per_split;
     if (launch_mx4_tiles(ga, &gb, Mx4Plan{pa.kind, 1, most}, stream)) return hipGetLastError();
