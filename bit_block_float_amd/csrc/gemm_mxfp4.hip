@@ -659,8 +659,14 @@ static Mx4Plan plan_of(const Mx4Product& p) {
     // (workgroups below 2^23, as above)
     if (mean <= 6 && most_units(p.groups.rows, p.groups.count, 5) * tiles_in(p.n, 16) < (1 << 23))
       return {kMx4Skinny2, 1, all};
-    if (mean <= 16) return {kMx4Small, 1, all};
-    return {mean >= 256 && mean * p.k >= (1 << 19) ? kMx4Large : kMx4Middle, 1, all};
+    // tiles as if every group ended in the middle of one
+    const auto tiles = [&](int64_t t) {
+      return (p.groups.rows / t + (p.groups.count + 1) / 2) * tiles_in(p.n, t);
+    };
+    if (mean <= 16 || tiles(128) < kMx4Cus / 2) return {kMx4Small, 1, all};
+    const bool large = mean >= 256 && mean * p.k >= (1 << 19) &&
+                       4 * tiles_in(tiles(256), kMx4Cus) < 3 * tiles_in(tiles(128), 2 * kMx4Cus);
+    return {large ? kMx4Large : kMx4Middle, 1, all};
   }
   // K in groups, groups x mean x m x n, fp32 Y, 128 x 128 and 256 x 256: 32 x 64 x 2048 x
   // 2048 104 and 114 (Y's bytes 103), 16 x 256 x 2048 x 5120 135 and 145 (129), 16 x 1024 x
@@ -752,14 +758,21 @@ hipError_t hif4_launch_gemm_mxfp4(const Mx4Product& p, void* workspace, hipStrea
   return hipGetLastError();
 }
 
-// Two independent products, in one launch where both take the same tile kernel whole.
+// Two independent products, in one launch where both take the same tile kernel whole, or
+// both are small (64 x 64 tiles cost little more than the kernel for few rows, a second
+// launch some 4 us), or as tiles of 128 x 128 fill the CUs once (1001 x 1300 x 640 in 5
+// groups: 11.4 us, apart 14.8).
 hipError_t hif4_launch_gemm_mxfp4_two(const Mx4Product& a, const Mx4Product& b, void* workspace,
                                       hipStream_t stream) {
   const Mx4Plan pa = plan_of(a), pb = plan_of(b);
-  if (pa.kind == pb.kind && pa.kind > kMx4Skinny2 && pa.splits == 1 && pb.splits == 1) {
-    const Mx4Args ga = mx4_args(a, mx4_tile_rows(pa.kind)), gb = mx4_args(b, mx4_tile_rows(pb.kind));
+  const bool small = pa.kind <= kMx4Small && pb.kind <= kMx4Small;
+  const bool once = pa.kind <= kMx4Middle && pb.kind <= kMx4Middle &&
+                    mx4_tiles(mx4_args(a, 128)) + mx4_tiles(mx4_args(b, 128)) <= 2 * (uint64_t)kMx4Cus;
+  if ((pa.kind == pb.kind || small || once) && pa.splits == 1 && pb.splits == 1) {
+    const Mx4Kind kind = small ? kMx4Small : once ? kMx4Middle : pa.kind;
+    const Mx4Args ga = mx4_args(a, mx4_tile_rows(kind)), gb = mx4_args(b, mx4_tile_rows(kind));
     const int most = pa.per_split > pb.per_split ? pa.per_split : pb.per_split;
-    if (launch_mx4_tiles(ga, &gb, Mx4Plan{pa.kind, 1, most}, stream)) return hipGetLastError();
+    if (launch_mx4_tiles(ga, &gb, Mx4Plan{kind, 1, most}, stream)) return hipGetLastError();
   }
   const hipError_t e = hif4_launch_gemm_mxfp4(a, workspace, stream);
   return e != hipSuccess ? e : hif4_launch_gemm_mxfp4(b, workspace, stream);

@@ -100,6 +100,8 @@ __device__ __forceinline__ void store_tile(const gf32x16_t (&acc)[kTN][kTM], cha
       char* dst = reinterpret_cast<char*>(Y) + (row * N + col) * kE;
       if (whole || (vec && row < M && col + kPer <= N)) {
         __builtin_nontemporal_store(v, reinterpret_cast<gu32x4_t*>(dst));
+      } else if (row < M && col + kPer <= N) {  // rows of any alignment: whole pieces all the same
+        __builtin_memcpy(dst, &v, 16);
       } else if (row < M) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {

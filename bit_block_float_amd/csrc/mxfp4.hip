@@ -12,6 +12,14 @@
 
 namespace hif4 {
 
+// Over lanes l, l ^ 16, l ^ 32 and l ^ 48, by permlane swaps (no LDS permutes).
+__device__ __forceinline__ uint32_t max_rows16(uint32_t v) {
+  auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(p[0], p[1]);
+  p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(p[0], p[1]);
+}
+
 // Along k. One lane owns 16 consecutive elements, two lanes a block; 8 lanes form a
 // word of four scales, which the products read as one.
 template <typename T, int kRows>
@@ -68,8 +76,12 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_tile_kernel(
     }
   }
   Run8<T> v[8];
-  if (begin < end) {
-    const T* src = x + b * rows * ld;
+  const T* src = x + b * rows * ld;
+  if (begin + 128 == end && tk * 128 + 128 <= k) {  // a whole tile
+    src += (begin + rg * 8) * ld + col0;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) load_whole<kRows>(v[r], src + r * ld);
+  } else if (begin < end) {
 #pragma unroll
     for (int r = 0; r < 8; ++r)
       v[r].template load<kRows>(src + min(begin + rg * 8 + r, end - 1) * ld, col0, k);
@@ -80,7 +92,9 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_tile_kernel(
     for (int r = 0; r < 8; ++r) v[r] = Run8<T>{};
   }
   if constexpr (kAlong) {
-    const int64_t row0 = b * rows + begin + rg * 8;
+    const int64_t at = (b * rows + begin + rg * 8) * tiles_k + tk;
+    uint32_t* const c = reinterpret_cast<uint32_t*>(codes + at * 64) + cg;
+    uint32_t* const sc = reinterpret_cast<uint32_t*>(scales) + at;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       uint32_t m = v[r].abs_max();
@@ -89,10 +103,10 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_tile_kernel(
       const uint32_t e = mx4_scale_of(m);
       uint32_t word = or8_u32(e << (8 * (cg >> 2)));
       word |= dpp<0x140>(word);  // row_mirror: over 16 lanes
-      const uint32_t c = mx4_encode(v[r], e);
+      const uint32_t code = mx4_encode(v[r], e);
       if (begin + rg * 8 + r < end) {
-        *reinterpret_cast<uint32_t*>(codes + ((row0 + r) * tiles_k + tk) * 64 + cg * 4) = c;
-        if (cg == 0) *reinterpret_cast<uint32_t*>(scales + ((row0 + r) * tiles_k + tk) * 4) = word;
+        c[(int64_t)r * tiles_k * 16] = code;
+        if (cg == 0) sc[(int64_t)r * tiles_k] = word;
       }
     }
   }
@@ -101,10 +115,7 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_tile_kernel(
     column_max(v, cm);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t m = cm[i];
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-      const uint32_t e = mx4_scale_of(m);
+      const uint32_t e = mx4_scale_of(max_rows16(cm[i]));
       tile[(cg * 8 + i) * kPitch + rg] = mx4_encode_column(v, i, e);
       if (lane < 16) part[(cg * 8 + i) * 4 + wave] = (uint8_t)e;
     }
@@ -131,7 +142,7 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_tile_kernel(
 template <bool kBf16>
 __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(
     const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint32_t runs_per_row,
-    FastDiv run_div, uint32_t total, uint32_t words_per_row, int k, bool vec,
+    FastDiv run_div, uint32_t total, uint32_t words_per_row, int k,
     void* __restrict__ out) {
   const uint32_t it = blockIdx.x * 256u + threadIdx.x;
   if (it >= total) return;
@@ -139,7 +150,8 @@ __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(
   const uint32_t j = it - row * runs_per_row;
   const int64_t at = (int64_t)row * words_per_row + j;
   const uint32_t w = codes[at], e = scales[at >> 2];
-  const float s = e8m0_f32(e);
+  const float s = mx4_scale(e);
+  const uint32_t nan = e == 255u ? 0x7FC07FC0u : 0u;  // or-ed to the values, in either type
   const int64_t off = (int64_t)row * k + j * 8;
   const int valid = k - (int)j * 8;
   if constexpr (kBf16) {
@@ -149,10 +161,10 @@ __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(
         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
         __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = e == 255u ? 0x7FC07FC0u : h[i];
+    for (int i = 0; i < 4; ++i) h[i] |= nan;
     uint16_t* o = reinterpret_cast<uint16_t*>(out) + off;
-    if (vec && valid >= 8) {
-      *reinterpret_cast<uint4*>(o) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (valid >= 8) {  // (whole 16-byte stores at any alignment of the row)
+      __builtin_memcpy(o, h, 16);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -167,11 +179,10 @@ __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(
     v[0] = p0[0], v[1] = p0[1], v[2] = p1[0], v[3] = p1[1];
     v[4] = p2[0], v[5] = p2[1], v[6] = p3[0], v[7] = p3[1];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = e == 255u ? __uint_as_float(0x7FC00000u) : v[i];
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(__float_as_uint(v[i]) | nan);
     float* o = reinterpret_cast<float*>(out) + off;
-    if (vec && valid >= 8) {
-      reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    if (valid >= 8) {
+      __builtin_memcpy(o, v, 32);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -251,7 +262,6 @@ hipError_t hif4_launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* sca
   const uint32_t rpr = (uint32_t)((k + 7) / 8);
   const FastDiv fd = make_fastdiv(rpr);
   const int64_t max_rows = ((int64_t)1 << 30) / rpr;
-  const bool vec = ((uintptr_t)out & 15) == 0 && k % (out_bf16 ? 8 : 4) == 0;
   for (int64_t r0 = 0; r0 < rows; r0 += max_rows) {
     const int64_t nr = rows - r0 < max_rows ? rows - r0 : max_rows;
     const uint32_t total = (uint32_t)(nr * rpr);
@@ -261,10 +271,10 @@ hipError_t hif4_launch_dequantize_mxfp4(const uint8_t* codes, const uint8_t* sca
     const uint8_t* s = scales + r0 * wpr / 4;
     if (out_bf16)
       hipLaunchKernelGGL(dequantize_mxfp4_kernel<true>, grid, block, 0, stream, c, s, rpr, fd, total,
-                         (uint32_t)wpr, (int)k, vec, o);
+                         (uint32_t)wpr, (int)k, o);
     else
       hipLaunchKernelGGL(dequantize_mxfp4_kernel<false>, grid, block, 0, stream, c, s, rpr, fd, total,
-                         (uint32_t)wpr, (int)k, vec, o);
+                         (uint32_t)wpr, (int)k, o);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

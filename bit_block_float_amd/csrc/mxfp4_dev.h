@@ -12,8 +12,12 @@ namespace hif4 {
 // that of amax minus 2, one more where the significand is above 1.5. 255 (E8M0's
 // NaN) if the block holds a NaN or an infinity.
 __device__ __forceinline__ uint32_t mx4_scale_of(uint32_t bits) {
-  const int e = (int)(bits >> 23) - 2 + (int)((bits & 0x7FFFFFu) > 0x400000u);
-  return bits >= 0x7F800000u ? 255u : (uint32_t)max(e, 0);
+  const uint32_t e = max((bits + 0x3FFFFFu) >> 23, 2u) - 2u;  // (carries above 1.5)
+  return bits >= 0x7F800000u ? 255u : e;
+}
+// The scale of a byte below 255 (byte 0 is 2^-127, subnormal in fp32).
+__device__ __forceinline__ float mx4_scale(uint32_t e) {
+  return __uint_as_float(max(e << 23, 0x400000u));
 }
 
 constexpr uint32_t kMx4Nan8 = 0x77777777u;  // the codes of a block whose scale is NaN
@@ -33,7 +37,7 @@ __device__ __forceinline__ uint32_t mx4_pair(uint32_t old, float a, float b, flo
 
 // The 8 codes of a run under the scale byte e: element i in bits 4i .. 4i + 3.
 __device__ __forceinline__ uint32_t mx4_encode(const Run8<uint16_t>& v, uint32_t e) {
-  const float s = e8m0_f32(e);
+  const float s = mx4_scale(e);
   uint32_t r = mx4_pair<0>(0u, v.w.x, s);
   r = mx4_pair<1>(r, v.w.y, s);
   r = mx4_pair<2>(r, v.w.z, s);
@@ -41,7 +45,7 @@ __device__ __forceinline__ uint32_t mx4_encode(const Run8<uint16_t>& v, uint32_t
   return e == 255u ? kMx4Nan8 : r;
 }
 __device__ __forceinline__ uint32_t mx4_encode(const Run8<float>& v, uint32_t e) {
-  const float s = e8m0_f32(e);
+  const float s = mx4_scale(e);
   uint32_t r = mx4_pair<0>(0u, v.v[0], v.v[1], s);
   r = mx4_pair<1>(r, v.v[2], v.v[3], s);
   r = mx4_pair<2>(r, v.v[4], v.v[5], s);
@@ -67,6 +71,19 @@ __device__ __forceinline__ uint32_t mx4_encode_column(const Run8<float> (&v)[8],
 #pragma unroll
   for (int r = 0; r < 8; ++r) c.v[r] = v[r].v[i];
   return mx4_encode(c, e);
+}
+
+// 8 elements that are all there, at an address aligned to 16 bytes (kAligned) or to the
+// element.
+template <int kRows>
+__device__ __forceinline__ void load_whole(Run8<uint16_t>& r, const uint16_t* p) {
+  if constexpr (kRows == kAligned) r.w = *reinterpret_cast<const uint4*>(p);
+  else __builtin_memcpy(&r.w, p, 16);
+}
+template <int kRows>
+__device__ __forceinline__ void load_whole(Run8<float>& r, const float* p) {
+  if constexpr (kRows == kAligned) p = reinterpret_cast<const float*>(__builtin_assume_aligned(p, 16));
+  __builtin_memcpy(r.v, p, 32);
 }
 
 // ---------------------------------------------------------------- groups of rows
