@@ -117,39 +117,52 @@ __device__ __forceinline__ uint32_t lanes_inclusive(uint32_t v) {
   return v;
 }
 __device__ __forceinline__ uint32_t units_of(const Groups& g, int e, int shift) {
-  if (e >= g.count) return 0;
   int64_t begin, end;
   group_range(g, e, begin, end);
   return (uint32_t)((end - begin + (1 << shift) - 1) >> shift);
 }
-__device__ __forceinline__ uint32_t group_units(const Groups& g, int shift) {
-  const int lane = threadIdx.x & 63;
+// (256 groups at a time: the loads of their offsets are in flight together)
+struct Units4 {
+  uint32_t n[4];
+  __device__ __forceinline__ Units4(const Groups& g, int e0, int count, int shift) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int e = e0 + c * 64 + (int)(threadIdx.x & 63);
+      n[c] = units_of(g, min(e, g.count - 1), shift);  // unconditional loads
+      n[c] = e < count ? n[c] : 0u;
+    }
+  }
+};
+__device__ __forceinline__ uint32_t units_before(const Groups& g, int shift, int group) {
   uint32_t sum = 0;
-  for (int e = lane; e < g.count; e += 64) sum += units_of(g, e, shift);
+  for (int e0 = 0; e0 < group; e0 += 256) {
+    const Units4 u(g, e0, group, shift);
+    sum += u.n[0] + u.n[1] + u.n[2] + u.n[3];
+  }
   return (uint32_t)__builtin_amdgcn_readlane((int)lanes_inclusive(sum), 63);
+}
+__device__ __forceinline__ uint32_t group_units(const Groups& g, int shift) {
+  return units_before(g, shift, g.count);
 }
 __device__ __forceinline__ bool group_unit(const Groups& g, int shift, uint32_t t, int& group,
                                            uint32_t& before) {
-  const int lane = threadIdx.x & 63;
   uint32_t sum = 0;
-  for (int e0 = 0; e0 < g.count; e0 += 64) {
-    const uint32_t n = units_of(g, e0 + lane, shift), incl = sum + lanes_inclusive(n);
-    const uint64_t past = __ballot(incl > t);
-    if (past != 0) {
-      const int first = __ffsll((unsigned long long)past) - 1;
-      group = e0 + first;
-      before = (uint32_t)__builtin_amdgcn_readlane((int)(incl - n), first);
-      return true;
+  for (int e0 = 0; e0 < g.count; e0 += 256) {
+    const Units4 u(g, e0, g.count, shift);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t incl = sum + lanes_inclusive(u.n[c]);
+      const uint64_t past = __ballot(incl > t);
+      if (past != 0) {
+        const int first = __ffsll((unsigned long long)past) - 1;
+        group = e0 + c * 64 + first;
+        before = (uint32_t)__builtin_amdgcn_readlane((int)(incl - u.n[c]), first);
+        return before <= t;  // (more only where offsets that do not ascend overflow the sum)
+      }
+      sum = (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
     }
-    sum = (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
   }
   return false;
-}
-__device__ __forceinline__ uint32_t units_before(const Groups& g, int shift, int group) {
-  const int lane = threadIdx.x & 63;
-  uint32_t sum = 0;
-  for (int e = lane; e < group; e += 64) sum += units_of(g, e, shift);
-  return (uint32_t)__builtin_amdgcn_readlane((int)lanes_inclusive(sum), 63);
 }
 
 // Units of 2^shift rows that groups of as many rows can have at most.

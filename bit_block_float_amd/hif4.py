@@ -805,7 +805,7 @@ def _check_mx4(codes, scales, name, dims=2):
 def dequantize_mxfp4(codes, scales, k=None, out_dtype=torch.float32, out=None, stream=None):
     """Values [rows][k] (fp32 or bf16; [experts][rows][k] of such codes) of codes and
     scales; k: the columns before the padding."""
-    *lead, kp = _check_mx4(codes, scales, "the", codes.dim() if codes.dim() in (2, 3) else 2)
+    *lead, kp = _check_mx4(codes, scales, "mxfp4", codes.dim() if codes.dim() in (2, 3) else 2)
     k = kp if k is None else int(k)
     if _up128(k) != kp or k < 0:
         raise ValueError(f"k = {k} does not fit codes of {kp} columns")

@@ -442,3 +442,43 @@ def test_norm_into_mxfp4_strides_and_values(hip):
     codes, scales = hip.layer_norm_quantize_mxfp4(x.cuda())
     v = hip.dequantize_mxfp4(codes, scales, k=1002)
     assert bool(torch.isnan(v[7]).all()) and not torch.isnan(v[:7]).any() and not torch.isnan(v[8:]).any()
+
+
+@pytest.mark.parametrize("offsets", [[0, 300, 100, 260], [-50, 10, 5000, 200], [400, 400, 0, 300], [300, 200, 100, 0],
+                                     [1 << 40, -(1 << 40), 1 << 62, 7]])
+def test_offsets_that_do_not_ascend_stay_within_the_arguments(hip, offsets):
+    """What the results are is not said; what lies before and behind them is left alone."""
+    rows, n, k = 300, 72, 256
+    off = torch.tensor(offsets, device="cuda")
+    x, w = _random(rows, k, 1), _experts(3, n, k, 2)
+    held = torch.full((rows * n + 4096,), 5.0, device="cuda")
+    hip.linear_mxfp4_grouped(*_cuda(x), *_cuda(w), off, y=held[2048:-2048].view(rows, n))
+    codes = torch.full((k * (mx4_ref.columns(rows, 3) // 2) + 4096,), 77, dtype=torch.uint8, device="cuda")
+    v = _x(rows, k, 3).cuda()
+    out = codes[2048:-2048].view(k, -1)
+    _, scales = hip.quantize_mxfp4(v, transposed=True, offsets=off, codes=out)
+    dx, dw = hip.linear_mxfp4_grouped_backward(_x(rows, n, 4).cuda(), out, scales,
+                                               *hip.quantize_mxfp4(torch.ones((3, n, k), device="cuda"), transposed=True),
+                                               off)
+    torch.cuda.synchronize()
+    assert bool((held[:2048] == 5).all()) and bool((held[-2048:] == 5).all())
+    assert bool((codes[:2048] == 77).all()) and bool((codes[-2048:] == 77).all())
+    assert dx.shape == (rows, k) and dw.shape == (3, n, k)
+
+
+def test_many_groups(hip):
+    """More groups than one pass over their offsets takes at once, most of them empty."""
+    g = torch.Generator().manual_seed(5)
+    counts = (torch.rand(1500, generator=g) < 0.1).long() * torch.randint(1, 60, (1500,), generator=g)
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+    rows, n, k = int(off[-1]), 20, 128
+    x, w = _random(rows, k, 1), _random(1500 * n, k, 2)
+    wq = tuple(t.view(1500, n, -1) for t in _cuda(w))
+    y = hip.linear_mxfp4_grouped(*_cuda(x), *wq, off.cuda())
+    wv, xv = mx4_ref.values(*w).view(1500, n, k), mx4_ref.values(*x)
+    expert = torch.repeat_interleave(torch.arange(1500), counts)
+    want = torch.bmm(wv[expert], xv[:, :, None])[:, :, 0]
+    s = torch.bmm(wv[expert].abs(), xv.abs()[:, :, None])[:, :, 0]
+    assert bool(((y.double().cpu() - want).abs() <= mx4_ref.bound(k, s, torch.float32)).all())
+    v = _x(rows, 40, 3)
+    _same(hip.quantize_mxfp4(v.cuda(), transposed=True, offsets=off.cuda()), mx4_ref.spaced(v, off.tolist()).T)
