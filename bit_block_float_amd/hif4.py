@@ -715,6 +715,7 @@ def linear_fp8_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype=N
 MXFP4_BLOCK = 32
 
 
+@functools.lru_cache(maxsize=1024)  # a function of the sizes alone
 def mxfp4_columns(rows, groups=0):
     """Columns of a transpose quantized along its source's rows (in `groups` groups)."""
     return int(lib().hif4_mxfp4_columns(rows, groups))
@@ -727,17 +728,20 @@ def _check_offsets(offsets):
     return offsets.numel() - 1
 
 
-def _mx4_out(lead, rows, length, codes, scales, dev):
-    """Codes [*lead, rows, length up to 128s / 2] and their scales, given or new."""
+_U8, _E8 = torch.uint8, torch.float8_e8m0fnu
+
+
+def _mx4_out(like, lead, rows, length, codes, scales):
+    """Codes [*lead, rows, length up to 128s / 2] and their scales, given or new beside `like`."""
     kp = _up128(length)
     if codes is None:
-        codes = torch.empty((*lead, rows, kp // 2), dtype=torch.uint8, device=dev)
+        codes = like.new_empty((*lead, rows, kp // 2), dtype=_U8)
     else:
-        _check_out(codes, "codes", (*lead, rows, kp // 2), torch.uint8)
+        _check_out(codes, "codes", (*lead, rows, kp // 2), _U8)
     if scales is None:
-        scales = torch.empty((*lead, rows, kp // MXFP4_BLOCK), dtype=torch.float8_e8m0fnu, device=dev)
+        scales = like.new_empty((*lead, rows, kp // MXFP4_BLOCK), dtype=_E8)
     else:
-        _check_out(scales, "scales", (*lead, rows, kp // MXFP4_BLOCK), torch.float8_e8m0fnu)
+        _check_out(scales, "scales", (*lead, rows, kp // MXFP4_BLOCK), _E8)
     return codes, scales
 
 
@@ -768,7 +772,7 @@ def quantize_mxfp4(x, transposed=False, offsets=None, codes=None, scales=None, s
     batch, rows, k, ld, lead, groups = _mx4_x(x, offsets, transposed)
     with _On(x, stream, offsets, codes, scales) as st:
         out = (k, mxfp4_columns(rows, groups)) if transposed else (rows, k)
-        codes, scales = _mx4_out(lead, *out, codes, scales, x.device)
+        codes, scales = _mx4_out(x, lead, *out, codes, scales)
         _ok(lib().hif4_quantize_mxfp4(_at(x), _DTYPE[x.dtype], batch, rows, k, ld, int(bool(transposed)),
                                       _at(offsets), groups, _at(codes), _at(scales), st),
             "hif4_quantize_mxfp4")
@@ -781,8 +785,8 @@ def quantize_mxfp4_both(x, offsets=None, stream=None):
     written."""
     batch, rows, k, ld, lead, groups = _mx4_x(x, offsets, True)
     with _On(x, stream, offsets) as st:
-        codes, scales = _mx4_out(lead, rows, k, None, None, x.device)
-        codes_t, scales_t = _mx4_out(lead, k, mxfp4_columns(rows, groups), None, None, x.device)
+        codes, scales = _mx4_out(x, lead, rows, k, None, None)
+        codes_t, scales_t = _mx4_out(x, lead, k, mxfp4_columns(rows, groups), None, None)
         _ok(lib().hif4_quantize_mxfp4_both(_at(x), _DTYPE[x.dtype], batch, rows, k, ld, _at(offsets), groups,
                                            _at(codes), _at(scales), _at(codes_t), _at(scales_t), st),
             "hif4_quantize_mxfp4_both")
@@ -791,15 +795,15 @@ def quantize_mxfp4_both(x, offsets=None, stream=None):
 
 def _check_mx4(codes, scales, name, dims=2):
     """Codes [..., rows, kp/2] with scales [..., rows, kp/32]: their leading sizes and kp."""
-    if (codes.dtype != torch.uint8 or codes.dim() != dims or not codes.is_contiguous()
-            or codes.shape[-1] % (FP8_BLOCK // 2)):
-        raise ValueError(f"{name}_codes must be a contiguous {dims}-D uint8 tensor, its rows a multiple of 64 "
-                         "bytes (128 codes) long")
-    kp = codes.shape[-1] * 2
-    want = (*codes.shape[:-1], kp // MXFP4_BLOCK)
-    if scales.dtype != torch.float8_e8m0fnu or tuple(scales.shape) != want or not scales.is_contiguous():
-        raise ValueError(f"{name}_scales must be a contiguous float8_e8m0fnu tensor of shape {want}")
-    return *codes.shape[:-1], kp
+    *lead, half = codes.shape
+    *lead_s, blocks = scales.shape
+    if (codes.dtype is _U8 and scales.dtype is _E8 and half == 16 * blocks and half % 64 == 0
+            and lead == lead_s and len(lead) == dims - 1 and codes.is_contiguous() and scales.is_contiguous()):
+        return *lead, 2 * half
+    raise ValueError(f"{name}_codes must be a contiguous {dims}-D uint8 tensor, its rows a multiple of 64 bytes (128 "
+                     f"codes) long, and {name}_scales a contiguous float8_e8m0fnu tensor of the same rows, a byte for "
+                     f"each 16 of codes; they are {codes.dtype} {tuple(codes.shape)} and {scales.dtype} "
+                     f"{tuple(scales.shape)}")
 
 
 def dequantize_mxfp4(codes, scales, k=None, out_dtype=torch.float32, out=None, stream=None):
@@ -813,7 +817,7 @@ def dequantize_mxfp4(codes, scales, k=None, out_dtype=torch.float32, out=None, s
         raise ValueError("out_dtype must be float32 or bfloat16")
     with _On(codes, stream, scales, out) as st:
         if out is None:
-            out = torch.empty((*lead, k), dtype=out_dtype, device=codes.device)
+            out = codes.new_empty((*lead, k), dtype=out_dtype)
         else:
             _check_out(out, "out", (*lead, k), out_dtype)
         rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
@@ -827,11 +831,11 @@ def linear_mxfp4_workspace_bytes(m, n, k):
     return int(lib().hif4_linear_mxfp4_workspace_bytes(m, n, k))
 
 
-def _y_out(y, m, n, y_dtype, dev):
+def _y_out(like, y, m, n, y_dtype):
     if y_dtype not in _DTYPE:
         raise ValueError("y_dtype must be float32 or bfloat16")
     if y is None:
-        return torch.empty((m, n), dtype=y_dtype, device=dev)
+        return like.new_empty((m, n), dtype=y_dtype)
     _check_out(y, "y", (m, n), y_dtype)
     return y
 
@@ -845,7 +849,7 @@ def linear_mxfp4(x_codes, x_scales, w_codes, w_scales, y_dtype=torch.float32, y=
     if kw != k:
         raise ValueError(f"x has {k} columns, w {kw}")
     with _On(x_codes, stream, x_scales, w_codes, w_scales, y, workspace) as st:
-        y = _y_out(y, m, n, y_dtype, x_codes.device)
+        y = _y_out(x_codes, y, m, n, y_dtype)
         need = linear_mxfp4_workspace_bytes(m, n, k)
         if workspace is None and need:
             workspace = torch.empty((need,), dtype=torch.uint8, device=x_codes.device)
@@ -867,7 +871,7 @@ def linear_mxfp4_grouped(x_codes, x_scales, w_codes, w_scales, offsets, y_dtype=
     if kw != k or experts != groups:
         raise ValueError(f"x has {k} columns and offsets {groups} groups, w {kw} columns and {experts} experts")
     with _On(x_codes, stream, x_scales, w_codes, w_scales, offsets, y) as st:
-        y = _y_out(y, m, n, y_dtype, x_codes.device)
+        y = _y_out(x_codes, y, m, n, y_dtype)
         _ok(lib().hif4_linear_mxfp4_grouped(_at(x_codes), _at(x_scales), _at(w_codes), _at(w_scales),
                                             _at(offsets), groups, m, n, k, _at(y), _DTYPE[y_dtype], st),
             "hif4_linear_mxfp4_grouped")
@@ -904,11 +908,10 @@ def linear_mxfp4_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype
         raise ValueError(f"dy is {m} x {n}: xt must be [k][{_up128(m)}], wt [k][{_up128(n)}]")
     dx_dtype = _mx4_gradient_types(dy, dx_dtype, dw_dtype)
     with _On(dy, stream, xt_codes, xt_scales, wt_codes, wt_scales, workspace) as st:
-        dx = torch.empty((m, k), dtype=dx_dtype, device=dy.device)
-        dw = torch.empty((n, k), dtype=dw_dtype, device=dy.device)
+        dx = dy.new_empty((m, k), dtype=dx_dtype)
+        dw = dy.new_empty((n, k), dtype=dw_dtype)
         if workspace is None:
-            workspace = torch.empty((linear_mxfp4_backward_workspace_bytes(m, n, k),), dtype=torch.uint8,
-                                    device=dy.device)
+            workspace = dy.new_empty((linear_mxfp4_backward_workspace_bytes(m, n, k),), dtype=_U8)
         _ok(lib().hif4_linear_mxfp4_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt_codes),
                                              _at(xt_scales), _at(wt_codes), _at(wt_scales), m, n, k,
                                              _at(dx), _DTYPE[dx_dtype], _at(dw), _DTYPE[dw_dtype],
@@ -935,11 +938,11 @@ def linear_mxfp4_grouped_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, 
                          f"[{_up128(n)}]")
     dx_dtype = _mx4_gradient_types(dy, dx_dtype, dw_dtype)
     with _On(dy, stream, xt_codes, xt_scales, wt_codes, wt_scales, offsets, workspace) as st:
-        dx = torch.empty((m, k), dtype=dx_dtype, device=dy.device)
-        dw = torch.empty((groups, n, k), dtype=dw_dtype, device=dy.device)
+        dx = dy.new_empty((m, k), dtype=dx_dtype)
+        dw = dy.new_empty((groups, n, k), dtype=dw_dtype)
         if workspace is None:
             need = linear_mxfp4_grouped_backward_workspace_bytes(groups, m, n, k)
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dy.device)
+            workspace = dy.new_empty((need,), dtype=_U8)
         _ok(lib().hif4_linear_mxfp4_grouped_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt_codes),
                                                      _at(xt_scales), _at(wt_codes), _at(wt_scales),
                                                      _at(offsets), groups, m, n, k, _at(dx),
@@ -1036,7 +1039,7 @@ def layer_norm_quantize_mxfp4(x, weight=None, bias=None, eps=1e-6, codes=None, s
     rows, c = x.shape
     wd = _check_affine(weight, bias, c)
     with _On(x, stream, weight, bias, codes, scales) as st:
-        codes, scales = _mx4_out((), rows, c, codes, scales, x.device)
+        codes, scales = _mx4_out(x, (), rows, c, codes, scales)
         _ok(lib().hif4_layer_norm_quantize_mxfp4(_at(x), _DTYPE[x.dtype], rows, c, _ld(x), _at(weight),
                                                  _at(bias), wd, float(eps), _at(codes), _at(scales), st),
             "hif4_layer_norm_quantize_mxfp4")
