@@ -139,6 +139,11 @@ struct Mx4Buffers {
 // Part `split`: stages [split per_split, (split + 1) per_split) only, the sums to that
 // plane of Y as float32 (few tiles and a long K: the parts are added by
 // mx4_reduce_kernel in order).
+//
+// Bound: what the tiles read through L2 (128 x 128: 136 bytes for 32768 operations), and with one or two tiles a CU the latency of their stages in turn. Two
+// workgroups a CU: one multiplies while the other waits or stores. 512 x 13824 x 5120 29
+// us (2.5 PFLOP/s), 4096 x 4096 x 512 12.2 (1.4); 64 x 64: 32 x 5120 x 5120 8.5 us, both
+// gradients of 1001 x 1300 x 640 6.3 to 7.3.
 template <int BM, int BN, int kStages>
 constexpr int kMx4Lds = kStages * (BM + BN) * (128 + 16) + 1024;  // stages, a sink for idle scale loads
 template <int BM, int BN, int kWM, int kWN, int kStages>
@@ -282,8 +287,8 @@ __global__ __launch_bounds__(kWM* kWN * 64) void mx4_tile_kernel(Mx4Args a, Mx4A
 // stage, and stage kb + 2 goes out into it by direct-to-LDS loads while run 1 multiplies
 // and run 0 of stage kb + 1 is read. Stages past the end load the last one again, into
 // one that no one reads. Where the last stage has one run only, the other's codes are
-// loaded as zeros (from beyond the buffers) and its scales taken as 1: an exit between
-// the runs, or a copy of run 0 behind the loop, made the compiler spill.
+// loaded as zeros (from beyond the buffers) and its scales taken as 1: with an exit
+// between the runs, or a copy of run 0 behind the loop, as tried, the compiler spilled.
 //
 // Scales come 32 bytes a row, four stages' worth, into a ring of two, one load a stage,
 // whose target is chosen without a branch (a branch in the loop lets the compiler move
@@ -292,11 +297,12 @@ __global__ __launch_bounds__(kWM* kWN * 64) void mx4_tile_kernel(Mx4Args a, Mx4A
 // the codes and cost 5%, these half of that.
 //
 // Bound: the matrix cores at the clock that power allows, and a tile's ends. Measured on
-// 57600 x 13824 x 5120, bf16 Y: 2.02 ms (4.0 PFLOP/s); the products alone, from registers,
-// 1.40 ms (5.8, at 1.55 GHz), without stores 1.80, without loads 1.76, without LDS reads
-// 1.88. Loads spread over a whole stage, fragments of half a run, rows of 64 bytes in four
-// slots with twice the time to land, and one barrier more a stage for earlier loads gave
-// nothing or less.
+// 57600 x 13824 x 5120, bf16 Y: 1.93 to 2.0 ms (4.1 PFLOP/s); the products alone, from
+// registers, 1.40 ms (5.8, at 1.55 GHz). When it took 2.02 ms, it took 1.80 without stores,
+// 1.76 without loads, 1.88 without LDS reads. Loads spread over a whole stage, fragments of
+// half a run, rows of 64 bytes in four slots with twice the time to land, one barrier more a
+// stage for earlier loads, and a start of XCDs or CUs at different times (so that not all
+// store at once) gave nothing or less.
 constexpr int kMx4BigSlot = 2 * 256 * 128;
 constexpr int kMx4BigRing = 2 * 256 * 32;
 constexpr int kMx4BigLds = 2 * kMx4BigSlot + 2 * kMx4BigRing;
@@ -462,7 +468,8 @@ void mx4_big_kernel(Mx4Args a, Mx4Args b, uint32_t first) {
   mx4_big(second ? b : a, blockIdx.x - (second ? first : 0u), lds);
 }
 
-// Y = sum of `splits` float32 planes, in order; 4 elements a thread.
+// Y = sum of `splits` float32 planes, in order; 4 elements a thread. Bound: the planes,
+// fresh in the caches, and a launch (64 x 5120 in 6: some 4 us of the call's 16.6).
 template <bool kBf16>
 __global__ __launch_bounds__(256) void mx4_reduce_kernel(const float* __restrict__ parts, int splits,
                                                          int64_t total, void* __restrict__ Y) {
@@ -495,6 +502,9 @@ __global__ __launch_bounds__(256) void mx4_reduce_kernel(const float* __restrict
 // (A scale word a run, the first way, was as many cache lines again as W itself: one
 // row of 13824 x 5120 17.0 us.) Rows past the last or columns past the workgroup's
 // repeat the last one and are not stored.
+// Measured, one row of 13824 x 5120 (37.6 MB) 8.4 to 9.3 us, 4.0 to 4.5 TB/s with launch
+// and the first latency; 96 rows over 32 groups of 5120 x 2048 29 to 33 us, 5.4 to 6.1 TB/s
+// of all weights (178 MB, some groups empty, part of W in the 256 MB cache).
 template <int kR, int kQuads>
 __global__ __launch_bounds__(512) void mx4_skinny_kernel(Mx4Args a, int cols, int parts) {
   __shared__ gf32x4_t sums[8][kR][64];
@@ -608,16 +618,17 @@ static int64_t tiles_in(int64_t v, int64_t tile) { return (v + tile - 1) / tile;
 //   32 x 2048 x 2048           4.1           5.3        8.2
 //   32 x 5120 x 5120           9.5           8.5       15
 //   128 x 13824 x 5120                      17         19.6
-//   256 x 13824 x 5120                      27         21
-//   512 x 5120 x 5120                       21         16         31
-//   512 x 13824 x 5120                      49         30         33
-//   1024 x 5120 x 5120                      37         27         33
-//   1024 x 13824 x 5120                     94         57         43
-//   2048 x 5120 x 5120                      69         45         35
-//   4096 x 4096 x 512                       24         12.2       13.4
-//   4096 x 4096 x 2048                      44         25.4       24.8
-//   8192 x 8192 x 256                                  34         43
-//   8192 x 8192 x 1024                     112         66         62
+//   256 x 13824 x 5120                      29         21          31
+//   512 x 5120 x 5120                       22         16          31
+//   512 x 13824 x 5120                      49         29          32
+//   1024 x 5120 x 5120                      38         28          31
+//   1024 x 13824 x 5120                     93         56          39
+//   2048 x 5120 x 5120                      69         46          33
+//   4096 x 4096 x 512                       23         12.2        12.5
+//   4096 x 4096 x 2048                      45         26.6        22.7
+//   8192 x 8192 x 256                       77         34          39
+//   8192 x 8192 x 512                       87         43          46
+//   8192 x 8192 x 1024                     112         79          61
 // A round of 256 tiles of 256 x 256 costs 4/3 of one of 512 tiles of 128 x 128, from
 // some four stages on (below, its ends count, which nothing else on the CU hides).
 // Splitting K pays for its second kernel from some 16 stages a part: 64 x 5120 x 5120
@@ -644,11 +655,11 @@ static Mx4Plan plan_mx4(int64_t m, int64_t n, int64_t k) {
 //   32 x 8 x 5120 x 2048        45         43         43
 //   8 x 16 x 5120 x 5120        38         34         38
 //   32 x 16 x 5120 x 2048       58         49         45
-//   32 x 64 x 5120 x 2048      142         67         51          71
-//   128 x 256 x 2048 x 1024               201        102         118
-//   32 x 256 x 5120 x 2048                174         98          99
-//   8 x 512 x 5120 x 5120                 199        109          86
-//   32 x 1024 x 5120 x 2048               570        302         280
+//   32 x 64 x 5120 x 2048      142         69         50          64
+//   128 x 256 x 2048 x 1024               197         97         101
+//   32 x 256 x 5120 x 2048                176         97          89
+//   8 x 512 x 5120 x 5120                 200        108          82
+//   32 x 1024 x 5120 x 2048               571        305         265
 // (units of 16 rows instead of 32, 32 x 3 x 5120 x 2048: 35.5: W is read again for the
 // second half of a group of more.)
 static Mx4Plan plan_of(const Mx4Product& p) {
@@ -668,10 +679,11 @@ static Mx4Plan plan_of(const Mx4Product& p) {
                        4 * tiles_in(tiles(256), kMx4Cus) < 3 * tiles_in(tiles(128), 2 * kMx4Cus);
     return {large ? kMx4Large : kMx4Middle, 1, all};
   }
-  // K in groups, groups x mean x m x n, fp32 Y, 128 x 128 and 256 x 256: 32 x 64 x 2048 x
-  // 2048 104 and 114 (Y's bytes 103), 16 x 256 x 2048 x 5120 135 and 145 (129), 16 x 1024 x
-  // 2048 x 5120 233 and 195, 8 x 2048 x 2048 x 5120 190 and 149, 4 x 512 x 1024 x 1024 7 and
-  // 13 (64 x 64: 10).
+  // K in groups, groups x mean x m x n, us with 128 x 128 and 256 x 256, fp32 Y (bf16): 32 x 64
+  // x 2048 x 2048 106 and 110 (83 and 81; Y's bytes 103 and 52), 16 x 256 x 2048 x 5120 134 and
+  // 144 (107 and 107; 129 and 65), 16 x 512 x 2048 x 5120 162 and 162 (137 and 126), 16 x 1024 x
+  // 2048 x 5120 230 and 194 (205 and 167), 8 x 2048 x 2048 x 5120 187 and 143 (173 and 131), 4 x
+  // 512 x 1024 x 1024 7 and 14 (64 x 64: 10).
   const int64_t t256 = p.groups.count * tiles_in(p.m, 256) * tiles_in(p.n, 256);
   if (t256 >= kMx4Cus && p.groups.rows / p.groups.count >= 512) return {kMx4Large, 1, all};
   return {p.groups.count * tiles_in(p.m, 128) * tiles_in(p.n, 128) >= kMx4Cus / 2 ? kMx4Middle : kMx4Small, 1, all};

@@ -21,7 +21,9 @@ __device__ __forceinline__ uint32_t max_rows16(uint32_t v) {
 }
 
 // Along k. One lane owns 16 consecutive elements, two lanes a block; 8 lanes form a
-// word of four scales, which the products read as one.
+// word of four scales, which the products read as one. One item a thread, all of a
+// launch's reads independent: 57600 x 5120 bf16 126 to 150 us from box to box (5.0 to
+// 5.9 TB/s; a copy 5.0 to 5.2).
 template <typename T, int kRows>
 __global__ __launch_bounds__(256) void quantize_mxfp4_rows_kernel(
     const T* __restrict__ x, int64_t ld, int k, uint32_t items_per_row, FastDiv item_div,
@@ -45,7 +47,10 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_rows_kernel(
 // One tile of 128 rows x 128 columns a workgroup; the rows are those of a unit (128
 // rows, or what is left of their group). Thread t holds rows 8 (t / 16) .. + 7 of
 // columns 8 (t % 16) .. + 7, so a wave holds a block's 32 rows of 128 columns. The
-// transposed codes go through LDS to leave as runs of 64 bytes.
+// transposed codes go through LDS to leave as runs of 64 bytes, half a line, which the
+// L2 joins for most (16384 x 2048: 46 MB reach memory of 38). Measured, both ways: 8192 x
+// 5120 bf16 31 to 33 us (4.0 TB/s), 16384 x 2048 in 16 groups 26 to 28; along the rows
+// only, 4099 x 1300 fp32 in 7 groups 9.2, 418 workgroups of one latency.
 //  kAlong: codes [rows][ceil(k/128)*64], scales [rows][ceil(k/128)*4].
 //  kCols: codes_t [k][units*64], scales_t [k][units*4] of batch number blockIdx.y.
 //  unit0: the launch's first unit; units behind the last group are written as zeros.
@@ -138,7 +143,9 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_tile_kernel(
 }
 
 // Codes back to values: 8 elements a thread, exact in either type (a value beyond the
-// type's range becomes infinite). Bound: HBM, 1/2 + 1/32 bytes in and 2 or 4 out.
+// type's range becomes infinite). Bound: HBM, 1/2 + 1/32 bytes in and 2 or 4 out:
+// 57600 x 5120 to bf16 123 to 128 us (5.9 TB/s). A NaN scale is or-ed in: a select with
+// branches took 5% more.
 template <bool kBf16>
 __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(
     const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint32_t runs_per_row,
