@@ -177,8 +177,8 @@ def _near(y, xv, wv, parts=64):
     assert bool((err <= tol).all()), (tuple(y.shape), y.dtype, float((err / tol).max()))
 
 
-# every kernel: up to 16 rows, 64-row tiles whole and with K split, 128-row tiles by eight and by
-# four waves, 256-row tiles; depths of one run, an odd and an even count of them
+# up to 16 and 32 rows, tiles of 64 x 64 whole and with K split, of 128 x 128; depths of one run, an
+# odd and an even count of them (sizes for every kernel, tiles of 256 x 256 among them: mx4_cases.py)
 LINEAR = [(1, 1, 128), (1, 13, 384), (3, 96, 5120), (16, 41, 2176), (17, 41, 128), (70, 96, 512), (300, 96, 5120),
           (301, 97, 4224), (129, 257, 13824), (1408, 1536, 256), (1409, 1535, 384), (2176, 2304, 256), (2049, 2305, 640),
           (2048, 9000, 256), (4097, 4099, 384), (5120, 8192, 128)]
