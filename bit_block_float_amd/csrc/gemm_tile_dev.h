@@ -122,6 +122,11 @@ __device__ __forceinline__ void store_tile(gf32x16_t (&acc)[kTN][kTM], char* sta
           }
         }
       }
+    } else if (vec && row0 + 32 * kTM <= M) {  // whole: no branch a store, which would wait for its read alone
+      // (57600 x 13824 x 5120, bf16 Y: in E4M3 3009 us without this case, 2989 with it; in MXFP4 1945, 1928)
+#pragma unroll
+      for (int p = 0; p < 32 / kRows; ++p, dst += step)
+        __builtin_nontemporal_store(piece(p), reinterpret_cast<gu32x4_t*>(dst));
     } else if (vec) {
 #pragma unroll
       for (int p = 0; p < 32 / kRows; ++p, dst += step) {
