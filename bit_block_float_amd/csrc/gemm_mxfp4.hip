@@ -773,17 +773,32 @@ hipError_t hif4_launch_gemm_mxfp4(const Mx4Product& p, void* workspace, hipStrea
   return hipGetLastError();
 }
 
-// Two independent products, in one launch where both take the same tile kernel whole, or
-// both are small (64 x 64 tiles cost little more than the kernel for few rows, a second
-// launch some 4 us), or as tiles of 128 x 128 fill the CUs once (1001 x 1300 x 640 in 5
-// groups: 11.4 us, apart 14.8).
+// Two independent products, in one launch where both take the same tile kernel whole. Where
+// they do not, but both are small (64 x 64 tiles cost little more than the kernel for few
+// rows, a second launch some 4 us), or as tiles of 128 x 128 fill the CUs once, they share
+// one up to a depth of 8 stages each: beyond, a tile's way along K costs more than the
+// launch. Both gradients with dY's quantization, us, in one launch and apart, by the depth
+// of dX (n / 256; at 8 stages one launch gains 2 us and loses 0.8 at its worst):
+//   m x n x k                       one     apart
+//   16 x 1024 x 640, 4 stages       9.9     12.3
+//   16 x 2048 x 640, 8             11.5     13.1
+//   16 x 4096 x 640, 16            18.1     14.9
+//   16 x 13824 x 64, 54            22.1     16.3
+//   128 x 2048 x 1024, 8           13.8     15.5
+//   128 x 4096 x 1024, 16          21.0     18.6
+//   128 x 7680 x 1024, 30          31.9     26.0
+//   1001 x 1300 x 640 in 5 groups  11.4     14.8 (the products alone)
 hipError_t hif4_launch_gemm_mxfp4_two(const Mx4Product& a, const Mx4Product& b, void* workspace,
                                       hipStream_t stream) {
   const Mx4Plan pa = plan_of(a), pb = plan_of(b);
-  const bool small = pa.kind <= kMx4Small && pb.kind <= kMx4Small;
-  const bool once = pa.kind <= kMx4Middle && pb.kind <= kMx4Middle &&
+  const auto shallow = [](const Mx4Product& p) {  // (a group of K: in the mean)
+    return tiles_in(p.mode == kMx4Depth ? p.k / p.groups.count : p.k, 256) <= 8;
+  };
+  const bool both = shallow(a) && shallow(b), same = pa.kind == pb.kind && pa.kind >= kMx4Small;
+  const bool small = both && pa.kind <= kMx4Small && pb.kind <= kMx4Small;
+  const bool once = both && pa.kind <= kMx4Middle && pb.kind <= kMx4Middle &&
                     mx4_tiles(mx4_args(a, 128)) + mx4_tiles(mx4_args(b, 128)) <= 2 * (uint64_t)kMx4Cus;
-  if ((pa.kind == pb.kind || small || once) && pa.splits == 1 && pb.splits == 1) {
+  if ((same || small || once) && pa.splits == 1 && pb.splits == 1) {
     const Mx4Kind kind = small ? kMx4Small : once ? kMx4Middle : pa.kind;
     const Mx4Args ga = mx4_args(a, mx4_tile_rows(kind)), gb = mx4_args(b, mx4_tile_rows(kind));
     const int most = pa.per_split > pb.per_split ? pa.per_split : pb.per_split;

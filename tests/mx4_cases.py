@@ -47,6 +47,10 @@ BACKWARD = [
     ((T256,), 2945, 2945, 2947, 3),                   # both in one launch
     ((T256,), 2945, 2945, 2947, 1), ((T256,), 2945, 2945, 2947, 2),
     ((T128,), 1200, 1290, 1410, 3), ((T64,), 200, 300, 130, 3),
+    # apart, as dX (dW) is deep for a kernel that is not its own
+    ((T128, SKINNY32), 20, 12000, 333, 3), ((T64, SKINNY16), 16, 13824, 64, 3), ((SKINNY16, T64), 4000, 16, 320, 3),
+    ((T128, T64), 128, 7680, 1024, 3),
+    ((T64,), 16, 2048, 640, 3), ((T128,), 128, 2048, 1024, 3),  # in one launch, as neither is
     ((SKINNY32,), 20, 12000, 333, 1), ((T64, SPLIT), 200, 9001, 130, 1), ((T64, SPLIT), 9001, 200, 130, 2),
     ((T64,), 70, 300, 130, 2), ((SKINNY16,), 9, 700, 333, 1),
 ]
@@ -58,7 +62,9 @@ GROUPED_BACKWARD = [
     ((T256,), 1100, [0, 100, 1100], 2900, 2818, 2),   # a group of one run
     ((T128,), 800, _UNEVEN, 1031, 2049, 3), ((T128,), 800, _UNEVEN, 1031, 2049, 1),
     ((T128,), 800, _UNEVEN, 640, 650, 2), ((T64,), 300, [0, 200, 200, 299], 130, 70, 2),
-    ((T64,), 300, [0, 200, 200, 299], 130, 70, 1), ((SKINNY32,), 30, [0, 17, 17, 18, 18, 30], 5000, 41, 1),
+    ((T64,), 300, [0, 200, 200, 299], 130, 70, 1),
+    ((T128, SKINNY32), 30, [0, 17, 17, 18, 18, 30], 5000, 41, 3), ((T64,), 30, [0, 17, 17, 18, 18, 30], 600, 300, 3),
+    ((SKINNY32,), 30, [0, 17, 17, 18, 18, 30], 5000, 41, 1),
 ]
 
 
