@@ -896,57 +896,77 @@ def _mx4_gradient_types(dy, dx_dtype, dw_dtype):
 
 
 def linear_mxfp4_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, dx_dtype=None,
-                          dw_dtype=torch.float32, workspace=None, stream=None):
+                          dw_dtype=torch.float32, workspace=None, stream=None, need_dx=True, need_dw=True):
     """Gradients of Y = X W^T through the quantizers (taken as the identity): dX [m][k] =
     Q(dY) W and dW [n][k] = Q(dY^T) X for dy [m][n] (bf16 or fp32), with X^T and W^T
     quantized along m and n (quantize_mxfp4(..., transposed=True)). dX is of dy's type
-    unless dx_dtype says otherwise."""
+    unless dx_dtype says otherwise. A gradient that is not needed is None and costs
+    nothing; without dX wt_codes and wt_scales may be None, without dW xt_codes and
+    xt_scales."""
     _check_rows(dy, "dy")
-    (m, n), (k, mp) = dy.shape, _check_mx4(xt_codes, xt_scales, "xt")
-    kw, np_ = _check_mx4(wt_codes, wt_scales, "wt")
-    if kw != k or mp != _up128(m) or np_ != _up128(n):
+    if not (need_dx or need_dw):
+        raise ValueError("one of need_dx and need_dw has to be set")
+    m, n = dy.shape
+    k = mp = np_ = None
+    if need_dw:
+        k, mp = _check_mx4(xt_codes, xt_scales, "xt")
+    if need_dx:
+        kw, np_ = _check_mx4(wt_codes, wt_scales, "wt")
+        k = kw if k is None else k
+    if (need_dx and (kw != k or np_ != _up128(n))) or (need_dw and mp != _up128(m)):
         raise ValueError(f"dy is {m} x {n}: xt must be [k][{_up128(m)}], wt [k][{_up128(n)}]")
     dx_dtype = _mx4_gradient_types(dy, dx_dtype, dw_dtype)
-    with _On(dy, stream, xt_codes, xt_scales, wt_codes, wt_scales, workspace) as st:
-        dx = dy.new_empty((m, k), dtype=dx_dtype)
-        dw = dy.new_empty((n, k), dtype=dw_dtype)
+    xt = (xt_codes, xt_scales) if need_dw else (None, None)
+    wt = (wt_codes, wt_scales) if need_dx else (None, None)
+    with _On(dy, stream, *xt, *wt, workspace) as st:
+        dx = dy.new_empty((m, k), dtype=dx_dtype) if need_dx else None
+        dw = dy.new_empty((n, k), dtype=dw_dtype) if need_dw else None
         if workspace is None:
             workspace = dy.new_empty((linear_mxfp4_backward_workspace_bytes(m, n, k),), dtype=_U8)
-        _ok(lib().hif4_linear_mxfp4_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt_codes),
-                                             _at(xt_scales), _at(wt_codes), _at(wt_scales), m, n, k,
-                                             _at(dx), _DTYPE[dx_dtype], _at(dw), _DTYPE[dw_dtype],
-                                             _at(workspace), _workspace_bytes(workspace), st),
+        _ok(lib().hif4_linear_mxfp4_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt[0]), _at(xt[1]),
+                                             _at(wt[0]), _at(wt[1]), m, n, k, _at(dx), _DTYPE[dx_dtype],
+                                             _at(dw), _DTYPE[dw_dtype], _at(workspace),
+                                             _workspace_bytes(workspace), st),
             "hif4_linear_mxfp4_backward")
     return dx, dw
 
 
 def linear_mxfp4_grouped_backward(dy, xt_codes, xt_scales, wt_codes, wt_scales, offsets, dx_dtype=None,
-                                  dw_dtype=torch.float32, workspace=None, stream=None):
+                                  dw_dtype=torch.float32, workspace=None, stream=None, need_dx=True,
+                                  need_dw=True):
     """Gradients of linear_mxfp4_grouped: dX [m][k], dX[i] = Q(dY)[i] W[e] for the rows i
     of each group e, and dW [experts][n][k], dW[e] = Q(dY_e^T) X_e (0 for a group without
     rows), for dy [m][n], with X^T quantized along each group's rows
     (quantize_mxfp4(x, transposed=True, offsets=offsets)) and the experts' W^T along n
     (quantize_mxfp4(w, transposed=True)). Rows of dX outside every group are not
-    written."""
+    written. need_dx and need_dw as for linear_mxfp4_backward."""
     _check_rows(dy, "dy")
-    (m, n), (k, mp) = dy.shape, _check_mx4(xt_codes, xt_scales, "xt")
-    experts, kw, np_ = _check_mx4(wt_codes, wt_scales, "wt", 3)
+    if not (need_dx or need_dw):
+        raise ValueError("one of need_dx and need_dw has to be set")
+    m, n = dy.shape
     groups = _check_offsets(offsets)
     want = mxfp4_columns(m, groups) if groups else 0
-    if kw != k or experts != groups or mp != want or np_ != _up128(n):
+    k = mp = None
+    if need_dw:
+        k, mp = _check_mx4(xt_codes, xt_scales, "xt")
+    if need_dx:
+        experts, kw, np_ = _check_mx4(wt_codes, wt_scales, "wt", 3)
+        k = kw if k is None else k
+    if (need_dx and (kw != k or experts != groups or np_ != _up128(n))) or (need_dw and mp != want):
         raise ValueError(f"dy is {m} x {n} in {groups} groups: xt must be [k][{want}], wt [{groups}][k]"
                          f"[{_up128(n)}]")
     dx_dtype = _mx4_gradient_types(dy, dx_dtype, dw_dtype)
-    with _On(dy, stream, xt_codes, xt_scales, wt_codes, wt_scales, offsets, workspace) as st:
-        dx = dy.new_empty((m, k), dtype=dx_dtype)
-        dw = dy.new_empty((groups, n, k), dtype=dw_dtype)
+    xt = (xt_codes, xt_scales) if need_dw else (None, None)
+    wt = (wt_codes, wt_scales) if need_dx else (None, None)
+    with _On(dy, stream, *xt, *wt, offsets, workspace) as st:
+        dx = dy.new_empty((m, k), dtype=dx_dtype) if need_dx else None
+        dw = dy.new_empty((groups, n, k), dtype=dw_dtype) if need_dw else None
         if workspace is None:
             need = linear_mxfp4_grouped_backward_workspace_bytes(groups, m, n, k)
             workspace = dy.new_empty((need,), dtype=_U8)
-        _ok(lib().hif4_linear_mxfp4_grouped_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt_codes),
-                                                     _at(xt_scales), _at(wt_codes), _at(wt_scales),
-                                                     _at(offsets), groups, m, n, k, _at(dx),
-                                                     _DTYPE[dx_dtype], _at(dw), _DTYPE[dw_dtype],
+        _ok(lib().hif4_linear_mxfp4_grouped_backward(_at(dy), _DTYPE[dy.dtype], _ld(dy), _at(xt[0]), _at(xt[1]),
+                                                     _at(wt[0]), _at(wt[1]), _at(offsets), groups, m, n, k,
+                                                     _at(dx), _DTYPE[dx_dtype], _at(dw), _DTYPE[dw_dtype],
                                                      _at(workspace), _workspace_bytes(workspace), st),
             "hif4_linear_mxfp4_grouped_backward")
     return dx, dw

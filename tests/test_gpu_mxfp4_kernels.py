@@ -264,3 +264,24 @@ def test_grouped_backward(hip, case, dtype):
                 assert not dw.any()
     if which & 1:
         assert bool((got.dx.y[:offsets[0]] == 3).all()) and bool((got.dx.y[offsets[-1]:] == 3).all())
+
+
+@pytest.mark.parametrize("groups", [False, True])
+def test_one_gradient_by_the_binding(hip, groups):
+    """The gradient that is asked for, as the C entry point gives it, without the other's operands."""
+    m, n, k = 300, 333, 200
+    off = torch.tensor([3, 100, 100, 299], device="cuda") if groups else None
+    dy = torch.nn.functional.pad(_x(m, n, 1, torch.bfloat16), (2, 3)).cuda()[:, 2:2 + n]  # rows of its own stride
+    xt = hip.quantize_mxfp4(_x(m, k, 2, torch.bfloat16).cuda(), transposed=True, offsets=off)
+    w = torch.stack([_x(n, k, 3 + e, torch.float32, 0.2) for e in range(3)]).cuda()
+    wt = hip.quantize_mxfp4(w if groups else w[0], transposed=True)
+    call = hip.linear_mxfp4_grouped_backward if groups else hip.linear_mxfp4_backward
+    tail = (off,) if groups else ()
+    rows = slice(3, 299) if groups else slice(0, m)
+    dx, dw = call(dy, None, None, *wt, *tail, need_dw=False)
+    assert dw is None and torch.equal(dx[rows], _C(hip, dy, xt, wt, n, k, 1, off).dx.y[rows])
+    dx, dw = call(dy, *xt, None, None, *tail, dw_dtype=torch.float32, need_dx=False)
+    assert dx is None and torch.equal(dw.flatten(0, -2), _C(hip, dy, xt, wt, n, k, 2, off).dw.y)
+    both = call(dy, *xt, *wt, *tail)
+    want = _C(hip, dy, xt, wt, n, k, 3, off)
+    assert torch.equal(both[0][rows], want.dx.y[rows]) and torch.equal(both[1].flatten(0, -2), want.dw.y)

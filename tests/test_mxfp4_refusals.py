@@ -183,3 +183,27 @@ def test_binding_checks_shapes_before_the_library():
     raises(hif4.linear_mxfp4_grouped_backward, dy, c(6, 64), s(6, 4), c(3, 6, 64), s(3, 6, 4), off)  # 3 x 128 columns
     raises(hif4.linear_mxfp4_grouped_backward, dy, c(6, 192), s(6, 12), c(2, 6, 64), s(2, 6, 4), off)
     raises(hif4.layer_norm_quantize_mxfp4, torch.empty((4, 8)), weight=torch.empty(7))
+
+
+def test_one_gradient_checks_what_it_needs():
+    from bit_block_float_amd import hif4
+    e8 = torch.float8_e8m0fnu
+    c = lambda *s: torch.empty(s, dtype=torch.uint8)  # noqa: E731
+    s = lambda *d: torch.empty(d, dtype=e8)  # noqa: E731
+    off = torch.zeros(4, dtype=torch.int64)
+    dy, none = torch.empty((4, 5)), (None, None)
+    raises = lambda f, *a, **kw: pytest.raises(ValueError, f, *a, **kw)  # noqa: E731
+    xt, wt, wte, xtg = (c(6, 64), s(6, 4)), (c(6, 64), s(6, 4)), (c(3, 6, 64), s(3, 6, 4)), (c(6, 192), s(6, 12))
+    raises(hif4.linear_mxfp4_backward, dy, *xt, *wt, need_dx=False, need_dw=False)
+    raises(hif4.linear_mxfp4_backward, dy, *none, c(6, 128), s(6, 8), need_dw=False)
+    raises(hif4.linear_mxfp4_backward, dy, c(6, 128), s(6, 8), *none, need_dx=False)
+    raises(hif4.linear_mxfp4_grouped_backward, dy, *xtg, *wte, off, need_dx=False, need_dw=False)
+    raises(hif4.linear_mxfp4_grouped_backward, dy, *none, c(2, 6, 64), s(2, 6, 4), off, need_dw=False)
+    raises(hif4.linear_mxfp4_grouped_backward, dy, *xt, *none, off, need_dx=False)
+    # what is not needed is not looked at: these get as far as the tensors' device
+    for call in (lambda: hif4.linear_mxfp4_backward(dy, *none, *wt, need_dw=False),
+                 lambda: hif4.linear_mxfp4_backward(dy, *xt, *none, need_dx=False),
+                 lambda: hif4.linear_mxfp4_grouped_backward(dy, *none, *wte, off, need_dw=False),
+                 lambda: hif4.linear_mxfp4_grouped_backward(dy, *xtg, *none, off, need_dx=False)):
+        with pytest.raises(ValueError, match="must be on the GPU"):
+            call()
