@@ -655,16 +655,25 @@ static Mx4Plan plan_mx4(int64_t m, int64_t n, int64_t k) {
 //   groups x mean x n x k     32 rows   64 x 64   128 x 128   256 x 256
 //   32 x 3 x 5120 x 2048        32         39         41
 //   128 x 4 x 2048 x 1024       30         40         36
-//   32 x 8 x 5120 x 2048        45         43         43
-//   8 x 16 x 5120 x 5120        38         34         38
-//   32 x 16 x 5120 x 2048       58         49         45
+//   32 x 8 x 5120 x 2048        45         43         44
+//   8 x 8 x 5120 x 5120                    32         38
+//   8 x 16 x 5120 x 5120        38         39         40
+//   16 x 16 x 2048 x 5120                  22         24
+//   32 x 16 x 1536 x 4096                  30         29
+//   8 x 16 x 13824 x 5120                  91         81
+//   32 x 16 x 5120 x 2048       58         47         45
+//   64 x 16 x 2048 x 2048                  40         36
+//   128 x 8 x 2048 x 1024                  48         39
+//   128 x 16 x 2048 x 1024                 52         42
 //   32 x 64 x 5120 x 2048      142         69         50          64
 //   128 x 256 x 2048 x 1024               197         97         101
 //   32 x 256 x 5120 x 2048                176         97          89
 //   8 x 512 x 5120 x 5120                 200        108          82
 //   32 x 1024 x 5120 x 2048               571        305         265
 // (units of 16 rows instead of 32, 32 x 3 x 5120 x 2048: 35.5: W is read again for the
-// second half of a group of more.)
+// second half of a group of more. Few rows a group are one tile each at either size, so the
+// small ones pay while the groups' column tiles are some two rounds of the 512 that the CUs
+// hold: 32 x 24 of them above are even, 8 x 216 lose from 12 rows a group on.)
 static Mx4Plan plan_of(const Mx4Product& p) {
   const int all = (int)tiles_in(p.k, 256);
   if (p.mode == kMx4Plain) return plan_mx4(p.m, p.n, p.k);
@@ -677,7 +686,8 @@ static Mx4Plan plan_of(const Mx4Product& p) {
     const auto tiles = [&](int64_t t) {
       return (p.groups.rows / t + (p.groups.count + 1) / 2) * tiles_in(p.n, t);
     };
-    if (mean <= 16 || tiles(128) < kMx4Cus / 2) return {kMx4Small, 1, all};
+    const bool few = mean <= 16 && p.groups.count * tiles_in(p.n, 64) <= 4 * kMx4Cus;
+    if (few || tiles(128) < kMx4Cus / 2) return {kMx4Small, 1, all};
     const bool large = mean >= 256 && mean * p.k >= (1 << 19) &&
                        4 * tiles_in(tiles(256), kMx4Cus) < 3 * tiles_in(tiles(128), 2 * kMx4Cus);
     return {large ? kMx4Large : kMx4Middle, 1, all};

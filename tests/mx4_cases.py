@@ -28,6 +28,7 @@ LINEAR = [
 ]
 
 _UNEVEN = [0, 1, 31, 160, 162, 162, 471, 640, 797]
+_MANY = [0] + torch.randint(0, 21, (127,), generator=torch.Generator().manual_seed(3)).cumsum(0).tolist() + [1400]
 # rows, offsets, n, k
 GROUPED = [
     ((T256,), 4100, [3, 4, 1300, 4098], 2100, 384),   # a group of one row, rows before and behind
@@ -35,6 +36,8 @@ GROUPED = [
     ((T256,), 4200, [0, 0, 4200], 2049, 1152),        # all rows in one of two
     ((T256,), 4400, [0, 300, 556, 1324, 4399], 2120, 2176),
     ((T128,), 800, _UNEVEN, 2050, 640), ((T128,), 799, _UNEVEN, 2049, 896), ((T128,), 3000, [5, 1000, 1129, 3000], 1031, 1152),
+    # few rows a group: many groups with many columns, few with few
+    ((T128,), 1400, _MANY, 520, 384), ((T128,), 1400, _MANY, 513, 1152), ((T64,), 1400, _MANY, 512, 384),
     ((T64,), 100, [0, 64, 64, 65, 67, 90, 90, 99, 100], 130, 1152), ((T64,), 800, _UNEVEN, 257, 2176),
     # few rows a group, some with more than a unit of 32
     ((SKINNY32,), 41, [0, 1, 34, 34, 36, 36, 40, 41], 41, 1152), ((SKINNY32,), 42, [0, 1, 34, 34, 36, 36, 40, 41], 300, 2688),
