@@ -462,7 +462,29 @@ def ceilings(torch, dev, stream):
                         "what": "v_mfma_f32_32x32x16_bf16 back to back from registers, 12,150 "
                                 "workgroups x 4 waves x 5184 MFMAs (the FFN-up launch's count)"}
     log(f"MFMA-only bf16: {tf:.0f} TFLOP/s")
-    del sink
+    # the same on MXFP4 codes, 80 x 16 products of K = 64 a wave: the count of the 4-bit product
+    # at the FFN-up shape; with the clock that its workgroups ran at
+    lib.hif4_probe_mfma_mxfp4.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p]
+    lib.hif4_probe_mfma_mxfp4.restype = ctypes.c_int
+    clocks = torch.empty((blocks, 2), dtype=torch.int64, device=dev)
+    for name, zeros in (("random", 0), ("zeros", 1)):
+        def probe4():
+            st = lib.hif4_probe_mfma_mxfp4(blocks, 80, zeros, ctypes.c_void_p(sink.data_ptr()),
+                                           ctypes.c_void_p(clocks.data_ptr()),
+                                           ctypes.c_void_p(stream.cuda_stream))
+            if st != 0:
+                raise RuntimeError(f"hif4_probe_mfma_mxfp4: status {st}")
+        ms_m, _ = rate(probe4, 0.0, reps=20)
+        tf = blocks * 4 * 80 * 16 * 2.0 * 32 * 32 * 64 / (ms_m * 1e-3) / 1e12
+        cycles, ticks = clocks.double().sum(0).tolist()
+        out[f"mfma_mxfp4_{name}"] = {
+            "ms": ms_m, "TFLOP/s": tf, "clock_GHz": cycles / ticks * 0.1,
+            "clocks_per_product": cycles / (blocks * 80 * 16),
+            "what": "v_mfma_scale_f32_32x32x64_f8f6f4 on E2M1 codes back to back from registers, "
+                    "12,150 workgroups x 4 waves x 1280 (the 4-bit FFN-up launch's count)"}
+        log(f"MFMA-only MXFP4, {name}: {tf:.0f} TFLOP/s at {cycles / ticks * 0.1:.2f} GHz")
+    del sink, clocks
     # reference point: the vendor bf16 GEMM (torch.mm, hipBLASLt) at the FFN-up shape on plain
     # bf16 operands (no HiF4 decode, no protected-channel residual)
     m, n, k = 57600, 13824, 5120

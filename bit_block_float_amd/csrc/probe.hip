@@ -3,8 +3,9 @@
 // libhif4_probe.so, declared in include/hif4_probe.h).
 //
 // Probes: HBM streaming rates (copy, read only, and the quantizer's 4 : 1
-// read : write mix) and the bf16 matrix-core ceiling under a full-chip load.
-// For the latter every wave issues back-to-back v_mfma_f32_32x32x16_bf16 on
+// read : write mix) and the bf16 and MXFP4 matrix-core ceilings under a full-chip
+// load. For these every wave issues back-to-back v_mfma_f32_32x32x16_bf16
+// (v_mfma_scale_f32_32x32x64_f8f6f4 on E2M1 codes) on
 // 16 independent accumulator blocks (the W4A4 kernel's 128 x 128 wave tile,
 // one wave per SIMD, four waves per workgroup), with register operands only
 // -- no memory traffic, no LDS, no other VALU work in the loop. Its rate is
@@ -45,6 +46,48 @@ void mfma_bf16_peak_kernel(int iters, float* __restrict__ out) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) s += acc[j][r];
   out[(size_t)blockIdx.x * blockDim.x + threadIdx.x] = s;
+}
+
+// The same on E2M1 codes, unit scales: 8 operand fragments of pseudo-random codes
+// (or of zeros, which draw little power), and the workgroup's time in core clocks
+// and in ticks of the 100 MHz counter, so that a rate has its clock.
+typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void mfma_mxfp4_peak_kernel(int iters, int zeros, float* __restrict__ out, uint64_t* __restrict__ clocks) {
+  i32x8_t a[4], b[4];
+  uint32_t state = blockIdx.x * 256u + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      state = state * 1664525u + 1013904223u;
+      const uint32_t mixed = state ^ (state >> 15);
+      a[i][j] = j < 4 && !zeros ? (int)mixed : 0;
+      b[i][j] = j < 4 && !zeros ? (int)(mixed * 2654435761u) : 0;
+    }
+  f32x16_t acc[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
+  const uint64_t c0 = clock64(), w0 = wall_clock64();
+  for (int it = 0; it < iters; ++it) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      acc[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[j >> 2], b[j & 3], acc[j], 4, 4, 0, 127, 0, 127);
+  }
+  const uint64_t c1 = clock64(), w1 = wall_clock64();
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s += acc[j][r];
+  out[(size_t)blockIdx.x * blockDim.x + threadIdx.x] = s;
+  if (threadIdx.x == 0) {
+    clocks[(size_t)blockIdx.x * 2] = c1 - c0;
+    clocks[(size_t)blockIdx.x * 2 + 1] = w1 - w0;
+  }
 }
 
 // HBM copy ceiling: a grid-stride copy of 16-byte words with four loads in
@@ -135,5 +178,13 @@ extern "C" int hif4_probe_mfma_bf16(int blocks, int iters, float* out, hipStream
   if (blocks <= 0 || iters <= 0 || out == nullptr) return 1;
   hipLaunchKernelGGL(mfma_bf16_peak_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, iters,
                      out);
+  return hipGetLastError() == hipSuccess ? 0 : 7;
+}
+
+extern "C" int hif4_probe_mfma_mxfp4(int blocks, int iters, int zeros, float* out, uint64_t* clocks,
+                                     hipStream_t stream) {
+  if (blocks <= 0 || iters <= 0 || out == nullptr || clocks == nullptr) return 1;
+  hipLaunchKernelGGL(mfma_mxfp4_peak_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, iters, zeros,
+                     out, clocks);
   return hipGetLastError() == hipSuccess ? 0 : 7;
 }

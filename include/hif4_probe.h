@@ -7,6 +7,7 @@
 #define HIF4_PROBE_H
 
 #include <stddef.h>
+#include <stdint.h>
 
 #include <hip/hip_runtime_api.h>
 
@@ -24,6 +25,16 @@ extern "C" {
  */
 __attribute__((visibility("default"))) int hif4_probe_mfma_bf16(int blocks, int iters, float *out,
                                                                  hipStream_t stream);
+
+/*
+ * hif4_probe_mfma_mxfp4 -- the same for v_mfma_scale_f32_32x32x64_f8f6f4 on E2M1
+ * codes (131,072 flops each): pseudo-random codes, or zeros (`zeros` not 0). clocks:
+ * uint64 [blocks][2] device buffer, each workgroup's time in core clocks and in ticks
+ * of the 100 MHz counter.
+ */
+__attribute__((visibility("default"))) int hif4_probe_mfma_mxfp4(int blocks, int iters, int zeros,
+                                                                  float *out, uint64_t *clocks,
+                                                                  hipStream_t stream);
 
 /*
  * hif4_probe_copy -- the achievable HBM streaming rate: copies `bytes`
