@@ -297,15 +297,15 @@ __global__ __launch_bounds__(kWM* kWN * 64) void mx4_tile_kernel(Mx4Args a, Mx4A
 // the codes and cost 5%, these half of that.
 //
 // Bound: the matrix cores at the clock that power allows, and a tile's ends. Measured on
-// 57600 x 13824 x 5120, bf16 Y: 1.93 to 2.0 ms (4.1 PFLOP/s); the products alone, from
-// registers, 1.40 ms (5.8, at 1.55 GHz). When it took 2.02 ms, it took 1.80 without stores,
-// 1.76 without loads, 1.88 without LDS reads. Loads spread over a whole stage, fragments of
-// half a run, rows of 64 bytes in four slots with twice the time to land, one barrier more a
-// stage for earlier loads, fragment reads spread over their run or in the order of need, and
-// a start of XCDs or CUs at different times (so that not all store at once) gave nothing or
-// less. Loads closer together than every other product cost 2 to 7%: the path from L2 is
-// the next bound (operands of zeros, which draw little power, take 1.62 ms). By depth, a
-// stage takes 1.82 us (4.7 PFLOP/s) and a tile's ends 6 (bf16 Y).
+// 57600 x 13824 x 5120, bf16 Y: 1.90 to 1.99 ms (4.2 PFLOP/s); the products alone, from
+// registers in as many workgroups, 1.27 ms (6.4, at 1.8 GHz). When it took 2.02 ms, it took
+// 1.80 without stores, 1.76 without loads, 1.88 without LDS reads. Loads spread over a
+// whole stage, fragments of half a run, rows of 64 bytes in four slots with twice the time
+// to land, one barrier more a stage for earlier loads, fragment reads spread over their run
+// or in the order of need, and a start of XCDs or CUs at different times (so that not all
+// store at once) gave nothing or less. Loads closer together than every other product cost
+// 2 to 7%: the path from L2 is the next bound (operands of zeros, which draw little power,
+// take 1.54 ms). By depth, a stage takes 1.7 us (5.0 PFLOP/s) and a tile's ends 6 (bf16 Y).
 constexpr int kMx4BigSlot = 2 * 256 * 128;
 constexpr int kMx4BigRing = 2 * 256 * 32;
 constexpr int kMx4BigLds = 2 * kMx4BigSlot + 2 * kMx4BigRing;
