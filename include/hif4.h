@@ -603,7 +603,8 @@ HIF4_EXPORT size_t hif4_linear_mxfp4_workspace_bytes(int64_t m, int64_t n, int64
 /*
  * hif4_linear_mxfp4 -- Y = X W^T, X [m][k], W [n][k] as codes and scales; the products
  * are exact, accumulated in fp32 in a fixed order, and rounded once to y_dtype. Every
- * scale byte counts as it is (255: NaN); a sum beyond fp32's range is infinite.
+ * scale byte counts as it is (255: NaN); a sum, or a part of it, beyond fp32's range is
+ * infinite (parts of either sign together: NaN).
  *  m, n   >= 0, below 2^31, ceil(m/128) ceil(n/128) < 2^24.
  *  k      >= 0, k % 128 == 0, at most 2^22; k = 0 gives Y = 0.
  *  y      [m][n] contiguous of y_dtype, 16-byte aligned.

@@ -148,6 +148,22 @@ def test_linear_does_not_change_from_run_to_run(hip, case):
         assert torch.equal(hip.linear_mxfp4(*x, *w), first)
 
 
+@_cases([c for c in mx4_cases.LINEAR if c[3] <= 1152])
+def test_linear_sums_beyond_the_range_are_not_finite(hip, case):
+    """Products of 2^122 to 2^127.2 whose sums pass 2^128: infinite, or NaN where parts of either sign meet; a
+    row and a column of zeros stay zero beside them."""
+    _, m, n, k = case
+    x, w = _random(m, k, 1, 189, 189), _random(n, k, 2, 187, 187)
+    x[0][0], w[0][n - 1] = 0, 0
+    want = mx4_ref.values(*x) @ mx4_ref.values(*w).T
+    past = want.abs() >= 2.0 ** 128
+    assert bool(past.any()) or m == 1
+    for dtype in DTYPES:
+        y = hip.linear_mxfp4(*_cuda(x), *_cuda(w), y_dtype=dtype).float().cpu()
+        assert not bool(torch.isfinite(y[past]).any())
+        assert not y[0].any() and not y[:, n - 1].any()
+
+
 # ---------------------------------------------------------------- a weight for each group of rows
 
 
